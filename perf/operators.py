@@ -10,7 +10,7 @@ Four operators, as a serving program calls them in `paged_kv_cache_64_gb300.api`
 
 A row (one token of one KV head: d values x of a 16-bit type) is held as m = min x, s = the smallest
 value of the type that is >= (max x - min x) / 15, and codes n = nearest integer to (x - m) / s, ties
-to even; it stands for m + s n.  A (block, KV head) record is B * d / 2 bytes of codes (two a byte, the
+to even (the differences rounded to fp32, the quotients not); it stands for m + s n.  A (block, KV head) record is B * d / 2 bytes of codes (two a byte, the
 even element low) followed by B pairs (s, m); a pool is uint8 [blocks][KV heads][B * (d / 2 + 4)].
 
 `own` selects the library's kernels; otherwise `run` computes the same in elementary torch operations.
@@ -98,14 +98,14 @@ def draw(rng):
 
 # ------------------------------------------------------------------ inputs
 def _quantise(x):
-    """Codes (int16), s and m (the type of x) of rows x [..., d] of a 16-bit type: differences and
-    quotients in 64 bits, so that values next to a border fall on the right side."""
+    """Codes (int16), s and m (the type of x) of rows x [..., d] of a 16-bit type: differences in 32
+    bits, quotients in 64, so that values next to a border fall on the right side."""
     lo, hi = x.amin(-1, keepdim=True), x.amax(-1, keepdim=True)
-    span = hi.double() - lo.double()
+    span = (hi.float() - lo.float()).double()
     step = span / torch.full_like(span, 15)  # a tensor: by a number it would be a product with 1/15
     s = step.to(x.dtype)
     s = torch.where(s.double() < step, (s.view(torch.int16) + 1).view(x.dtype), s)
-    t = (x.double() - lo.double()) / s.double()
+    t = (x.float() - lo.float()).double() / s.double()
     n = torch.where(s == 0, 0.0, t).round().clamp(0, 15)
     return n.to(torch.int16), s, lo
 

@@ -299,6 +299,52 @@ size_t pa_decode_fp8_workspace_size(int num_seqs, int num_q_heads, int num_kv_he
                                     int head_dim, int block_size, int max_seq_len,
                                     int partition_tokens, pa_dtype dtype);
 
+/* ------------------------------------------------------------------------
+ * 4-bit KV cache (a variant).  A row (one token's K or V of one KV head,
+ * head_dim values x of the 16-bit type dtype) is held with a scale and a
+ * minimum of its own:
+ *   m = min x;  s = the smallest dtype value >= (max x - m) / 15;
+ *   code n_i = the integer nearest to (x_i - m) / s, ties to even (0 .. 15);
+ *   it stands for m + s * n_i, so |x_i - (m + s n_i)| <= s / 2.
+ * Differences are rounded to fp32, quotients are compared exactly.  A row of
+ * equal values has s = 0 and codes 0.  A row that holds a NaN or an infinity,
+ * or whose max x - min x passes fp32's range, is stored as s = m = NaN and
+ * reads as NaN; -0 as a minimum is stored as +0.
+ * Pool layout: uint8 [num_blocks][num_kv_heads][pa_int4_record_bytes], where
+ * the record of a (block, KV head) is block_size * head_dim / 2 bytes of
+ * codes, [block_size][head_dim / 2] with element 2i in the low and 2i + 1 in
+ * the high four bits of byte i, then block_size pairs (s, m) of dtype:
+ * block_size * (head_dim / 2 + 4) bytes.  A block is a multiple of 16 bytes,
+ * so pa_copy_blocks copies such pools (block_bytes = num_kv_heads * record).
+ * head_dim in {64, 128}; block_size in {16, 32}; pools 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+/* Bytes of a (block, KV head) record; 0 for an unsupported shape. */
+size_t pa_int4_record_bytes(int head_dim, int block_size);
+
+/* pa_cache_write_int4: pa_cache_write into 4-bit pools.  A negative slot
+ * skips its token, a slot >= num_blocks*block_size is a bad index (its token
+ * skipped).  The slots written by one call must be distinct.
+ *   k_out, v_out: both NULL, or [num_tokens][num_kv_heads][head_dim] of dtype
+ *   (16-byte aligned): the values that the stored rows stand for, as
+ *   pa_cache_read_int4 gives them (skipped tokens' rows are left as they
+ *   were); they may be k_new and v_new themselves.
+ * num_tokens * num_kv_heads below 2^31. */
+pa_status pa_cache_write_int4(const void *k_new, const void *v_new, const int64_t *slot_mapping,
+                              int num_tokens, void *k_pool, void *v_pool, int num_blocks,
+                              int num_kv_heads, int head_dim, int block_size, void *k_out,
+                              void *v_out, pa_dtype dtype, void *stream);
+
+/* pa_cache_read_int4: for every t and KV head h, k_out[t][h] = the row at slot
+ * slot_mapping[t] of k_pool (same for V): m + s * n in fp32, rounded to dtype
+ * to nearest even, saturating at dtype's largest finite value (a NaN row gives
+ * NaN).  A negative slot leaves its rows of k_out and v_out as they were; a
+ * slot past the pool is a bad index (its rows left too).  The same slot may be
+ * named more than once.  Arguments as pa_cache_write_int4. */
+pa_status pa_cache_read_int4(void *k_out, void *v_out, const int64_t *slot_mapping, int num_tokens,
+                             const void *k_pool, const void *v_pool, int num_blocks,
+                             int num_kv_heads, int head_dim, int block_size, pa_dtype dtype,
+                             void *stream);
+
 /* Partition size pa_decode uses for these shapes when partition_tokens = 0
  * (-1 means it will run single pass).  Needs the current CUDA device. */
 int pa_decode_auto_partition(int num_seqs, int num_kv_heads, int max_seq_len, int head_dim,

@@ -68,6 +68,11 @@ SIGNATURES = {
                                _c_int, _vp, _c_sz, _c_int, _vp]),
     "pa_decode_fp8_workspace_size": (_c_sz, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
                                              _c_int, _c_int]),
+    "pa_int4_record_bytes": (_c_sz, [_c_int, _c_int]),
+    "pa_cache_write_int4": (_c_int, [_vp, _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int,
+                                     _c_int, _vp, _vp, _c_int, _vp]),
+    "pa_cache_read_int4": (_c_int, [_vp, _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int,
+                                    _c_int, _c_int, _vp]),
     "pa_decode_auto_partition": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
                                           _c_int]),
     "pa_decode_fp8_auto_partition": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int,

@@ -299,6 +299,91 @@ def decode_fp8(out, q, k_pool, v_pool, block_tables, seq_lens, max_seq_len, scal
     return workspace
 
 
+def _one_device(first, **others):
+    """Index of the device of `first`; every other tensor given must lie there."""
+    dev = first.get_device()
+    for name, t in others.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} must be on the device of the other tensors (cuda:{dev})")
+    return dev
+
+
+def _on_device(dev, stream, fn, *args):
+    """fn(*args, stream) with `dev` current; stream None: its current stream."""
+    if dev == torch.cuda.current_device():
+        return fn(*args, _stream_handle(stream))
+    with torch.cuda.device(dev):
+        return fn(*args, _stream_handle(stream))
+
+
+def int4_pool_shape(num_blocks, num_kv_heads, block_size, head_dim):
+    """Shape of a 4-bit pool (a uint8 tensor): one record a (block, KV head),
+    block_size * (head_dim / 2 + 4) bytes (layout in pa.h)."""
+    rec = _lib.load().pa_int4_record_bytes(int(head_dim), int(block_size))
+    if not rec:
+        raise ValueError("4-bit pools hold head_dim 64 or 128 in blocks of 16 or 32")
+    return (int(num_blocks), int(num_kv_heads), rec)
+
+
+def _int4_pools(k_pool, v_pool, hkv, d):
+    """(blocks, block size) of a pair of 4-bit pools."""
+    if k_pool.dtype != torch.uint8 or v_pool.dtype != torch.uint8:
+        raise TypeError("4-bit pools are uint8 tensors of records")
+    if k_pool.dim() != 3 or v_pool.shape != k_pool.shape or k_pool.shape[1] != hkv:
+        raise ValueError(f"4-bit pools must both be [blocks, {hkv}, record bytes] (int4_pool_shape)")
+    row = d // 2 + 4
+    if k_pool.shape[2] not in (16 * row, 32 * row):
+        raise ValueError(f"a record of {k_pool.shape[2]} bytes is no block of 16 or 32 rows of "
+                         f"head_dim {d}")
+    return k_pool.shape[0], k_pool.shape[2] // row
+
+
+def cache_write_int4(k_new, v_new, slot_mapping, k_pool, v_pool, k_out=None, v_out=None,
+                     stream=None):
+    """reshape_and_cache into 4-bit pools (uint8, int4_pool_shape): each row
+    of k_new / v_new (16-bit [T, Hkv, d]) quantised with its own scale and
+    minimum at its slot (int64 [T]; < 0 skips; distinct).  k_out / v_out (like
+    k_new; may be k_new / v_new) receive the values the stored rows stand for."""
+    if k_new.dim() != 3 or v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
+        raise ValueError("k_new and v_new must both be [T, Hkv, d] of one type")
+    T, hkv, d = k_new.shape
+    nb, bs = _int4_pools(k_pool, v_pool, hkv, d)
+    if slot_mapping.shape != (T,):
+        raise ValueError("slot_mapping must be [T]")
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out go together")
+    for t in (k_out, v_out):
+        if t is not None and (t.shape != k_new.shape or t.dtype != k_new.dtype):
+            raise ValueError("k_out and v_out must be like k_new")
+    null = ctypes.c_void_p(0)
+    rc = _on_device(
+        _one_device(k_new, v_new=v_new, slot_mapping=slot_mapping, k_pool=k_pool, v_pool=v_pool,
+                    k_out=k_out, v_out=v_out),
+        stream, _lib.load().pa_cache_write_int4, _cuda(k_new, "k_new"), _cuda(v_new, "v_new"),
+        _cuda(slot_mapping, "slot_mapping", torch.int64), T, _cuda(k_pool, "k_pool"),
+        _cuda(v_pool, "v_pool"), nb, hkv, d, bs,
+        null if k_out is None else _cuda(k_out, "k_out"),
+        null if v_out is None else _cuda(v_out, "v_out"), _dt(k_new))
+    _lib.check("pa_cache_write_int4", rc)
+
+
+def cache_read_int4(k_out, v_out, slot_mapping, k_pool, v_pool, stream=None):
+    """Rows of 4-bit pools back as 16-bit values: k_out / v_out [T, Hkv, d]
+    at slot_mapping (int64 [T]; rows of a negative slot are left alone)."""
+    if k_out.dim() != 3 or v_out.shape != k_out.shape or v_out.dtype != k_out.dtype:
+        raise ValueError("k_out and v_out must both be [T, Hkv, d] of one type")
+    T, hkv, d = k_out.shape
+    nb, bs = _int4_pools(k_pool, v_pool, hkv, d)
+    if slot_mapping.shape != (T,):
+        raise ValueError("slot_mapping must be [T]")
+    rc = _on_device(
+        _one_device(k_out, v_out=v_out, slot_mapping=slot_mapping, k_pool=k_pool, v_pool=v_pool),
+        stream, _lib.load().pa_cache_read_int4, _cuda(k_out, "k_out"), _cuda(v_out, "v_out"),
+        _cuda(slot_mapping, "slot_mapping", torch.int64), T, _cuda(k_pool, "k_pool"),
+        _cuda(v_pool, "v_pool"), nb, hkv, d, bs, _dt(k_out))
+    _lib.check("pa_cache_read_int4", rc)
+
+
 def cascade_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                            max_seq_len, prefix_len, dtype):
     return _lib.load().pa_decode_cascade_workspace_size(num_seqs, num_q_heads, num_kv_heads,

@@ -345,6 +345,66 @@ pa_status pa_cache_read_int4(void *k_out, void *v_out, const int64_t *slot_mappi
                              int num_kv_heads, int head_dim, int block_size, pa_dtype dtype,
                              void *stream);
 
+/* pa_decode_int4: pa_decode over 4-bit pools: out[i][h] =
+ * sum_p softmax(s)_p * (m + s n)(V_i[p]) with s_p = scale * dot(q[i][h],
+ * (m + s n)(K_i[p])), the stored values unrounded.  q finite.  Arguments,
+ * partition_tokens and workspace as pa_decode (pools as above, workspace size
+ * from pa_decode_int4_workspace_size); the group size is at most 8. */
+pa_status pa_decode_int4(void *out, const void *q, const void *k_pool, const void *v_pool,
+                         int num_blocks, const int32_t *block_tables, int max_blocks_per_seq,
+                         const int32_t *seq_lens, int max_seq_len, int num_seqs, int num_q_heads,
+                         int num_kv_heads, int head_dim, int block_size, float scale,
+                         int partition_tokens, void *workspace, size_t workspace_bytes,
+                         pa_dtype dtype, void *stream);
+
+size_t pa_decode_int4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int block_size, int max_seq_len, int partition_tokens,
+                                     pa_dtype dtype);
+
+/* ------------------------------------------------------------------------
+ * pa_qk_norm_rope: what lies between a layer's projections and its decode, in
+ * one pass: the RMS norm of every query and key head, the rotary positions,
+ * and the cache write.
+ *   y = x * w / sqrt(mean(x^2) + eps)          over the head_dim values of a head
+ *   for i < rotary_dim / 2, with (a, b) = (y[i], y[i + rotary_dim / 2]), or
+ *   (y[2i], y[2i + 1]) when interleaved, and c, s the position's table row:
+ *       (a, b) becomes (a c_i - b s_i, b c_i + a s_i)
+ * in fp32 throughout, rounded to dtype once.  The turned queries go to q_out;
+ * each token's turned key heads and its value heads (as they are) go to its
+ * slot, exactly as pa_cache_write / pa_cache_write_fp8 / pa_cache_write_int4
+ * would write them.
+ * Device pointers, 16-byte aligned:
+ *   q [num_tokens][num_q_heads][head_dim], k, v [num_tokens][num_kv_heads]
+ *     [head_dim]: heads dense, *_stride elements from a token to the next
+ *     (multiples of 8, at least the token's own elements), so that they may be
+ *     column ranges of one projection's output;
+ *   q_out like q; it may be q itself with the same stride, and overlaps no
+ *     other argument;
+ *   q_weight, k_weight [head_dim] of dtype;
+ *   cos_sin float [num_positions][rotary_dim]: cosines of the rotary_dim / 2
+ *     angles, then their sines; rotary_dim a multiple of 16, 16 .. head_dim;
+ *   positions int64 [num_tokens], each in [0, num_positions): another value is
+ *     a bad index and its token is skipped (q_out and cache left as they were);
+ *   slot_mapping int64 [num_tokens] as in pa_cache_write (a negative slot: the
+ *     queries only), distinct.
+ *   kv_format: the pools hold dtype (PA_KV_16BIT), E4M3 codes with k_scale and
+ *     v_scale (PA_KV_E4M3; the scales are ignored otherwise) or 4-bit records
+ *     (PA_KV_INT4).
+ * head_dim in {64, 128}; block_size in {16, 32}; any num_q_heads that is a
+ * multiple of num_kv_heads; eps >= 0 and finite.
+ * ---------------------------------------------------------------------- */
+typedef enum { PA_KV_16BIT = 0, PA_KV_E4M3 = 1, PA_KV_INT4 = 2 } pa_kv_format;
+
+pa_status pa_qk_norm_rope(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride,
+                          const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                          const void *q_weight, const void *k_weight, float eps,
+                          const float *cos_sin, int num_positions, int rotary_dim,
+                          int interleaved, const int64_t *positions, const int64_t *slot_mapping,
+                          int num_tokens, void *k_pool, void *v_pool, int num_blocks,
+                          int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                          pa_kv_format kv_format, float k_scale, float v_scale, pa_dtype dtype,
+                          void *stream);
+
 /* Partition size pa_decode uses for these shapes when partition_tokens = 0
  * (-1 means it will run single pass).  Needs the current CUDA device. */
 int pa_decode_auto_partition(int num_seqs, int num_kv_heads, int max_seq_len, int head_dim,

@@ -23,6 +23,7 @@ STATUS = {
 # Size of the fixed device scratch behind pa_decode_static_scratch (pa.h).
 STATIC_SCRATCH_BYTES = 16 << 20
 PA_F16, PA_BF16 = 0, 1
+PA_KV_16BIT, PA_KV_E4M3, PA_KV_INT4 = 0, 1, 2
 
 # Every symbol pa.h declares, with (restype, argtypes).
 _c_int, _c_i64, _c_sz, _c_f = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
@@ -73,6 +74,14 @@ SIGNATURES = {
                                      _c_int, _vp, _vp, _c_int, _vp]),
     "pa_cache_read_int4": (_c_int, [_vp, _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int,
                                     _c_int, _c_int, _vp]),
+    "pa_decode_int4": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _vp, _c_int, _vp, _c_int, _c_int, _c_int,
+                                _c_int, _c_int, _c_int, _c_f, _c_int, _vp, _c_sz, _c_int, _vp]),
+    "pa_decode_int4_workspace_size": (_c_sz, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                              _c_int, _c_int]),
+    "pa_qk_norm_rope": (_c_int, [_vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _vp,
+                                 _c_f, _vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _vp, _vp,
+                                 _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_f, _c_f,
+                                 _c_int, _vp]),
     "pa_decode_auto_partition": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
                                           _c_int]),
     "pa_decode_fp8_auto_partition": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int,

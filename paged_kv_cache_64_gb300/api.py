@@ -309,11 +309,12 @@ def _one_device(first, **others):
 
 
 def _on_device(dev, stream, fn, *args):
-    """fn(*args, stream) with `dev` current; stream None: its current stream."""
+    """fn(*args, stream) with `dev` current (stream None: its current stream;
+    False: fn takes none)."""
     if dev == torch.cuda.current_device():
-        return fn(*args, _stream_handle(stream))
+        return fn(*args) if stream is False else fn(*args, _stream_handle(stream))
     with torch.cuda.device(dev):
-        return fn(*args, _stream_handle(stream))
+        return fn(*args) if stream is False else fn(*args, _stream_handle(stream))
 
 
 def int4_pool_shape(num_blocks, num_kv_heads, block_size, head_dim):
@@ -382,6 +383,118 @@ def cache_read_int4(k_out, v_out, slot_mapping, k_pool, v_pool, stream=None):
         _cuda(slot_mapping, "slot_mapping", torch.int64), T, _cuda(k_pool, "k_pool"),
         _cuda(v_pool, "v_pool"), nb, hkv, d, bs, _dt(k_out))
     _lib.check("pa_cache_read_int4", rc)
+
+
+def int4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len,
+                        partition_tokens, dtype):
+    return _lib.load().pa_decode_int4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                     block_size, max_seq_len, partition_tokens,
+                                                     _DTYPES[dtype])
+
+
+def decode_int4(out, q, k_pool, v_pool, block_tables, seq_lens, max_seq_len, scale,
+                partition_tokens=0, workspace=None, stream=None):
+    """Paged decode attention over 4-bit pools (uint8, int4_pool_shape) into
+    out [S, Hq, d]; q / out 16-bit.  partition_tokens and workspace as for
+    decode (a workspace allocated here is of int4_workspace_size bytes and
+    tied to the stream)."""
+    if q.dim() != 3 or out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("q and out must both be [S, Hq, d] of one type")
+    S, hq, d = q.shape
+    if k_pool.dim() != 3:
+        raise ValueError("4-bit pools are [blocks, Hkv, record bytes] (int4_pool_shape)")
+    hkv = k_pool.shape[1]
+    nb, bs = _int4_pools(k_pool, v_pool, hkv, d)
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or seq_lens.shape != (S,):
+        raise ValueError("block_tables must be [S, max_blocks], seq_lens [S]")
+    dt = _dt(q)
+    dev = _one_device(q, out=out, k_pool=k_pool, v_pool=v_pool, block_tables=block_tables,
+                      seq_lens=seq_lens, workspace=workspace)
+    lib = _lib.load()
+    args = (_cuda(out, "out"), _cuda(q, "q"), _cuda(k_pool, "k_pool"), _cuda(v_pool, "v_pool"), nb,
+            _cuda(block_tables, "block_tables", torch.int32), block_tables.shape[1],
+            _cuda(seq_lens, "seq_lens", torch.int32), int(max_seq_len), S, hq, hkv, d, bs,
+            float(scale), int(partition_tokens))
+    need = _on_device(dev, False, lib.pa_decode_int4_workspace_size, S, hq, hkv, d, bs,
+                      int(max_seq_len), int(partition_tokens), dt)
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = alloc_workspace(need, q.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    ws = _cuda(workspace, "workspace") if workspace is not None else ctypes.c_void_p(0)
+    wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _lib.check("pa_decode_int4", _on_device(dev, stream, lib.pa_decode_int4, *args, ws, wbytes, dt))
+    return workspace
+
+
+def _token_rows(t, name, T, d):
+    """(address, elements from a token to the next) of t [T, heads, d] whose
+    heads are dense."""
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != d:
+        raise ValueError(f"{name} must be [{T}, heads, {d}], got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    own = t.shape[1] * d
+    step = t.stride(0) if T > 1 else own
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d) or step < own:
+        raise ValueError(f"{name}: each token's heads must be dense and apart from the next's")
+    return ctypes.c_void_p(t.data_ptr()), step
+
+
+def qk_norm_rope(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, positions, slot_mapping, k_pool,
+                 v_pool, interleaved=False, k_scale=None, v_scale=None, stream=None):
+    """RMS norm of every q and k head, rotary positions and the cache write in
+    one pass (pa_qk_norm_rope).  q, q_out [T, Hq, d]; k, v [T, Hkv, d] (tokens
+    may be strided: column ranges of one projection; q_out may be q);
+    weights [d]; cos_sin float32 [positions, rotary_dim] (cosines, sines);
+    positions, slot_mapping int64 [T].  The pools' form is theirs: like q
+    [NB, Hkv, B, d], E4M3 codes (uint8, the same shape, with k_scale and
+    v_scale) or 4-bit records (uint8, int4_pool_shape)."""
+    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or q_out.shape != q.shape:
+        raise ValueError("q and q_out must be [T, Hq, d], k and v [T, Hkv, d]")
+    T, hq, d = q.shape
+    hkv = k.shape[1]
+    dt = q.dtype
+    if not (dt == k.dtype == v.dtype == q_out.dtype == q_weight.dtype == k_weight.dtype):
+        raise TypeError("q, q_out, k, v and the weights must have one type")
+    if q_weight.shape != (d,) or k_weight.shape != (d,):
+        raise ValueError("the weights must be [head_dim]")
+    if positions.shape != (T,) or slot_mapping.shape != (T,):
+        raise ValueError("positions and slot_mapping must be [T]")
+    ks = vs = 1.0
+    if k_pool.dtype == torch.uint8 and k_pool.dim() == 3:
+        fmt = _lib.PA_KV_INT4
+        nb, bs = _int4_pools(k_pool, v_pool, hkv, d)
+    else:
+        if k_pool.dim() != 4 or v_pool.shape != k_pool.shape or k_pool.shape[1] != hkv \
+                or k_pool.shape[3] != d:
+            raise ValueError(f"pools must both be [blocks, {hkv}, block size, {d}] or 4-bit records")
+        nb, _, bs, _ = k_pool.shape
+        if k_pool.dtype == torch.uint8 and v_pool.dtype == torch.uint8:
+            fmt = _lib.PA_KV_E4M3
+            if k_scale is None or v_scale is None:
+                raise ValueError("E4M3 pools need k_scale and v_scale")
+            ks, vs = float(k_scale), float(v_scale)
+        elif k_pool.dtype == dt and v_pool.dtype == dt:
+            fmt = _lib.PA_KV_16BIT
+        else:
+            raise TypeError("pools must have q's type or be uint8 codes")
+    qo, qo_step = _token_rows(q_out, "q_out", T, d)
+    qp, q_step = _token_rows(q, "q", T, d)
+    kp, k_step = _token_rows(k, "k", T, d)
+    vp, v_step = _token_rows(v, "v", T, d)
+    cs = _cuda(cos_sin, "cos_sin", torch.float32, ndim=2)
+    rc = _on_device(
+        _one_device(q, q_out=q_out, k=k, v=v, q_weight=q_weight, k_weight=k_weight,
+                    cos_sin=cos_sin, positions=positions, slot_mapping=slot_mapping,
+                    k_pool=k_pool, v_pool=v_pool),
+        stream, _lib.load().pa_qk_norm_rope, qo, qo_step, qp, q_step, kp, k_step, vp, v_step,
+        _cuda(q_weight, "q_weight"), _cuda(k_weight, "k_weight"), float(eps), cs,
+        cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)),
+        _cuda(positions, "positions", torch.int64),
+        _cuda(slot_mapping, "slot_mapping", torch.int64), T, _cuda(k_pool, "k_pool"),
+        _cuda(v_pool, "v_pool"), nb, hq, hkv, d, bs, fmt, ks, vs, _dt(q))
+    _lib.check("pa_qk_norm_rope", rc)
 
 
 def cascade_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,

@@ -804,6 +804,7 @@ struct ResolvedDecode {
     int part_tokens;  // the partition size asked for (or chosen when automatic)
     bool fp8 = false;  // E4M3 pools: the E4M3 variants of the tensor-core kernel
     int span = 1;      // partitions per CTA (tensor-core kernel); grid.x = ceil(NP / span)
+    bool int4 = false;  // 4-bit pools: the kernel of pa_decode_int4.cu
 };
 
 // Scales of E4M3 pools (element = scale * code value).
@@ -828,7 +829,8 @@ static bool use_tensor_cores(int head_dim, int group) {
 
 static pa_status resolve(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                          int block_size, int max_seq_len, int partition_tokens, pa_dtype dtype,
-                         ResolvedDecode *r, bool fp8 = false, bool merge_span = true) {
+                         ResolvedDecode *r, bool fp8 = false, bool merge_span = true,
+                         bool int4 = false) {
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_seq_len < 0)
         return PA_ERR_INVALID;
     if (num_seqs > 65535 || num_kv_heads > 65535) return PA_ERR_INVALID;  // grid y and z
@@ -839,14 +841,16 @@ static pa_status resolve(int num_seqs, int num_q_heads, int num_kv_heads, int he
     if (G > 8 || (head_dim != 64 && head_dim != 128) || (block_size != 16 && block_size != 32))
         return PA_ERR_UNSUPPORTED;
     if (!pick_decode(dtype, head_dim, group_pad(G), &r->entry)) return PA_ERR_UNSUPPORTED;
-    r->tc = use_tensor_cores(head_dim, G);
+    r->tc = use_tensor_cores(head_dim, G) && !int4;
     r->fp8 = fp8;
+    r->int4 = int4;
     if (fp8 && !fp8_supported(head_dim, G)) return PA_ERR_UNSUPPORTED;
     r->bf16 = dtype == PA_BF16;
     r->head_dim = head_dim;
     int P = partition_tokens;
     if (P == 0) {
         const int per_sm = r->fp8  ? fp8_ctas_per_sm(dtype == PA_BF16, head_dim, G)
+                           : r->int4 ? int4_ctas_per_sm(dtype == PA_BF16, head_dim)
                            : r->tc ? tc_ctas_per_sm(dtype == PA_BF16, head_dim)
                                    : decode_ctas_per_sm(r->entry);
         P = auto_partition(num_seqs, num_kv_heads, max_seq_len, per_sm, block_size, 4.0, 512);
@@ -913,6 +917,8 @@ static pa_status launch_decode(const ResolvedDecode &r, DecodeParams prm, int nu
         prm.one_wave = (r.tc || r.fp8) &&
                        (int64_t)chunks * num_kv_heads * num_seqs <= (int64_t)sm_count() * per_sm;
     }
+    if (r.int4)
+        return launch_decode_int4(prm, r.bf16, r.head_dim, chunks, num_kv_heads, num_seqs, stream);
     if (r.fp8) {
         if (prm.prefix_parts) return PA_ERR_UNSUPPORTED;  // no cascade over E4M3 pools
         prm.span = span;
@@ -988,13 +994,13 @@ static pa_status decode_impl(void *out, const void *q, const void *k_new, const 
                              int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                              float scale, int partition_tokens, void *workspace,
                              size_t workspace_bytes, pa_dtype dtype, void *stream,
-                             const KvFp8 *fp8 = nullptr) {
+                             const KvFp8 *fp8 = nullptr, bool int4 = false) {
     ResolvedDecode r;
     if (fp8 && (!(fp8->k_scale > 0.f) || !(fp8->v_scale > 0.f) || !std::isfinite(fp8->k_scale) ||
                 !std::isfinite(fp8->v_scale)))
         return PA_ERR_INVALID;
     pa_status st = resolve(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
-                           max_seq_len, partition_tokens, dtype, &r, fp8 != nullptr);
+                           max_seq_len, partition_tokens, dtype, &r, fp8 != nullptr, true, int4);
     if (st != PA_OK) return st;
     if (num_seqs > 0 && (!out || !aligned16(out))) return PA_ERR_INVALID;
     DecodeParams prm;
@@ -1189,6 +1195,29 @@ pa_status pa_decode_fp8(void *out, const void *q, const void *k_new, const void 
                        block_tables, max_blocks_per_seq, seq_lens, max_seq_len, num_seqs,
                        num_q_heads, num_kv_heads, head_dim, block_size, scale, partition_tokens,
                        workspace, workspace_bytes, dtype, stream, &fp8);
+}
+
+size_t pa_decode_int4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int block_size, int max_seq_len, int partition_tokens,
+                                     pa_dtype dtype) {
+    ResolvedDecode r;
+    if (resolve(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len,
+                partition_tokens, dtype, &r, false, true, true) != PA_OK)
+        return 0;
+    if (r.P <= 0) return 0;
+    return workspace_layout(num_seqs, num_q_heads, head_dim, r.NP, num_kv_heads).bytes;
+}
+
+pa_status pa_decode_int4(void *out, const void *q, const void *k_pool, const void *v_pool,
+                         int num_blocks, const int32_t *block_tables, int max_blocks_per_seq,
+                         const int32_t *seq_lens, int max_seq_len, int num_seqs, int num_q_heads,
+                         int num_kv_heads, int head_dim, int block_size, float scale,
+                         int partition_tokens, void *workspace, size_t workspace_bytes,
+                         pa_dtype dtype, void *stream) {
+    return decode_impl(out, q, nullptr, nullptr, nullptr, k_pool, v_pool, num_blocks,
+                       block_tables, max_blocks_per_seq, seq_lens, max_seq_len, num_seqs,
+                       num_q_heads, num_kv_heads, head_dim, block_size, scale, partition_tokens,
+                       workspace, workspace_bytes, dtype, stream, nullptr, true);
 }
 
 pa_status pa_decode_step(void *out, const void *q, const void *k_new, const void *v_new,

@@ -564,6 +564,12 @@ int fp8_ctas_per_sm(bool bf16, int head_dim, int group);
 pa_status launch_decode_fp8(const DecodeParams &prm, bool bf16, int head_dim, int num_partitions,
                             int num_kv_heads, int num_seqs, cudaStream_t stream);
 
+// Decode over 4-bit pools (pa_decode_int4.cu); the pool pointers of prm are
+// those of the records.
+int int4_ctas_per_sm(bool bf16, int head_dim);
+pa_status launch_decode_int4(const DecodeParams &prm, bool bf16, int head_dim, int num_partitions,
+                             int num_kv_heads, int num_seqs, cudaStream_t stream);
+
 // Prefix pass of the shared-prefix (cascade) decode (pa_cascade.cu): the
 // positions [0, prefix_len) that every sequence reaches through the same
 // block-table entries (sequence 0's row gives them), attended once per KV

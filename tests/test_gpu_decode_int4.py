@@ -213,6 +213,16 @@ def test_nan_rows_reach_only_their_own_heads():
         assert torch.isfinite(out).all()
 
 
+def test_sequences_of_nan_rows_alone():
+    def rows(rng, shape):
+        return np.full(shape, np.nan)
+    for where in ("k_rows", "v_rows"):
+        c = Case([1, 0, 70], 1, 3, 64, 16, "bf16", **{where: rows})
+        for partition in (-1, 16, 0):
+            out = c.gpu(partition).float()
+            assert torch.isnan(out[[0, 2]]).all() and not out[1].any()
+
+
 def test_workspace_of_garbage_is_scratch():
     c = Case([700, 90, 1500], 2, 4, 128, 16, "bf16")
     for partition in (256, 96):

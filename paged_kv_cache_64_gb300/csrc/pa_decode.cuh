@@ -566,7 +566,7 @@ pa_status launch_decode_fp8(const DecodeParams &prm, bool bf16, int head_dim, in
 
 // Decode over 4-bit pools (pa_decode_int4.cu); the pool pointers of prm are
 // those of the records.
-int int4_ctas_per_sm(bool bf16, int head_dim);
+int int4_ctas_per_sm(bool bf16, int head_dim, int block_size, int group);
 pa_status launch_decode_int4(const DecodeParams &prm, bool bf16, int head_dim, int num_partitions,
                              int num_kv_heads, int num_seqs, cudaStream_t stream);
 

@@ -42,12 +42,14 @@ namespace pa {
 constexpr int kInt4Warps = 4;
 constexpr int kInt4MaxG = 8;
 
+constexpr int kInt4Step = 32;  // positions a warp takes at a time: two score tiles
+
 template <int D>
 struct Int4Shape {
-    static constexpr int CODES = kUnit * D / 2;             // bytes of a tile's codes
-    static constexpr int STAGE = 2 * CODES + 2 * kUnit * 4; // K codes, V codes, K and V (s, m)
-    static constexpr int STAGES = D == 128 ? 4 : 6;
-    static constexpr int RING = STAGES * STAGE;             // a warp's
+    static constexpr int CODES = kInt4Step * D / 2;              // bytes of a step's codes
+    static constexpr int STAGE = 2 * CODES + 2 * kInt4Step * 4;  // K, V codes, K, V (s, m)
+    static constexpr int STAGES = D == 128 ? 3 : 4;
+    static constexpr int RING = STAGES * STAGE;                  // a warp's
     static constexpr int RED_BYTES = kInt4Warps * kInt4MaxG * (D + 2) * 4;
     static constexpr int SMEM_BYTES = kInt4Warps * RING > RED_BYTES ? kInt4Warps * RING : RED_BYTES;
 };
@@ -77,10 +79,10 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <bool BF16, int D>
+template <bool BF16, int D, int B, bool H4>
 __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const DecodeParams p) {
     using S = Int4Shape<D>;
-    constexpr int KW = D / 32;  // words of a key row a lane holds (32 D / 128 codes)
+    constexpr int KW = D / 32;  // words of a key row a lane holds (8 codes each)
     constexpr int VW = D / 64;  // words of a value row a lane holds
     extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -103,67 +105,76 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
         return;
     }
     if (chunk >= nparts) return;
-    const int end = L - start < P ? L : start + P;
-    const int ntiles = (end - start + kUnit - 1) / kUnit;
-    const int my_tiles = (ntiles - warp + kInt4Warps - 1) / kInt4Warps;
+    const int count = L - start < P ? L - start : P;  // positions of this chunk
+    const int nsteps = (count + kInt4Step - 1) / kInt4Step;
+    const int my_steps = (nsteps - warp + kInt4Warps - 1) / kInt4Warps;
 
     // -------------------------------------------------------------- loads
+    constexpr int E = kInt4Step / B;                 // blocks of a step
+    constexpr int REC = int4_record_bytes<D>(B);
+    constexpr int BLOCK_CODES = B * D / 2, PIECES = B / 4;  // 16-byte pieces of a block's (s, m)
     uint8_t *ring = smem + warp * S::RING;
-    const int rec_bytes = int4_record_bytes<D>(p.block_size);
-    const uint8_t *kpool = reinterpret_cast<const uint8_t *>(p.k_pool);
-    const uint8_t *vpool = reinterpret_cast<const uint8_t *>(p.v_pool);
-    const int32_t *table = seq_table(p, seq);
-    // block ids of this warp's tiles, 32 tiles at a time, a lane each
+    const uint32_t block_stride = (uint32_t)p.num_kv_heads * REC;
+    const uint8_t *kl = reinterpret_cast<const uint8_t *>(p.k_pool) + kvh * REC + lane * 16;
+    const uint8_t *vl = reinterpret_cast<const uint8_t *>(p.v_pool) + kvh * REC + lane * 16;
+    const uint8_t *pl = (lane < PIECES ? kl : vl - PIECES * 16) + BLOCK_CODES;
+    const uint32_t pdst = (lane < PIECES ? lane : lane + kInt4Step / 4 - PIECES) * 16;
+    const int32_t *table = seq_table(p, seq) + start / B;
+    // block ids of this warp's steps, a lane each, 32 at a time; -1 past the end
     auto window = [&](int w) -> int {
-        const int kt = warp + kInt4Warps * (32 * w + lane);
-        if (kt >= ntiles) return 0;
-        const int phys = table[(start + kt * kUnit) >> p.log2_block];
+        const int i = 32 * w + lane;
+        const int b = (warp + kInt4Warps * (i / E)) * E + i % E;
+        if (b * B >= count) return -1;
+        const int phys = table[b];
         if ((unsigned)phys < (unsigned)p.num_blocks) return phys;
         record_error(p.err, PA_ERR_BAD_INDEX);
         return 0;
     };
     int cur = window(0), nxt = 0;
-    auto issue = [&](int k, int stage) {
-        if (k < my_tiles) {
-            if ((k & 31) == 0) {
-                if (k) cur = nxt;
-                nxt = window((k >> 5) + 1);
+    auto issue = [&](int k, uint8_t *dst) {
+        if (k < my_steps) {
+            const int i = k * E;
+            if ((i & 31) == 0) {
+                if (i) cur = nxt;
+                nxt = window((i >> 5) + 1);
             }
-            const int phys = __shfl_sync(kFullMask, cur, k & 31);
-            const int row = (start + (warp + kInt4Warps * k) * kUnit) & (p.block_size - 1);
-            const int64_t rec = ((int64_t)phys * p.num_kv_heads + kvh) * rec_bytes;
-            const int codes = row * (D / 2), params = p.block_size * (D / 2) + row * 4;
-            uint8_t *dst = ring + stage * S::STAGE;
 #pragma unroll
-            for (int i = 0; i < S::CODES / 512; ++i) {
-                const int b = i * 512 + lane * 16;
-                cp_async16_cg(dst + b, kpool + rec + codes + b);
-                cp_async16_cg(dst + S::CODES + b, vpool + rec + codes + b);
+            for (int e = 0; e < E; ++e) {
+                const int phys = __shfl_sync(kFullMask, cur, (i + e) & 31);
+                if (phys < 0) break;  // the step's second block, past the end
+                const uint64_t off = (uint64_t)(uint32_t)phys * block_stride;
+#pragma unroll
+                for (int c = 0; c < BLOCK_CODES / 512; ++c) {
+                    uint8_t *to = dst + e * BLOCK_CODES + c * 512 + lane * 16;
+                    cp_async16_cg(to, kl + off + c * 512);
+                    cp_async16_cg(to + S::CODES, vl + off + c * 512);
+                }
+                if (lane < 2 * PIECES)
+                    cp_async16_cg(dst + 2 * S::CODES + e * (B * 4) + pdst, pl + off);
             }
-            if (lane < 8)
-                cp_async16_cg(dst + 2 * S::CODES + lane * 16,
-                              (lane < 4 ? kpool : vpool) + rec + params + (lane & 3) * 16);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int k = 0; k < S::STAGES - 1; ++k) issue(k, k);
+    for (int k = 0; k < S::STAGES - 1; ++k) issue(k, ring + k * S::STAGE);
 
     // ------------------------------------------------------------ queries
-    // B fragments: column r is head r, this lane's elements are those of its
-    // key words.  2^kq brings the head's largest |q| below 2^15; elements
-    // that meet codes in the high four bits are divided by 16.
+    // B fragments: column r is head r (H4, at most four heads: r mod 4), this
+    // lane's elements are those of its key words.  2^kq brings the head's
+    // largest |q| below 2^15; elements that meet codes in the high four bits
+    // are divided by 16.
     uint32_t qf[KW][4];
     float cs[2], qs[2];  // of the score tile's columns 2t, 2t + 1
     {
+        const int head = H4 ? r & 3 : r;
         float x[KW][8];
         float top = 0.f, sum = 0.f;
 #pragma unroll
         for (int j = 0; j < KW; ++j) {
             uint4 raw = make_uint4(0, 0, 0, 0);
-            if (r < G)
+            if (head < G)
                 raw = *reinterpret_cast<const uint4 *>(
-                    p.q + ((int64_t)seq * p.num_q_heads + kvh * G + r) * D + (t * KW + j) * 8);
+                    p.q + ((int64_t)seq * p.num_q_heads + kvh * G + head) * D + (t * KW + j) * 8);
             widen8<BF16>(raw, x[j]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -195,74 +206,92 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
     }
 
     // ---------------------------------------------------------- main loop
-    // O[a][...]: dimensions 2a and 2a + 1 of this lane's D/8, heads 2t and
+    // O[a][...]: dimensions 2a and 2a + 1 of this lane's D/8, columns 2t and
     // 2t + 1, in units of 2^-24 / fe (odd dimensions 16 times that).
     float O[4 * VW][4];
 #pragma unroll
     for (int a = 0; a < 4 * VW; ++a) O[a][0] = O[a][1] = O[a][2] = O[a][3] = 0.f;
-    float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, pm[2] = {0.f, 0.f};
-    int ve = -110;                  // scales of V seen so far are below 2^ve
+    float M[2] = {0.f, 0.f}, l[2] = {0.f, 0.f}, pm[2] = {0.f, 0.f};
+    int ve = -110;                  // scales of V seen so far are at most 2^ve
+    float vtop = pow2i(ve);
     float fe = pow2i(7 - ve);       // weights are P s' fe, at most 2^8 2^7
     // Fragment row r is position pr of its half tile: pairs of rows (r, r + 1)
     // and rows of equal t differ in parity, so that neither the key loads (two
     // rows a quarter warp) nor the value loads (four rows a half warp) meet in
     // a bank more than they must.
     const int pr = r ^ ((r >> 1) & 1);
-    const int pv[2] = {(2 * t) ^ (t & 1), (2 * t + 1) ^ (t & 1)};
     constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
+    const int koff = pr * (D / 2) + t * (4 * KW);
+    const int voff = S::CODES + (2 * t) * (D / 2) + r * (4 * VW);
+    const int vx = (t & 1) * (D / 2);  // positions 2t, 2t + 1 change places where t is odd
     int stage = 0;
-    for (int k = 0; k < my_tiles; ++k) {
+#pragma unroll 1
+    for (int k = 0; k < my_steps; ++k) {
         cp_async_wait<S::STAGES - 2>();
         __syncwarp();
-        issue(k + S::STAGES - 1, stage == 0 ? S::STAGES - 1 : stage - 1);
         const uint8_t *tile = ring + stage * S::STAGE;
+        issue(k + S::STAGES - 1, ring + (stage == 0 ? S::STAGES - 1 : stage - 1) * S::STAGE);
         stage = stage + 1 == S::STAGES ? 0 : stage + 1;
 
-        // scores: two chains of MMAs over the dimensions
-        uint32_t w0[KW], w1[KW];
-        if constexpr (KW == 4) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(tile + pr * 64 + t * 16);
-            const uint4 b = *reinterpret_cast<const uint4 *>(tile + (8 + pr) * 64 + t * 16);
-            w0[0] = a.x; w0[1] = a.y; w0[2] = a.z; w0[3] = a.w;
-            w1[0] = b.x; w1[1] = b.y; w1[2] = b.z; w1[3] = b.w;
-        } else {
-            const uint2 a = *reinterpret_cast<const uint2 *>(tile + pr * 32 + t * 8);
-            const uint2 b = *reinterpret_cast<const uint2 *>(tile + (8 + pr) * 32 + t * 8);
-            w0[0] = a.x; w0[1] = a.y;
-            w1[0] = b.x; w1[1] = b.y;
-        }
+        // scores less the running maximum, base 2: s[u] is (position pr, columns
+        // 2t, 2t + 1), (position 8 + pr, the same) of the u-th 16 positions
+        float s[2][4], sv[2][2], mv[2][2];
         const uint32_t *par = reinterpret_cast<const uint32_t *>(tile + 2 * S::CODES);
-        const uint32_t pk0 = par[pr], pk1 = par[8 + pr], pv0 = par[16 + pr], pv1 = par[24 + pr];
-        float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < KW; ++j) {
-            mma_f16(c0, w0[j] & kLo, w1[j] & kLo, w0[j] & kHi, w1[j] & kHi, qf[j][0], qf[j][1]);
-            const uint32_t u0 = w0[j] >> 8, u1 = w1[j] >> 8;
-            mma_f16(c1, u0 & kLo, u1 & kLo, u0 & kHi, u1 & kHi, qf[j][2], qf[j][3]);
-        }
-        const float sk0 = from16<BF16>(pk0 & 0xffffu), mk0 = from16<BF16>(pk0 >> 16);
-        const float sk1 = from16<BF16>(pk1 & 0xffffu), mk1 = from16<BF16>(pk1 >> 16);
-        float sv0 = from16<BF16>(pv0 & 0xffffu), mv0 = from16<BF16>(pv0 >> 16);
-        float sv1 = from16<BF16>(pv1 & 0xffffu), mv1 = from16<BF16>(pv1 >> 16);
-        float s[4];  // (position pr, heads 2t, 2t + 1), (position 8 + pr, the same), base 2
+        for (int u = 0; u < 2; ++u) {
+            uint32_t w[2][KW];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            s[h] = fmaf(c0[h] + c1[h], sk0 * cs[h], mk0 * qs[h]);
-            s[2 + h] = fmaf(c0[2 + h] + c1[2 + h], sk1 * cs[h], mk1 * qs[h]);
+            for (int h = 0; h < 2; ++h) {
+                const uint8_t *src = tile + koff + (16 * u + 8 * h) * (D / 2);
+                if constexpr (KW == 4) {
+                    const uint4 a = *reinterpret_cast<const uint4 *>(src);
+                    w[h][0] = a.x; w[h][1] = a.y; w[h][2] = a.z; w[h][3] = a.w;
+                } else {
+                    const uint2 a = *reinterpret_cast<const uint2 *>(src);
+                    w[h][0] = a.x; w[h][1] = a.y;
+                }
+            }
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < KW; ++j) {
+                mma_f16(c, w[0][j] & kLo, w[1][j] & kLo, w[0][j] & kHi, w[1][j] & kHi, qf[j][0],
+                        qf[j][1]);
+                const uint32_t u0 = w[0][j] >> 8, u1 = w[1][j] >> 8;
+                mma_f16(c, u0 & kLo, u1 & kLo, u0 & kHi, u1 & kHi, qf[j][2], qf[j][3]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t pk = par[16 * u + 8 * h + pr], pv = par[32 + 16 * u + 8 * h + pr];
+                const float sk = from16<BF16>(pk & 0xffffu), mk = from16<BF16>(pk >> 16);
+                sv[u][h] = from16<BF16>(pv & 0xffffu);
+                mv[u][h] = from16<BF16>(pv >> 16);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    s[u][2 * h + i] = fmaf(c[2 * h + i], sk * cs[i], fmaf(mk, qs[i], -M[i]));
+            }
         }
-        const int left = end - start - (warp + kInt4Warps * k) * kUnit;
-        if (left < kUnit) {  // slots past the end hold anything
-            if (pr >= left) s[0] = s[1] = -INFINITY, sv0 = mv0 = 0.f;
-            if (8 + pr >= left) s[2] = s[3] = -INFINITY, sv1 = mv1 = 0.f;
+        const int left = count - (warp + kInt4Warps * k) * kInt4Step;
+        if (left < kInt4Step) {  // slots past the end hold anything
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (16 * u + 8 * h + pr >= left) {
+                        s[u][2 * h] = s[u][2 * h + 1] = -INFINITY;
+                        sv[u][h] = mv[u][h] = 0.f;
+                    }
         }
 
         // The running maximum moves only when a score passes it by more than
-        // kLazyRescale, the running scale when one passes it.
-        const float sv = fmaxf(sv0, sv1);
-        const bool moves = fmaxf(s[0], s[2]) > M[0] + kLazyRescale ||
-                           fmaxf(s[1], s[3]) > M[1] + kLazyRescale || sv * fe > 128.f;
+        // kLazyRescale (and with the first step), the running scale when one
+        // passes it.
+        float top = fmaxf(fmaxf(sv[0][0], sv[0][1]), fmaxf(sv[1][0], sv[1][1]));
+        float mx[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            mx[i] = fmaxf(fmaxf(s[0][i], s[0][2 + i]), fmaxf(s[1][i], s[1][2 + i]));
+        const bool moves = fmaxf(mx[0], mx[1]) > kLazyRescale || top > vtop || k == 0;
         if (__any_sync(kFullMask, moves)) {
-            float top = sv, mx[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) {
                 top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
@@ -273,16 +302,23 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
             e = e > 127 ? 127 : e < ve ? ve : e;
             const float shrink = pow2i(ve - e < -126 ? -126 : ve - e);
             ve = e;
+            vtop = pow2i(ve);
             fe = pow2i(7 - ve);
             float f[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float m = fmaxf(M[h], mx[h]);
-                f[h] = m == -INFINITY ? 1.f : fast_exp2(M[h] - m);
-                M[h] = m;
-                l[h] *= f[h];
-                pm[h] *= f[h];
-                f[h] *= shrink;
+            for (int i = 0; i < 2; ++i) {
+                const float up = k == 0 ? mx[i] : fmaxf(mx[i], 0.f);
+                M[i] += up;
+                f[i] = fast_exp2(-up);
+                if (k == 0) f[i] = 0.f;  // nothing summed yet
+                l[i] *= f[i];
+                pm[i] *= f[i];
+                f[i] *= shrink;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    s[u][i] -= up;
+                    s[u][2 + i] -= up;
+                }
             }
 #pragma unroll
             for (int a = 0; a < 4 * VW; ++a) {
@@ -293,55 +329,62 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
             }
         }
 
-        // weights, their sums, and the two f16 terms of P s' fe, transposed to
-        // B fragments (rows: positions, columns: heads)
-        uint32_t bh[2], bl[2];
-        {
-            const float g0 = sv0 * fe, g1 = sv1 * fe;
-            const float p0 = fast_exp2(s[0] - M[0]), p1 = fast_exp2(s[1] - M[1]);
-            const float p2 = fast_exp2(s[2] - M[0]), p3 = fast_exp2(s[3] - M[1]);
-            l[0] += p0 + p2;
-            l[1] += p1 + p3;
-            pm[0] = fmaf(p0, mv0, fmaf(p2, mv1, pm[0]));
-            pm[1] = fmaf(p1, mv0, fmaf(p3, mv1, pm[1]));
-            const float x0 = p0 * g0, x1 = p1 * g0, x2 = p2 * g1, x3 = p3 * g1;
-            const uint32_t h0 = half2_bits(x0, x1), h1 = half2_bits(x2, x3);
-            const float2 y0 = widen2<false>(h0), y1 = widen2<false>(h1);
-            bh[0] = transpose8(h0);
-            bh[1] = transpose8(h1);
-            bl[0] = transpose8(half2_bits(x0 - y0.x, x1 - y0.y));
-            bl[1] = transpose8(half2_bits(x2 - y1.x, x3 - y1.y));
-        }
-
-        // O += V^T (P s')
-        const uint8_t *vt = tile + S::CODES + r * (4 * VW);
-        uint32_t v[4][VW];  // positions pv[0], pv[1], 8 + pv[0], 8 + pv[1]
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint8_t *src = vt + ((i >> 1) * 8 + pv[i & 1]) * (D / 2);
-            if constexpr (VW == 2) {
-                const uint2 a = *reinterpret_cast<const uint2 *>(src);
-                v[i][0] = a.x;
-                v[i][1] = a.y;
-            } else {
-                v[i][0] = *reinterpret_cast<const uint32_t *>(src);
+        for (int u = 0; u < 2; ++u) {
+            // weights, their sums, and the two f16 terms of P s' fe, transposed
+            // to B fragments (rows: positions, columns: heads; H4: the second
+            // terms of heads 0 .. 3 are columns 4 .. 7)
+            uint32_t bh[2], bl[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float g = sv[u][h] * fe;
+                const float p0 = fast_exp2(s[u][2 * h]), p1 = fast_exp2(s[u][2 * h + 1]);
+                l[0] += p0;
+                l[1] += p1;
+                pm[0] = fmaf(p0, mv[u][h], pm[0]);
+                pm[1] = fmaf(p1, mv[u][h], pm[1]);
+                const float x0 = p0 * g, x1 = p1 * g;
+                const uint32_t hi = half2_bits(x0, x1);
+                const float2 y = widen2<false>(hi);
+                const uint32_t lo = half2_bits(x0 - y.x, x1 - y.y);
+                if constexpr (H4) {
+                    bh[h] = transpose8(t < 2 ? hi : lo);
+                } else {
+                    bh[h] = transpose8(hi);
+                    bl[h] = transpose8(lo);
+                }
             }
-        }
+
+            // O += V^T (P s')
+            uint32_t v[4][VW];  // of B fragment rows 2t, 2t + 1, 8 + 2t, 9 + 2t
 #pragma unroll
-        for (int j = 0; j < VW; ++j) {
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t *src = tile + voff + (16 * u + 8 * (i >> 1)) * (D / 2) +
+                                     (i & 1 ? D / 2 - vx : vx);
+                if constexpr (VW == 2) {
+                    const uint2 a = *reinterpret_cast<const uint2 *>(src);
+                    v[i][0] = a.x;
+                    v[i][1] = a.y;
+                } else {
+                    v[i][0] = *reinterpret_cast<const uint32_t *>(src);
+                }
+            }
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {  // codes 0 .. 3 and 4 .. 7 of the words
-                const uint32_t sel = half ? 0x7632u : 0x5410u;
-                uint32_t x = __byte_perm(v[0][j], v[1][j], sel);
-                uint32_t y = __byte_perm(v[2][j], v[3][j], sel);
+            for (int j = 0; j < VW; ++j) {
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float(&acc)[4] = O[4 * j + 2 * half + q];
-                    const uint32_t a0 = x & kLo, a1 = x & kHi, a2 = y & kLo, a3 = y & kHi;
-                    mma_f16(acc, a0, a1, a2, a3, bh[0], bh[1]);
-                    mma_f16(acc, a0, a1, a2, a3, bl[0], bl[1]);
-                    x >>= 8;
-                    y >>= 8;
+                for (int half = 0; half < 2; ++half) {  // codes 0 .. 3 and 4 .. 7 of the words
+                    const uint32_t sel = half ? 0x7632u : 0x5410u;
+                    uint32_t x = __byte_perm(v[0][j], v[1][j], sel);
+                    uint32_t y = __byte_perm(v[2][j], v[3][j], sel);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        float(&acc)[4] = O[4 * j + 2 * half + q];
+                        const uint32_t a0 = x & kLo, a1 = x & kHi, a2 = y & kLo, a3 = y & kHi;
+                        mma_f16(acc, a0, a1, a2, a3, bh[0], bh[1]);
+                        if constexpr (!H4) mma_f16(acc, a0, a1, a2, a3, bl[0], bl[1]);
+                        x >>= 8;
+                        y >>= 8;
+                    }
                 }
             }
         }
@@ -357,10 +400,16 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
             l[h] += __shfl_xor_sync(kFullMask, l[h], o);
             pm[h] += __shfl_xor_sync(kFullMask, pm[h], o);
         }
+    if constexpr (H4) {  // the two terms' sums
+#pragma unroll
+        for (int a = 0; a < 4 * VW; ++a)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) O[a][i] += __shfl_xor_sync(kFullMask, O[a][i], 2);
+    }
     __syncthreads();  // the rings are done with
     float *red = reinterpret_cast<float *>(smem);  // [W][8][D]
     float *red_m = red + kInt4Warps * kInt4MaxG * D, *red_l = red_m + kInt4Warps * kInt4MaxG;
-    {
+    if (!H4 || t < 2) {
         const float unit = pow2i(ve);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -371,7 +420,7 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
                 dst[a] = make_float2(fmaf(O[a][h] * 0x1p17f, unit, pm[h]),
                                      fmaf(O[a][2 + h] * 0x1p13f, unit, pm[h]));
             if (r == 0) {
-                red_m[g] = M[h];
+                red_m[g] = my_steps > 0 ? M[h] : -INFINITY;
                 red_l[g] = l[h];
             }
         }
@@ -409,15 +458,24 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
 
 using Int4Kernel = void (*)(const DecodeParams);
 
-static Int4Kernel pick_int4(bool bf16, int D, int *smem) {
-    *smem = D == 64 ? Int4Shape<64>::SMEM_BYTES : Int4Shape<128>::SMEM_BYTES;
-    if (D == 64) return bf16 ? decode_int4_kernel<true, 64> : decode_int4_kernel<false, 64>;
-    return bf16 ? decode_int4_kernel<true, 128> : decode_int4_kernel<false, 128>;
+template <bool BF16, int D>
+static Int4Kernel int4_variant(int block_size, bool h4) {
+    if (block_size == 16)
+        return h4 ? decode_int4_kernel<BF16, D, 16, true> : decode_int4_kernel<BF16, D, 16, false>;
+    return h4 ? decode_int4_kernel<BF16, D, 32, true> : decode_int4_kernel<BF16, D, 32, false>;
 }
 
-int int4_ctas_per_sm(bool bf16, int head_dim) {
+static Int4Kernel pick_int4(bool bf16, int D, int block_size, int group, int *smem) {
+    const bool h4 = group <= 4;
+    *smem = D == 64 ? Int4Shape<64>::SMEM_BYTES : Int4Shape<128>::SMEM_BYTES;
+    if (D == 64)
+        return bf16 ? int4_variant<true, 64>(block_size, h4) : int4_variant<false, 64>(block_size, h4);
+    return bf16 ? int4_variant<true, 128>(block_size, h4) : int4_variant<false, 128>(block_size, h4);
+}
+
+int int4_ctas_per_sm(bool bf16, int head_dim, int block_size, int group) {
     int smem = 0, n = 0;
-    Int4Kernel k = pick_int4(bf16, head_dim, &smem);
+    Int4Kernel k = pick_int4(bf16, head_dim, block_size, group, &smem);
     if (!ensure_smem_attr(reinterpret_cast<const void *>(k), smem)) return 1;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, 32 * kInt4Warps, smem) != cudaSuccess)
         return 1;
@@ -428,7 +486,7 @@ pa_status launch_decode_int4(const DecodeParams &prm, bool bf16, int head_dim, i
                              int num_kv_heads, int num_seqs, cudaStream_t stream) {
     if (num_seqs == 0) return PA_OK;
     int smem = 0;
-    Int4Kernel k = pick_int4(bf16, head_dim, &smem);
+    Int4Kernel k = pick_int4(bf16, head_dim, prm.block_size, prm.group, &smem);
     if (!ensure_smem_attr(reinterpret_cast<const void *>(k), smem)) return PA_ERR_CUDA;
     DecodeParams p = prm;
     if (p.compact) p.compact = 2;  // full chunks first, the short last ones at the end

@@ -46,12 +46,13 @@ constexpr int kInt4Step = 32;  // positions a warp takes at a time: two score ti
 
 template <int D>
 struct Int4Shape {
-    static constexpr int CODES = kInt4Step * D / 2;              // bytes of a step's codes
-    static constexpr int STAGE = 2 * CODES + 2 * kInt4Step * 4;  // K, V codes, K, V (s, m)
+    static constexpr int HALF = kInt4Step * (D / 2 + 4);  // a step's K (or V) records
+    static constexpr int STAGE = 2 * HALF;
     static constexpr int STAGES = D == 128 ? 3 : 4;
-    static constexpr int RING = STAGES * STAGE;                  // a warp's
-    static constexpr int RED_BYTES = kInt4Warps * kInt4MaxG * (D + 2) * 4;
-    static constexpr int SMEM_BYTES = kInt4Warps * RING > RED_BYTES ? kInt4Warps * RING : RED_BYTES;
+    static constexpr int RING = STAGES * STAGE;           // a warp's
+    static constexpr int BARS = kInt4Warps * RING;        // offset of the mbarriers
+    static constexpr int SMEM_BYTES = BARS + kInt4Warps * STAGES * 8;
+    static_assert(kInt4Warps * kInt4MaxG * (D + 2) * 4 <= BARS, "the merge reuses the rings");
 };
 
 // D += A B: A 16 x 16 f16 (row-major fragments), B 16 x 8 f16, D 16 x 8 fp32.
@@ -61,6 +62,15 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         "{%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same from zero.
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Transpose of an 8 x 8 matrix of 16-bit values held two a lane.
@@ -74,11 +84,6 @@ __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t
 
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) { return narrow2<false>(a, b); }
 
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 template <bool BF16, int D, int B, bool H4>
 __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const DecodeParams p) {
     using S = Int4Shape<D>;
@@ -87,6 +92,12 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
     extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, t = lane & 3;  // fragment row (or column) and quad lane
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::BARS) + warp * S::STAGES;
+    if (lane == 0) {
+        for (int i = 0; i < S::STAGES; ++i) mbar_init(&bars[i], 1);
+        mbar_init_fence();
+    }
+    __syncwarp();
     pdl_wait();
     int chunk, kvh, seq;
     if (p.compact) {
@@ -110,53 +121,47 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
     const int my_steps = (nsteps - warp + kInt4Warps - 1) / kInt4Warps;
 
     // -------------------------------------------------------------- loads
-    constexpr int E = kInt4Step / B;                 // blocks of a step
+    // A step is one or two whole records of K and as many of V, each a bulk
+    // copy issued by a lane of its own; lane 2 e + (0 K, 1 V) takes block e.
+    constexpr int E = kInt4Step / B;  // blocks of a step
     constexpr int REC = int4_record_bytes<D>(B);
-    constexpr int BLOCK_CODES = B * D / 2, PIECES = B / 4;  // 16-byte pieces of a block's (s, m)
     uint8_t *ring = smem + warp * S::RING;
     const uint32_t block_stride = (uint32_t)p.num_kv_heads * REC;
-    const uint8_t *kl = reinterpret_cast<const uint8_t *>(p.k_pool) + kvh * REC + lane * 16;
-    const uint8_t *vl = reinterpret_cast<const uint8_t *>(p.v_pool) + kvh * REC + lane * 16;
-    const uint8_t *pl = (lane < PIECES ? kl : vl - PIECES * 16) + BLOCK_CODES;
-    const uint32_t pdst = (lane < PIECES ? lane : lane + kInt4Step / 4 - PIECES) * 16;
+    const uint8_t *mine = reinterpret_cast<const uint8_t *>(lane & 1 ? p.v_pool : p.k_pool) +
+                          (int64_t)kvh * REC;
+    const uint32_t to = (lane & 1) * S::HALF + (lane >> 1) * REC;
     const int32_t *table = seq_table(p, seq) + start / B;
     // block ids of this warp's steps, a lane each, 32 at a time; -1 past the end
     auto window = [&](int w) -> int {
         const int i = 32 * w + lane;
         const int b = (warp + kInt4Warps * (i / E)) * E + i % E;
-        if (b * B >= count) return -1;
+        if (b >= (count + B - 1) / B) return -1;
         const int phys = table[b];
         if ((unsigned)phys < (unsigned)p.num_blocks) return phys;
         record_error(p.err, PA_ERR_BAD_INDEX);
         return 0;
     };
     int cur = window(0), nxt = 0;
-    auto issue = [&](int k, uint8_t *dst) {
-        if (k < my_steps) {
-            const int i = k * E;
-            if ((i & 31) == 0) {
-                if (i) cur = nxt;
-                nxt = window((i >> 5) + 1);
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int phys = __shfl_sync(kFullMask, cur, (i + e) & 31);
-                if (phys < 0) break;  // the step's second block, past the end
-                const uint64_t off = (uint64_t)(uint32_t)phys * block_stride;
-#pragma unroll
-                for (int c = 0; c < BLOCK_CODES / 512; ++c) {
-                    uint8_t *to = dst + e * BLOCK_CODES + c * 512 + lane * 16;
-                    cp_async16_cg(to, kl + off + c * 512);
-                    cp_async16_cg(to + S::CODES, vl + off + c * 512);
-                }
-                if (lane < 2 * PIECES)
-                    cp_async16_cg(dst + 2 * S::CODES + e * (B * 4) + pdst, pl + off);
-            }
+    auto issue = [&](int k, int stage) {
+        if (k >= my_steps) return;
+        const int i = k * E;
+        if ((i & 31) == 0) {
+            if (i) cur = nxt;
+            nxt = window((i >> 5) + 1);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        const int phys = __shfl_sync(kFullMask, cur, (i + (lane >> 1)) & 31);
+        // (every lane is past its reads of this stage: the ballot, and the
+        // barrier before the copies)
+        const bool copies = lane < 2 * E && phys >= 0;
+        const int n = __popc(__ballot_sync(kFullMask, copies));
+        if (lane == 0) mbar_arrive_expect_tx(&bars[stage], (uint32_t)(n * REC));
+        __syncwarp();
+        if (copies)
+            bulk_copy_g2s(ring + stage * S::STAGE + to, mine + (uint64_t)(uint32_t)phys * block_stride,
+                          REC, &bars[stage]);
     };
 #pragma unroll
-    for (int k = 0; k < S::STAGES - 1; ++k) issue(k, ring + k * S::STAGE);
+    for (int k = 0; k < S::STAGES - 1; ++k) issue(k, k);
 
     // ------------------------------------------------------------ queries
     // B fragments: column r is head r (H4, at most four heads: r mod 4), this
@@ -206,8 +211,8 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
     }
 
     // ---------------------------------------------------------- main loop
-    // O[a][...]: dimensions 2a and 2a + 1 of this lane's D/8, columns 2t and
-    // 2t + 1, in units of 2^-24 / fe (odd dimensions 16 times that).
+    // O[a][...]: of this lane's D/8 dimensions, 2a, and 2a + 1 16 times with 2a
+    // added, columns 2t and 2t + 1, in units of 2^-24 / fe.
     float O[4 * VW][4];
 #pragma unroll
     for (int a = 0; a < 4 * VW; ++a) O[a][0] = O[a][1] = O[a][2] = O[a][3] = 0.f;
@@ -221,28 +226,36 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
     // a bank more than they must.
     const int pr = r ^ ((r >> 1) & 1);
     constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
+    // offsets of position `pos` of a step in its half of a stage
+    constexpr int U = B == 32 ? 16 * (D / 2) : REC;       // 16 positions on
+    constexpr int PU = B == 32 ? 16 * 4 : REC;            // the same for the (s, m) pairs
     const int koff = pr * (D / 2) + t * (4 * KW);
-    const int voff = S::CODES + (2 * t) * (D / 2) + r * (4 * VW);
+    const int poff = B * (D / 2) + pr * 4;
+    const int voff = S::HALF + (2 * t) * (D / 2) + r * (4 * VW);
     const int vx = (t & 1) * (D / 2);  // positions 2t, 2t + 1 change places where t is odd
     int stage = 0;
+    uint32_t parity = 0;
+    bool arrived = true;
 #pragma unroll 1
     for (int k = 0; k < my_steps; ++k) {
-        cp_async_wait<S::STAGES - 2>();
-        __syncwarp();
+        arrived = __all_sync(kFullMask, mbar_wait(&bars[stage], parity));
+        if (!arrived) break;
         const uint8_t *tile = ring + stage * S::STAGE;
-        issue(k + S::STAGES - 1, ring + (stage == 0 ? S::STAGES - 1 : stage - 1) * S::STAGE);
-        stage = stage + 1 == S::STAGES ? 0 : stage + 1;
+        issue(k + S::STAGES - 1, stage == 0 ? S::STAGES - 1 : stage - 1);
+        if (++stage == S::STAGES) {
+            stage = 0;
+            parity ^= 1;
+        }
 
         // scores less the running maximum, base 2: s[u] is (position pr, columns
         // 2t, 2t + 1), (position 8 + pr, the same) of the u-th 16 positions
         float s[2][4], sv[2][2], mv[2][2];
-        const uint32_t *par = reinterpret_cast<const uint32_t *>(tile + 2 * S::CODES);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             uint32_t w[2][KW];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint8_t *src = tile + koff + (16 * u + 8 * h) * (D / 2);
+                const uint8_t *src = tile + koff + u * U + 8 * h * (D / 2);
                 if constexpr (KW == 4) {
                     const uint4 a = *reinterpret_cast<const uint4 *>(src);
                     w[h][0] = a.x; w[h][1] = a.y; w[h][2] = a.z; w[h][3] = a.w;
@@ -251,17 +264,23 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
                     w[h][0] = a.x; w[h][1] = a.y;
                 }
             }
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            float c[4];
 #pragma unroll
             for (int j = 0; j < KW; ++j) {
-                mma_f16(c, w[0][j] & kLo, w[1][j] & kLo, w[0][j] & kHi, w[1][j] & kHi, qf[j][0],
-                        qf[j][1]);
+                const uint32_t a0 = w[0][j] & kLo, a1 = w[1][j] & kLo;
+                const uint32_t a2 = w[0][j] & kHi, a3 = w[1][j] & kHi;
+                if (j == 0)
+                    mma_f16_zero(c, a0, a1, a2, a3, qf[j][0], qf[j][1]);
+                else
+                    mma_f16(c, a0, a1, a2, a3, qf[j][0], qf[j][1]);
                 const uint32_t u0 = w[0][j] >> 8, u1 = w[1][j] >> 8;
                 mma_f16(c, u0 & kLo, u1 & kLo, u0 & kHi, u1 & kHi, qf[j][2], qf[j][3]);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t pk = par[16 * u + 8 * h + pr], pv = par[32 + 16 * u + 8 * h + pr];
+                const uint8_t *par = tile + poff + u * PU + 8 * h * 4;
+                const uint32_t pk = *reinterpret_cast<const uint32_t *>(par);
+                const uint32_t pv = *reinterpret_cast<const uint32_t *>(par + S::HALF);
                 const float sk = from16<BF16>(pk & 0xffffu), mk = from16<BF16>(pk >> 16);
                 sv[u][h] = from16<BF16>(pv & 0xffffu);
                 mv[u][h] = from16<BF16>(pv >> 16);
@@ -359,7 +378,7 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
             uint32_t v[4][VW];  // of B fragment rows 2t, 2t + 1, 8 + 2t, 9 + 2t
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint8_t *src = tile + voff + (16 * u + 8 * (i >> 1)) * (D / 2) +
+                const uint8_t *src = tile + voff + u * U + 8 * (i >> 1) * (D / 2) +
                                      (i & 1 ? D / 2 - vx : vx);
                 if constexpr (VW == 2) {
                     const uint2 a = *reinterpret_cast<const uint2 *>(src);
@@ -374,16 +393,17 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {  // codes 0 .. 3 and 4 .. 7 of the words
                     const uint32_t sel = half ? 0x7632u : 0x5410u;
-                    uint32_t x = __byte_perm(v[0][j], v[1][j], sel);
-                    uint32_t y = __byte_perm(v[2][j], v[3][j], sel);
+                    const uint32_t x = __byte_perm(v[0][j], v[1][j], sel);
+                    const uint32_t y = __byte_perm(v[2][j], v[3][j], sel);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
+                        // a whole byte, 16 n(odd) + n(even), and its low half
+                        const uint32_t xb = q ? __byte_perm(x, 0u, 0x4341) : x & 0x00ff00ffu;
+                        const uint32_t yb = q ? __byte_perm(y, 0u, 0x4341) : y & 0x00ff00ffu;
+                        const uint32_t xl = (q ? xb : x) & kLo, yl = (q ? yb : y) & kLo;
                         float(&acc)[4] = O[4 * j + 2 * half + q];
-                        const uint32_t a0 = x & kLo, a1 = x & kHi, a2 = y & kLo, a3 = y & kHi;
-                        mma_f16(acc, a0, a1, a2, a3, bh[0], bh[1]);
-                        if constexpr (!H4) mma_f16(acc, a0, a1, a2, a3, bl[0], bl[1]);
-                        x >>= 8;
-                        y >>= 8;
+                        mma_f16(acc, xl, xb, yl, yb, bh[0], bh[1]);
+                        if constexpr (!H4) mma_f16(acc, xl, xb, yl, yb, bl[0], bl[1]);
                     }
                 }
             }
@@ -392,7 +412,13 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
 
     // -------------------------------------------------------------- merge
     pdl_trigger();
-    cp_async_wait<0>();
+    if (!arrived && lane == 0) {
+        // A bounded wait ran out: let copies still in flight land (bounded
+        // again) before the shared memory goes; the output is then unspecified.
+        record_error(p.err, PA_ERR_DEVICE_TIMEOUT);
+        for (int i = 0; i < S::STAGES; ++i) (void)mbar_wait(&bars[i], i >= stage ? parity : parity ^ 1);
+    }
+    __syncwarp();
 #pragma unroll
     for (int o = 4; o <= 16; o <<= 1)
 #pragma unroll
@@ -418,7 +444,7 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
 #pragma unroll
             for (int a = 0; a < 4 * VW; ++a)  // 2^24 / fe = 2^(17 + ve)
                 dst[a] = make_float2(fmaf(O[a][h] * 0x1p17f, unit, pm[h]),
-                                     fmaf(O[a][2 + h] * 0x1p13f, unit, pm[h]));
+                                     fmaf((O[a][2 + h] - O[a][h]) * 0x1p13f, unit, pm[h]));
             if (r == 0) {
                 red_m[g] = my_steps > 0 ? M[h] : -INFINITY;
                 red_l[g] = l[h];

@@ -84,6 +84,9 @@ struct DecodeParams {
     float k_inv;
     float v_inv;
     float v_scale;
+    // 4-bit pools: balanced ranges instead of chunks (pa_decode_int4.cu);
+    // part_m, part_l and part_o are then laid out by its slots.
+    int balanced;
 };
 
 // Length of sequence i, clamped to what the launch covers; a value out of
@@ -567,6 +570,9 @@ pa_status launch_decode_fp8(const DecodeParams &prm, bool bf16, int head_dim, in
 // Decode over 4-bit pools (pa_decode_int4.cu); the pool pointers of prm are
 // those of the records.
 int int4_ctas_per_sm(bool bf16, int head_dim, int block_size, int group);
+int int4_balanced_ctas(bool bf16, int head_dim, int block_size, int group, int num_seqs,
+                       int num_kv_heads, int max_seq_len);
+bool int4_balanced_cuts(int max_seq_len);
 pa_status launch_decode_int4(const DecodeParams &prm, bool bf16, int head_dim, int num_partitions,
                              int num_kv_heads, int num_seqs, cudaStream_t stream);
 

@@ -27,10 +27,9 @@
 // pipeline; with 8 columns a position costs a warp one MMA here (K and V
 // together two), and the masks feed it from the registers the loads filled.
 //
-// A warp works alone: its own tiles of 16 positions (every fourth of the
-// CTA's chunk), its own ring of stages filled by cp.async, its own running
+// A warp works alone: every fourth 32 positions of the CTA's piece, its own
+// ring of stages filled by bulk copies of whole records, its own running
 // maximum and sums; the four warps merge at the end through shared memory.
-// Long sequences are split over CTAs and combined as in the other decodes.
 #include <cstdint>
 
 #include "pa_decode.cuh"
@@ -84,39 +83,321 @@ __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t
 
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) { return narrow2<false>(a, b); }
 
+// Balanced ranges (automatic partitions).  The batch's work is one line of
+// units of 128 positions, sequence by sequence and head by head; CTA c takes
+// the units from bound(c) to bound(c + 1), where bound(c) = c * share, moved to
+// the next head's border where that is at most `slack` units away, so that no
+// head is cut for a sliver.  Every CTA works the line out from the lengths (one
+// load and a scan), so shares are equal whatever the lengths are, in one wave.
+// The partials of heads that bounds cut are merged by a second kernel.
+// A CTA's range: units [unit, end) of the line.  Its next unit is unit `at`
+// of the n units of head kvh of sequence seq.
+struct Int4Range {
+    int share, slack;
+    int unit, end;
+    int seq, kvh, at, n;
+};
+
+// A piece of work: `count` positions of a head from `start` on (-1: none
+// left), its partial's slot and the head's number of partials.
+struct Int4Piece {
+    int seq, kvh, start, count;
+    int slot, nparts;
+};
+
+constexpr int kInt4Unit = kInt4Step * kInt4Warps;  // positions
+constexpr int kInt4MinShare = 4;                   // units: smaller shares cost more than they save
+constexpr int kInt4MinSlack = 2;
+constexpr int kInt4BalancedSeqs = 1024;            // longer batches: a CTA an item, by the hardware
+
+__device__ __forceinline__ int int4_units(const DecodeParams &p, int seq) {
+    return (item_len(p, seq, false) + kInt4Unit - 1) / kInt4Unit;
+}
+
+// Pieces that bounds cut the range's present head into, and the first bound
+// inside it: those past its first slack units and before its last.
+__device__ __forceinline__ int int4_parts(const Int4Range &r, int *first) {
+    const int a = r.unit - r.at, b = a + r.n;  // the head on the line
+    *first = (a + r.slack) / r.share + 1;
+    const int last = b - r.slack - 1 < 0 ? -1 : (b - r.slack - 1) / r.share;
+    return max(last - *first + 1, 0) + 1;
+}
+
+// The range of CTA `cta` of ncta, or (cta < 0) the place of head `head`
+// (sequence head / Hkv), with n = 0 for one without positions.  Called by all T
+// threads of the block; ends synchronised.
+template <int T>
+__device__ __forceinline__ void int4_plan(const DecodeParams &p, int ncta, int cta, int head,
+                                          Int4Range *range) {
+    __shared__ int sums[T / 32];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int per = (p.num_seqs + T - 1) / T;
+    const int s0 = min(tid * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
+    int mine = 0;
+    for (int s = s0; s < s1; ++s) mine += int4_units(p, s);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kFullMask, incl, o);
+        if (lane >= o) incl += x;
+    }
+    if (lane == 31) sums[tid >> 5] = incl;
+    __syncthreads();
+    int before = incl - mine, all = 0;
+#pragma unroll
+    for (int w = 0; w < T / 32; ++w) {
+        if (w < (tid >> 5)) before += sums[w];
+        all += sums[w];
+    }
+    const int H = p.num_kv_heads, total = all * H;
+    const int share = max((total + ncta - 1) / ncta, kInt4MinShare);
+    const int slack = max(share / 16, kInt4MinSlack);
+    if (cta < 0) {
+        const int seq = head / H;
+        if (seq >= s0 && seq < s1) {
+            int base = before;
+            for (int s = s0; s < seq; ++s) base += int4_units(p, s);
+            range->seq = seq;
+            range->kvh = head - seq * H;
+            range->at = 0;
+            range->n = int4_units(p, seq);
+            range->unit = base * H + range->kvh * range->n;
+        }
+    } else {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int u = min((cta + b) * share, total);
+            if (u == total) {
+                if (tid == 0) {
+                    if (b == 0) range->unit = total;
+                    range->end = total;
+                }
+            } else if (u >= before * H && u < (before + mine) * H) {  // in this thread's sequences
+                int base = before * H, seq = s0, n = int4_units(p, s0);
+                while (u >= base + n * H) {
+                    base += n * H;
+                    n = int4_units(p, ++seq);
+                }
+                const int kvh = (u - base) / n;
+                int at = u - base - kvh * n;
+                if (at <= slack)
+                    at = 0;
+                else if (n - at <= slack)
+                    at = n;
+                if (b == 0) {
+                    range->seq = seq;
+                    range->kvh = kvh;
+                    range->at = at;
+                    range->n = n;
+                    range->unit = base + kvh * n + at;
+                } else {
+                    range->end = base + kvh * n + at;
+                }
+            }
+        }
+    }
+    if (tid == 0) {
+        range->share = share;
+        range->slack = slack;
+    }
+    __syncthreads();
+}
+
+// The next piece of the range (one thread).
+__device__ __forceinline__ void int4_next_piece(const DecodeParams &p, Int4Range *range,
+                                             Int4Piece *piece) {
+    Int4Range &r = *range;
+    if (r.unit >= r.end) {
+        piece->count = -1;
+        return;
+    }
+    if (r.at == r.n) {  // the next head with anything in it
+        r.at = 0;
+        if (++r.kvh == p.num_kv_heads) {
+            r.kvh = 0;
+            do r.n = int4_units(p, ++r.seq);
+            while (r.n == 0);
+        }
+    }
+    const int units = min(r.n - r.at, r.end - r.unit);
+    piece->seq = r.seq;
+    piece->kvh = r.kvh;
+    piece->start = r.at * kInt4Unit;
+    piece->count = min(item_len(p, r.seq, false), (r.at + units) * kInt4Unit) - piece->start;
+    piece->slot = 2 * (int)blockIdx.x + (r.at == 0 ? 1 : 0);
+    int first;
+    piece->nparts = int4_parts(r, &first);
+    r.unit += units;
+    r.at += units;
+}
+
+// Partials of the balanced ranges: CTA c leaves at most two, of the head its
+// range starts inside of (slot 2 c) and of the one it ends inside of, if that
+// one starts in it (slot 2 c + 1): m, l [slot][8] and O [slot][G][D].
+//
+// The merge: out = sum_k w_k O_k / sum_k w_k, w_k = l_k 2^(m_k - max m), over the
+// n partials of every head that bounds cut.  Few heads (HEADS, cut into many
+// partials each): a block a query head, its threads four dimensions each of
+// every SLICES-th partial.  Many heads: a block a bound, at work if that is the
+// first inside a head, its threads four dimensions each of all partials of
+// one or two query heads.  A thread has eight partials' loads in flight and
+// keeps its own running maximum, so nothing waits for the maxima first.
+constexpr int kInt4MergeHeads = 512, kInt4MergeBounds = 128;  // threads
+
+template <bool BF16, int D, bool HEADS>
+__global__ void __launch_bounds__(HEADS ? kInt4MergeHeads : kInt4MergeBounds)
+    int4_merge_kernel(const DecodeParams p, int ncta) {
+    constexpr int T = HEADS ? kInt4MergeHeads : kInt4MergeBounds;
+    constexpr int ITEMS = D / 4, ROWS = T / ITEMS, SLICES = HEADS ? ROWS : 1;
+    __shared__ Int4Range range;
+    __shared__ float4 sums[HEADS ? T : 1];
+    __shared__ float tops[ROWS], totals[ROWS];
+    const int item = threadIdx.x % ITEMS, row = threadIdx.x / ITEMS;
+    // the decode kernel began after all work before it was done, so the lengths
+    // are there
+    int4_plan<T>(p, ncta, HEADS ? -1 : blockIdx.x + 1, blockIdx.x, &range);
+    int first = 0, n = 0;
+    const bool mine = (HEADS ? range.n > 0 : range.unit < range.end && range.at > 0 &&
+                                                 range.at < range.n) &&
+                      (n = int4_parts(range, &first)) > 1 && (HEADS || first == blockIdx.x + 1);
+    pdl_wait();
+    if (!mine) return;
+    auto slot = [&](int k) { return k == 0 ? 2 * (first - 1) + 1 : 2 * (first - 1 + k); };
+    for (int g = HEADS ? blockIdx.y : row; g < p.group; g += ROWS) {
+        const float4 *rows = reinterpret_cast<const float4 *>(p.part_o) + g * ITEMS + item;
+        const int64_t stride = (int64_t)p.group * ITEMS;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float total = 0.f, M = -INFINITY;
+        for (int k0 = HEADS ? row : 0; k0 < n; k0 += 8 * SLICES) {
+            float4 v[8];
+            float m[8], l[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int s = slot(min(k0 + j * SLICES, n - 1));
+                v[j] = __ldcg(rows + s * stride);
+                m[j] = __ldcg(p.part_m + s * kInt4MaxG + g);
+                l[j] = __ldcg(p.part_l + s * kInt4MaxG + g);
+            }
+            float top = M;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, m[j]);
+            const float f = fast_exp2(M - top);
+            M = top;
+            total *= f;
+            o.x *= f;
+            o.y *= f;
+            o.z *= f;
+            o.w *= f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (k0 + j * SLICES >= n) break;
+                const float w = l[j] * fast_exp2(m[j] - M);
+                total += w;
+                o.x += w * v[j].x;
+                o.y += w * v[j].y;
+                o.z += w * v[j].z;
+                o.w += w * v[j].w;
+            }
+        }
+        if constexpr (HEADS) {
+            sums[threadIdx.x] = o;
+            if (item == 0) {
+                tops[row] = M;
+                totals[row] = total;
+            }
+            __syncthreads();
+            if (row > 0) return;
+            float top = M;
+#pragma unroll
+            for (int s = 1; s < SLICES; ++s) top = fmaxf(top, tops[s]);
+            o = make_float4(0.f, 0.f, 0.f, 0.f);
+            total = 0.f;
+#pragma unroll
+            for (int s = 0; s < SLICES; ++s) {
+                const float f = fast_exp2(tops[s] - top);  // a slice without partials: 0
+                const float4 v = sums[s * ITEMS + item];
+                total += f * totals[s];
+                o.x += f * v.x;
+                o.y += f * v.y;
+                o.z += f * v.z;
+                o.w += f * v.w;
+            }
+        }
+        const float f = 1.f / total;
+        uint16_t *out = static_cast<uint16_t *>(p.out) +
+                        ((int64_t)range.seq * p.num_q_heads + range.kvh * p.group + g) * D;
+        reinterpret_cast<uint2 *>(out)[item] =
+            make_uint2(narrow2<BF16>(o.x * f, o.y * f), narrow2<BF16>(o.z * f, o.w * f));
+        if constexpr (HEADS) return;
+    }
+}
+
 template <bool BF16, int D, int B, bool H4>
-__global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
+    const __grid_constant__ DecodeParams p) {
     using S = Int4Shape<D>;
     constexpr int KW = D / 32;  // words of a key row a lane holds (8 codes each)
     constexpr int VW = D / 64;  // words of a value row a lane holds
     extern __shared__ __align__(16) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r = lane >> 2, t = lane & 3;  // fragment row (or column) and quad lane
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::BARS) + warp * S::STAGES;
-    if (lane == 0) {
-        for (int i = 0; i < S::STAGES; ++i) mbar_init(&bars[i], 1);
+    if (threadIdx.x % 32 == 0) {
+        for (int i = 0; i < S::STAGES; ++i)
+            mbar_init(reinterpret_cast<uint64_t *>(smem + S::BARS) + threadIdx.x / 32 * S::STAGES + i, 1);
         mbar_init_fence();
     }
     __syncwarp();
     pdl_wait();
-    int chunk, kvh, seq;
-    if (p.compact) {
-        if (!compact_item(p, blockIdx.x, &seq, &chunk, &kvh)) return;
+    int stage = 0;        // of the warp's next step
+    uint32_t parity = 0;
+    bool arrived = true;
+
+    // The CTA's pieces of work: one chunk of one head (partition_tokens given),
+    // or every piece of its balanced range.  What only the ends of a piece need
+    // waits in shared memory.
+    __shared__ Int4Range range;
+    __shared__ Int4Piece piece;
+    if (p.balanced) {
+        pdl_trigger();  // the merge kernel may work out its plan
+        int4_plan<32 * kInt4Warps>(p, gridDim.x, blockIdx.x, 0, &range);
     } else {
-        chunk = blockIdx.x, kvh = blockIdx.y, seq = blockIdx.z;
+        int chunk, kvh, seq;
+        if (p.compact) {
+            if (!compact_item(p, blockIdx.x, &seq, &chunk, &kvh)) return;
+        } else {
+            chunk = blockIdx.x, kvh = blockIdx.y, seq = blockIdx.z;
+        }
+        if (threadIdx.x == 0) {
+            const int P = p.partition_tokens;
+            const int L = item_len(p, seq, chunk == 0 && kvh == 0);
+            piece.seq = seq;
+            piece.kvh = kvh;
+            piece.start = chunk * P;
+            piece.count = L == 0 ? (chunk == 0 ? 0 : -1) : max(min(L - chunk * P, P), -1);
+            piece.nparts = L == 0 ? 1 : (L - 1) / P + 1;
+            piece.slot = chunk;
+        }
+        __syncthreads();
+        if (piece.count < 0) return;
     }
-    const int L = item_len(p, seq, threadIdx.x == 0 && chunk == 0 && kvh == 0);
-    const int G = p.group, P = p.partition_tokens;
-    const int nparts = L == 0 ? 0 : (L - 1) / P + 1;
-    const int start = chunk * P;
-    uint16_t *out = static_cast<uint16_t *>(p.out) + ((int64_t)seq * p.num_q_heads + kvh * G) * D;
-    if (L == 0) {
-        if (chunk == 0)
-            for (int i = threadIdx.x; i < G * D; i += blockDim.x) out[i] = 0;
+    for (;;) {
+    if (p.balanced) {
+        if (threadIdx.x == 0) int4_next_piece(p, &range, &piece);
+        __syncthreads();
+        if (piece.count < 0) break;
+    }
+    // Taken anew for every piece, so that what follows from them is not kept in
+    // registers from one piece to the next.
+    int tid = threadIdx.x;
+    asm volatile("" : "+r"(tid));
+    const int warp = tid >> 5, lane = tid & 31;
+    const int r = lane >> 2, t = lane & 3;  // fragment row (or column) and quad lane
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::BARS) + warp * S::STAGES;
+    const int G = p.group;
+    const int seq = piece.seq, kvh = piece.kvh, start = piece.start, count = piece.count;
+    if (count == 0) {  // a sequence without tokens
+        uint16_t *out = static_cast<uint16_t *>(p.out) + ((int64_t)seq * p.num_q_heads + kvh * G) * D;
+        for (int i = threadIdx.x; i < G * D; i += blockDim.x) out[i] = 0;
         return;
     }
-    if (chunk >= nparts) return;
-    const int count = L - start < P ? L - start : P;  // positions of this chunk
     const int nsteps = (count + kInt4Step - 1) / kInt4Step;
     const int my_steps = (nsteps - warp + kInt4Warps - 1) / kInt4Warps;
 
@@ -161,7 +442,8 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
                           REC, &bars[stage]);
     };
 #pragma unroll
-    for (int k = 0; k < S::STAGES - 1; ++k) issue(k, k);
+    for (int k = 0; k < S::STAGES - 1; ++k)
+        issue(k, stage + k < S::STAGES ? stage + k : stage + k - S::STAGES);
 
     // ------------------------------------------------------------ queries
     // B fragments: column r is head r (H4, at most four heads: r mod 4), this
@@ -233,9 +515,6 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
     const int poff = B * (D / 2) + pr * 4;
     const int voff = S::HALF + (2 * t) * (D / 2) + r * (4 * VW);
     const int vx = (t & 1) * (D / 2);  // positions 2t, 2t + 1 change places where t is odd
-    int stage = 0;
-    uint32_t parity = 0;
-    bool arrived = true;
 #pragma unroll 1
     for (int k = 0; k < my_steps; ++k) {
         arrived = __all_sync(kFullMask, mbar_wait(&bars[stage], parity));
@@ -411,7 +690,6 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
     }
 
     // -------------------------------------------------------------- merge
-    pdl_trigger();
     if (!arrived && lane == 0) {
         // A bounded wait ran out: let copies still in flight land (bounded
         // again) before the shared memory goes; the output is then unspecified.
@@ -452,6 +730,8 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
         }
     }
     __syncthreads();
+    const int nparts = piece.nparts, slot = piece.slot;
+    uint16_t *out = static_cast<uint16_t *>(p.out) + ((int64_t)seq * p.num_q_heads + kvh * G) * D;
     for (int i = threadIdx.x; i < G * (D / 2); i += blockDim.x) {
         const int g = i / (D / 2), x0 = i % (D / 2) * 2;
         float M = -INFINITY;
@@ -466,20 +746,40 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(const D
             o1 += f * red[at * D + x0 + 1];
         }
         const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+        if (M == -INFINITY) M = 0.f;  // NaN scores alone: l = NaN counts
         if (nparts == 1) {
             *reinterpret_cast<uint32_t *>(out + g * D + x0) = narrow2<BF16>(o0 * inv, o1 * inv);
         } else {
-            const int64_t row = part_row(p, seq, kvh * G + g, chunk);
+            const int64_t row =
+                p.balanced ? (int64_t)slot * G + g : part_row(p, seq, kvh * G + g, slot);
+            const int64_t ml = p.balanced ? (int64_t)slot * kInt4MaxG + g : row;
             if (x0 == 0) {
-                p.part_m[row] = M == -INFINITY ? 0.f : M;  // NaN scores alone: l = NaN counts
-                p.part_l[row] = lsum;
+                p.part_m[ml] = M;
+                p.part_l[ml] = lsum;
             }
             *reinterpret_cast<float2 *>(p.part_o + row * D + x0) = make_float2(o0 * inv, o1 * inv);
         }
     }
-    if (nparts > 1 && p.counters != nullptr)
-        finish_item<BF16, D>(p, seq, kvh, nparts, chunk, nparts, false,
-                             reinterpret_cast<float *>(smem), Int4Shape<D>::SMEM_BYTES);
+    if (!p.balanced) break;
+    // the next piece's copies write where this one's sums stand
+    __syncthreads();
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }  // pieces
+    if (!p.balanced) {
+        pdl_trigger();
+        if (piece.nparts > 1 && p.counters != nullptr)
+            finish_item<BF16, D>(p, piece.seq, piece.kvh, piece.nparts, piece.slot, piece.nparts, false,
+                                 reinterpret_cast<float *>(smem), S::BARS);
+        return;
+    }
+    // every sequence's length is reported on by one CTA, which also writes the
+    // rows of those without tokens
+    for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
+        if (item_len(p, s, threadIdx.x == 0) > 0) continue;
+        uint32_t *row = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) +
+                                                     (int64_t)s * p.num_q_heads * D);
+        for (int i = threadIdx.x; i < p.num_q_heads * (D / 2); i += blockDim.x) row[i] = 0;
+    }
 }
 
 using Int4Kernel = void (*)(const DecodeParams);
@@ -499,6 +799,18 @@ static Int4Kernel pick_int4(bool bf16, int D, int block_size, int group, int *sm
     return bf16 ? int4_variant<true, 128>(block_size, h4) : int4_variant<false, 128>(block_size, h4);
 }
 
+using Int4Merge = void (*)(const DecodeParams, int);
+
+template <bool BF16, int D>
+static Int4Merge merge_variant(bool few) {
+    return few ? int4_merge_kernel<BF16, D, true> : int4_merge_kernel<BF16, D, false>;
+}
+
+static Int4Merge pick_merge(bool bf16, int D, bool few) {
+    if (D == 64) return bf16 ? merge_variant<true, 64>(few) : merge_variant<false, 64>(few);
+    return bf16 ? merge_variant<true, 128>(few) : merge_variant<false, 128>(few);
+}
+
 int int4_ctas_per_sm(bool bf16, int head_dim, int block_size, int group) {
     int smem = 0, n = 0;
     Int4Kernel k = pick_int4(bf16, head_dim, block_size, group, &smem);
@@ -508,6 +820,25 @@ int int4_ctas_per_sm(bool bf16, int head_dim, int block_size, int group) {
     return n > 0 ? n : 1;
 }
 
+// CTAs of a balanced launch: one wave, or as many as there can be shares; 0
+// where the batch is not for balanced ranges.
+int int4_balanced_ctas(bool bf16, int head_dim, int block_size, int group, int num_seqs,
+                       int num_kv_heads, int max_seq_len) {
+    const int64_t units =
+        (int64_t)num_seqs * num_kv_heads * (((int64_t)max_seq_len + kInt4Unit - 1) / kInt4Unit);
+    if (num_seqs > kInt4BalancedSeqs || units >= (1 << 30)) return 0;
+    const int64_t shares = (units + kInt4MinShare - 1) / kInt4MinShare;
+    const int64_t slots =
+        (int64_t)sm_count() * int4_ctas_per_sm(bf16, head_dim, block_size, group);
+    const int64_t n = shares < slots ? shares : slots;
+    return n < 1 ? 1 : (int)n;
+}
+
+// Whether bounds can cut a head: not when every head is shorter than two slacks.
+bool int4_balanced_cuts(int max_seq_len) {
+    return (max_seq_len + kInt4Unit - 1) / kInt4Unit > 2 * kInt4MinSlack + 1;
+}
+
 pa_status launch_decode_int4(const DecodeParams &prm, bool bf16, int head_dim, int num_partitions,
                              int num_kv_heads, int num_seqs, cudaStream_t stream) {
     if (num_seqs == 0) return PA_OK;
@@ -515,6 +846,24 @@ pa_status launch_decode_int4(const DecodeParams &prm, bool bf16, int head_dim, i
     Int4Kernel k = pick_int4(bf16, head_dim, prm.block_size, prm.group, &smem);
     if (!ensure_smem_attr(reinterpret_cast<const void *>(k), smem)) return PA_ERR_CUDA;
     DecodeParams p = prm;
+    if (p.balanced) {
+        p.compact = 0;
+        if (launch_pdl(k, dim3((unsigned)num_partitions), dim3(32 * kInt4Warps), (size_t)smem, stream,
+                       p) != cudaSuccess)
+            return PA_ERR_CUDA;
+        if (p.part_o && num_partitions > 1) {
+            // a head cut into 8 partials or more on average: a block a query head
+            const int64_t heads = (int64_t)num_seqs * num_kv_heads;
+            const bool few = 8 * heads <= num_partitions;
+            const dim3 grid = few ? dim3((unsigned)heads, (unsigned)p.group)
+                                  : dim3((unsigned)num_partitions - 1);
+            if (launch_pdl(pick_merge(bf16, head_dim, few), grid,
+                           dim3(few ? kInt4MergeHeads : kInt4MergeBounds), 0, stream, p,
+                           num_partitions) != cudaSuccess)
+                return PA_ERR_CUDA;
+        }
+        return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    }
     if (p.compact) p.compact = 2;  // full chunks first, the short last ones at the end
     const dim3 grid = decode_grid(p, num_partitions, num_kv_heads, num_seqs);
     if (launch_pdl(k, grid, dim3(32 * kInt4Warps), (size_t)smem, stream, p) != cudaSuccess)

@@ -9,6 +9,7 @@ import os
 from . import build as _build
 
 PA_OK = 0
+PA_ERR_INVALID = 1
 STATUS = {
     0: "PA_OK",
     1: "PA_ERR_INVALID",

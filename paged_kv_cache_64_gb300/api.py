@@ -299,22 +299,29 @@ def decode_fp8(out, q, k_pool, v_pool, block_tables, seq_lens, max_seq_len, scal
     return workspace
 
 
-def _one_device(first, **others):
-    """Index of the device of `first`; every other tensor given must lie there."""
-    dev = first.get_device()
-    for name, t in others.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} must be on the device of the other tensors (cuda:{dev})")
+def _addr(t, name, dev, dtype=None):
+    """Address of a dense tensor on device `dev` (its index), checked."""
+    if t.get_device() != dev or not t.is_contiguous() or (dtype is not None and t.dtype is not dtype):
+        _cuda(t, name, dtype)  # says what is wrong, or:
+        raise ValueError(f"{name} must be on the device of the other tensors (cuda:{dev})")
+    return t.data_ptr()
+
+
+def _device_of(t, name):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
     return dev
 
 
 def _on_device(dev, stream, fn, *args):
-    """fn(*args, stream) with `dev` current (stream None: its current stream;
-    False: fn takes none)."""
-    if dev == torch.cuda.current_device():
-        return fn(*args) if stream is False else fn(*args, _stream_handle(stream))
-    with torch.cuda.device(dev):
-        return fn(*args) if stream is False else fn(*args, _stream_handle(stream))
+    """fn(*args, stream handle) with `dev` current; stream None: its current
+    stream."""
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return _on_device(dev, stream, fn, *args)
+    return fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
+              else stream.cuda_stream)
 
 
 def int4_pool_shape(num_blocks, num_kv_heads, block_size, head_dim):
@@ -356,15 +363,14 @@ def cache_write_int4(k_new, v_new, slot_mapping, k_pool, v_pool, k_out=None, v_o
     for t in (k_out, v_out):
         if t is not None and (t.shape != k_new.shape or t.dtype != k_new.dtype):
             raise ValueError("k_out and v_out must be like k_new")
-    null = ctypes.c_void_p(0)
+    dt = _dt(k_new)
+    dev = _device_of(k_new, "k_new")
     rc = _on_device(
-        _one_device(k_new, v_new=v_new, slot_mapping=slot_mapping, k_pool=k_pool, v_pool=v_pool,
-                    k_out=k_out, v_out=v_out),
-        stream, _lib.load().pa_cache_write_int4, _cuda(k_new, "k_new"), _cuda(v_new, "v_new"),
-        _cuda(slot_mapping, "slot_mapping", torch.int64), T, _cuda(k_pool, "k_pool"),
-        _cuda(v_pool, "v_pool"), nb, hkv, d, bs,
-        null if k_out is None else _cuda(k_out, "k_out"),
-        null if v_out is None else _cuda(v_out, "v_out"), _dt(k_new))
+        dev, stream, _lib.load().pa_cache_write_int4, _addr(k_new, "k_new", dev),
+        _addr(v_new, "v_new", dev), _addr(slot_mapping, "slot_mapping", dev, torch.int64), T,
+        _addr(k_pool, "k_pool", dev), _addr(v_pool, "v_pool", dev), nb, hkv, d, bs,
+        None if k_out is None else _addr(k_out, "k_out", dev),
+        None if v_out is None else _addr(v_out, "v_out", dev), dt)
     _lib.check("pa_cache_write_int4", rc)
 
 
@@ -377,11 +383,12 @@ def cache_read_int4(k_out, v_out, slot_mapping, k_pool, v_pool, stream=None):
     nb, bs = _int4_pools(k_pool, v_pool, hkv, d)
     if slot_mapping.shape != (T,):
         raise ValueError("slot_mapping must be [T]")
+    dt = _dt(k_out)
+    dev = _device_of(k_out, "k_out")
     rc = _on_device(
-        _one_device(k_out, v_out=v_out, slot_mapping=slot_mapping, k_pool=k_pool, v_pool=v_pool),
-        stream, _lib.load().pa_cache_read_int4, _cuda(k_out, "k_out"), _cuda(v_out, "v_out"),
-        _cuda(slot_mapping, "slot_mapping", torch.int64), T, _cuda(k_pool, "k_pool"),
-        _cuda(v_pool, "v_pool"), nb, hkv, d, bs, _dt(k_out))
+        dev, stream, _lib.load().pa_cache_read_int4, _addr(k_out, "k_out", dev),
+        _addr(v_out, "v_out", dev), _addr(slot_mapping, "slot_mapping", dev, torch.int64), T,
+        _addr(k_pool, "k_pool", dev), _addr(v_pool, "v_pool", dev), nb, hkv, d, bs, dt)
     _lib.check("pa_cache_read_int4", rc)
 
 
@@ -408,37 +415,45 @@ def decode_int4(out, q, k_pool, v_pool, block_tables, seq_lens, max_seq_len, sca
     if block_tables.dim() != 2 or block_tables.shape[0] != S or seq_lens.shape != (S,):
         raise ValueError("block_tables must be [S, max_blocks], seq_lens [S]")
     dt = _dt(q)
-    dev = _one_device(q, out=out, k_pool=k_pool, v_pool=v_pool, block_tables=block_tables,
-                      seq_lens=seq_lens, workspace=workspace)
+    dev = _device_of(q, "q")
     lib = _lib.load()
-    args = (_cuda(out, "out"), _cuda(q, "q"), _cuda(k_pool, "k_pool"), _cuda(v_pool, "v_pool"), nb,
-            _cuda(block_tables, "block_tables", torch.int32), block_tables.shape[1],
-            _cuda(seq_lens, "seq_lens", torch.int32), int(max_seq_len), S, hq, hkv, d, bs,
-            float(scale), int(partition_tokens))
-    need = _on_device(dev, False, lib.pa_decode_int4_workspace_size, S, hq, hkv, d, bs,
-                      int(max_seq_len), int(partition_tokens), dt)
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = alloc_workspace(need, q.device)
-        if stream is not None:
-            workspace.record_stream(stream)
-    ws = _cuda(workspace, "workspace") if workspace is not None else ctypes.c_void_p(0)
-    wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _lib.check("pa_decode_int4", _on_device(dev, stream, lib.pa_decode_int4, *args, ws, wbytes, dt))
+    args = (_addr(out, "out", dev), _addr(q, "q", dev), _addr(k_pool, "k_pool", dev),
+            _addr(v_pool, "v_pool", dev), nb, _addr(block_tables, "block_tables", dev, torch.int32),
+            block_tables.shape[1], _addr(seq_lens, "seq_lens", dev, torch.int32), int(max_seq_len), S,
+            hq, hkv, d, bs, float(scale), int(partition_tokens))
+
+    def run(ws):
+        if ws is None:
+            return _on_device(dev, stream, lib.pa_decode_int4, *args, None, 0, dt)
+        return _on_device(dev, stream, lib.pa_decode_int4, *args, _addr(ws, "workspace", dev),
+                          ws.nbytes, dt)
+
+    rc = run(workspace)
+    if rc == _lib.PA_ERR_INVALID:  # perhaps for want of a workspace: nothing was launched
+        with torch.cuda.device(dev):
+            need = int4_workspace_size(S, hq, hkv, d, bs, int(max_seq_len), int(partition_tokens),
+                                       q.dtype)
+        if need and (workspace is None or workspace.nbytes < need):
+            workspace = alloc_workspace(need, q.device)
+            if stream is not None:
+                workspace.record_stream(stream)
+            rc = run(workspace)
+    _lib.check("pa_decode_int4", rc)
     return workspace
 
 
-def _token_rows(t, name, T, d):
+def _token_rows(t, name, dev, T, heads, d):
     """(address, elements from a token to the next) of t [T, heads, d] whose
     heads are dense."""
-    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != d:
-        raise ValueError(f"{name} must be [{T}, heads, {d}], got {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    own = t.shape[1] * d
-    step = t.stride(0) if T > 1 else own
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d) or step < own:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the others (cuda:{dev})")
+    own = heads * d
+    step, head, one = t.stride()
+    if T <= 1:
+        step = own
+    if one != 1 or (heads > 1 and head != d) or step < own:
         raise ValueError(f"{name}: each token's heads must be dense and apart from the next's")
-    return ctypes.c_void_p(t.data_ptr()), step
+    return t.data_ptr(), step
 
 
 def qk_norm_rope(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, positions, slot_mapping, k_pool,
@@ -454,6 +469,8 @@ def qk_norm_rope(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, positions, sl
         raise ValueError("q and q_out must be [T, Hq, d], k and v [T, Hkv, d]")
     T, hq, d = q.shape
     hkv = k.shape[1]
+    if k.shape[0] != T or k.shape[2] != d:
+        raise ValueError("q and q_out must be [T, Hq, d], k and v [T, Hkv, d]")
     dt = q.dtype
     if not (dt == k.dtype == v.dtype == q_out.dtype == q_weight.dtype == k_weight.dtype):
         raise TypeError("q, q_out, k, v and the weights must have one type")
@@ -479,21 +496,19 @@ def qk_norm_rope(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, positions, sl
             fmt = _lib.PA_KV_16BIT
         else:
             raise TypeError("pools must have q's type or be uint8 codes")
-    qo, qo_step = _token_rows(q_out, "q_out", T, d)
-    qp, q_step = _token_rows(q, "q", T, d)
-    kp, k_step = _token_rows(k, "k", T, d)
-    vp, v_step = _token_rows(v, "v", T, d)
-    cs = _cuda(cos_sin, "cos_sin", torch.float32, ndim=2)
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [positions, rotary_dim]")
+    code = _dt(q)
+    dev = _device_of(q, "q")
     rc = _on_device(
-        _one_device(q, q_out=q_out, k=k, v=v, q_weight=q_weight, k_weight=k_weight,
-                    cos_sin=cos_sin, positions=positions, slot_mapping=slot_mapping,
-                    k_pool=k_pool, v_pool=v_pool),
-        stream, _lib.load().pa_qk_norm_rope, qo, qo_step, qp, q_step, kp, k_step, vp, v_step,
-        _cuda(q_weight, "q_weight"), _cuda(k_weight, "k_weight"), float(eps), cs,
+        dev, stream, _lib.load().pa_qk_norm_rope, *_token_rows(q_out, "q_out", dev, T, hq, d),
+        *_token_rows(q, "q", dev, T, hq, d), *_token_rows(k, "k", dev, T, hkv, d),
+        *_token_rows(v, "v", dev, T, hkv, d), _addr(q_weight, "q_weight", dev),
+        _addr(k_weight, "k_weight", dev), float(eps), _addr(cos_sin, "cos_sin", dev, torch.float32),
         cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)),
-        _cuda(positions, "positions", torch.int64),
-        _cuda(slot_mapping, "slot_mapping", torch.int64), T, _cuda(k_pool, "k_pool"),
-        _cuda(v_pool, "v_pool"), nb, hq, hkv, d, bs, fmt, ks, vs, _dt(q))
+        _addr(positions, "positions", dev, torch.int64),
+        _addr(slot_mapping, "slot_mapping", dev, torch.int64), T, _addr(k_pool, "k_pool", dev),
+        _addr(v_pool, "v_pool", dev), nb, hq, hkv, d, bs, fmt, ks, vs, code)
     _lib.check("pa_qk_norm_rope", rc)
 
 

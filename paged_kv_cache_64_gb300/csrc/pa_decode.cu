@@ -1224,15 +1224,16 @@ size_t pa_decode_int4_workspace_size(int num_seqs, int num_q_heads, int num_kv_h
                                      int block_size, int max_seq_len, int partition_tokens,
                                      pa_dtype dtype) {
     ResolvedDecode r;
+    Int4Balance b;
+    if (partition_tokens == 0 &&
+        resolve(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len, -1, dtype, &r,
+                false, true, true) == PA_OK &&
+        int4_balance(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len, dtype,
+                     &b))
+        return b.cuts ? b.ws.bytes : 0;
     if (resolve(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len,
                 partition_tokens, dtype, &r, false, true, true) != PA_OK)
         return 0;
-    if (partition_tokens == 0) {
-        Int4Balance b;
-        if (int4_balance(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len,
-                         dtype, &b))
-            return b.cuts ? b.ws.bytes : 0;
-    }
     if (r.P <= 0) return 0;
     return workspace_layout(num_seqs, num_q_heads, head_dim, r.NP, num_kv_heads).bytes;
 }

@@ -31,6 +31,7 @@
 // ring of stages filled by bulk copies of whole records, its own running
 // maximum and sums; the four warps merge at the end through shared memory.
 #include <cstdint>
+#include <mutex>
 
 #include "pa_decode.cuh"
 #include "pa_int4.cuh"
@@ -811,13 +812,20 @@ static Int4Merge pick_merge(bool bf16, int D, bool few) {
     return bf16 ? merge_variant<true, 128>(few) : merge_variant<false, 128>(few);
 }
 
+// Resident CTAs per SM; asked of the runtime once per variant and device.
 int int4_ctas_per_sm(bool bf16, int head_dim, int block_size, int group) {
-    int smem = 0, n = 0;
+    static std::mutex mu;
+    static int known[128][16] = {};
+    int smem = 0, n = 0, dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 1;
+    int &slot = known[dev][8 * bf16 + 4 * (head_dim == 64) + 2 * (block_size == 32) + (group > 4)];
+    std::lock_guard<std::mutex> lock(mu);
+    if (slot > 0) return slot;
     Int4Kernel k = pick_int4(bf16, head_dim, block_size, group, &smem);
     if (!ensure_smem_attr(reinterpret_cast<const void *>(k), smem)) return 1;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, 32 * kInt4Warps, smem) != cudaSuccess)
         return 1;
-    return n > 0 ? n : 1;
+    return slot = n > 0 ? n : 1;
 }
 
 // CTAs of a balanced launch: one wave, or as many as there can be shares; 0

@@ -1,12 +1,13 @@
 // pa_cache_write_int4 and pa_cache_read_int4: rows into and out of paged
 // 4-bit pools (see pa_int4.cuh for the format).
 //
-// A row of D values is D/8 consecutive lanes, 8 elements (16 bytes of 16-bit
-// values, 4 bytes of codes) a lane, so a warp reads and writes whole rows.
+// A row of D values is D/16 consecutive lanes, 16 elements (32 bytes of 16-bit
+// values, 8 bytes of codes) a lane, so a warp reads and writes whole rows.
 // Bound by HBM: 2 bytes an element on the 16-bit side, 0.53 (D = 128) or 0.56
 // (D = 64) in the pool.
 #include <cstdint>
 
+#include "pa_decode.cuh"
 #include "pa_int4.cuh"
 #include "pa_internal.h"
 
@@ -24,57 +25,81 @@ struct Int4IoParams {
     int *err;
 };
 
-// Byte offset of slot `slot`'s codes in the pool and of its (s, m) pair from
-// the start of its record.
-template <int D>
-__device__ __forceinline__ int64_t int4_record(const Int4IoParams &p, int64_t slot, int head,
-                                               int *off) {
-    const int64_t blk = slot >> p.log2_block;
-    *off = (int)(slot & ((1 << p.log2_block) - 1));
-    return (blk * p.num_kv_heads + head) * (int64_t)int4_record_bytes<D>(1 << p.log2_block);
-}
-
 constexpr int kInt4Threads = 256;
+constexpr int kInt4Unroll = 2;  // rows a lane has in flight
 
 // blockIdx.y: 0 K, 1 V.  READ: pool -> values; otherwise values -> pool, and
 // the stored values out when dst is given.
 template <bool BF16, int D, bool READ>
 __global__ void __launch_bounds__(kInt4Threads) int4_rows_kernel(const Int4IoParams p) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // programmatic dependent launch
-    constexpr int LANES = D / 8, ROWS = kInt4Threads / LANES;
+    pdl_wait();
+    constexpr int LANES = D / 16, ROWS = kInt4Threads / LANES, U = kInt4Unroll;
     const int which = blockIdx.y, c = threadIdx.x % LANES;
-    for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < p.rows; r0 += (int64_t)gridDim.x * ROWS) {
-        const int64_t row = r0 + threadIdx.x / LANES;
-        int64_t slot = -1;
-        int head = 0;
-        if (row < p.rows) {
-            const int t = (int)row / p.num_kv_heads;
-            head = (int)row - t * p.num_kv_heads;
-            slot = p.slots[t];
-            if (slot >= p.num_slots) {
-                if (c == 0) record_error(p.err, PA_ERR_BAD_INDEX);
-                slot = -1;
-            }
+    const uint4 *src = which ? p.src[1] : p.src[0];
+    uint4 *dst = which ? p.dst[1] : p.dst[0];
+    uint8_t *pool = which ? p.pool[1] : p.pool[0];
+    const int block = 1 << p.log2_block, record = int4_record_bytes<D>(block);
+    for (int64_t r0 = (int64_t)blockIdx.x * (ROWS * U); r0 < p.rows;
+         r0 += (int64_t)gridDim.x * (ROWS * U)) {
+        int64_t slot[U];
+        int row[U];
+        uint8_t *codes[U], *pair[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = r0 + u * ROWS + threadIdx.x / LANES;
+            row[u] = r < p.rows ? (int)r : -1;
+            slot[u] = row[u] >= 0 ? p.slots[row[u] / p.num_kv_heads] : -1;
         }
-        int off = 0;
-        uint8_t *rec = nullptr;
-        if (slot >= 0) rec = p.pool[which] + int4_record<D>(p, slot, head, &off);
-        const int64_t piece = row * LANES + c;
-        Int4Row q;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (slot[u] >= p.num_slots) {
+                if (c == 0) record_error(p.err, PA_ERR_BAD_INDEX);
+                slot[u] = -1;
+            }
+            const int off = (int)(slot[u] & (block - 1));
+            uint8_t *rec = pool + ((slot[u] >> p.log2_block) * p.num_kv_heads +
+                                            row[u] % p.num_kv_heads) * record;
+            codes[u] = rec + off * (D / 2) + c * 8;
+            pair[u] = rec + block * (D / 2) + off * 4;
+        }
         if constexpr (READ) {
-            if (slot < 0) continue;
-            q.codes = *reinterpret_cast<const uint32_t *>(rec + off * (D / 2) + c * 4);
-            q.params = *reinterpret_cast<const uint32_t *>(rec + (D / 2 << p.log2_block) + off * 4);
-            p.dst[which][piece] = read8_int4<BF16>(q.codes, q.params);
+            uint2 q[U];
+            uint32_t sm[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (slot[u] < 0) continue;
+                q[u] = *reinterpret_cast<const uint2 *>(codes[u]);
+                sm[u] = *reinterpret_cast<const uint32_t *>(pair[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (slot[u] < 0) continue;
+                uint4 *to = dst + (int64_t)row[u] * (D / 8) + 2 * c;
+                to[0] = read8_int4<BF16>(q[u].x, sm[u]);
+                to[1] = read8_int4<BF16>(q[u].y, sm[u]);
+            }
         } else {
-            float x[8];
-            widen8<BF16>(slot >= 0 ? p.src[which][piece] : make_uint4(0, 0, 0, 0), x);
-            q = quantise_row_int4<BF16, LANES>(x);
-            if (slot < 0) continue;  // after the row's shuffles
-            *reinterpret_cast<uint32_t *>(rec + off * (D / 2) + c * 4) = q.codes;
-            if (c == 0)
-                *reinterpret_cast<uint32_t *>(rec + (D / 2 << p.log2_block) + off * 4) = q.params;
-            if (p.dst[which]) p.dst[which][piece] = read8_int4<BF16>(q.codes, q.params);
+            uint4 raw[U][2];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
+                if (slot[u] < 0) continue;
+                const uint4 *from = src + (int64_t)row[u] * (D / 8) + 2 * c;
+                raw[u][0] = from[0];
+                raw[u][1] = from[1];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const Int4Row<2> q = quantise_row_int4<BF16, LANES, 2>(raw[u]);
+                if (slot[u] < 0) continue;  // after the row's shuffles
+                *reinterpret_cast<uint2 *>(codes[u]) = make_uint2(q.codes[0], q.codes[1]);
+                if (c == 0) *reinterpret_cast<uint32_t *>(pair[u]) = q.params;
+                if (dst) {
+                    uint4 *to = dst + (int64_t)row[u] * (D / 8) + 2 * c;
+                    to[0] = read8_int4<BF16>(q.codes[0], q.params);
+                    to[1] = read8_int4<BF16>(q.codes[1], q.params);
+                }
+            }
         }
     }
 }
@@ -100,7 +125,7 @@ static pa_status int4_rows(bool read, Int4IoParams p, int num_tokens, const void
     p.rows = num_tokens * num_kv_heads;
     p.num_kv_heads = num_kv_heads;
     p.log2_block = block_size == 16 ? 4 : 5;
-    const int rows_per_block = kInt4Threads / (head_dim / 8);
+    const int rows_per_block = kInt4Threads / (head_dim / 16) * kInt4Unroll;
     const int64_t blocks = ((int64_t)p.rows + rows_per_block - 1) / rows_per_block;
     const int64_t cap = 16ll * (sm_count() > 0 ? sm_count() : 152);
     const dim3 grid((unsigned)(blocks < cap ? blocks : cap), 2);
@@ -111,7 +136,8 @@ static pa_status int4_rows(bool read, Int4IoParams p, int num_tokens, const void
     PA_CASE(true, 64, false) PA_CASE(true, 64, true) PA_CASE(true, 128, false)
     PA_CASE(true, 128, true)
 #undef PA_CASE
-    kern<<<grid, kInt4Threads, 0, as_stream(stream)>>>(p);
+    if (launch_pdl(kern, grid, dim3(kInt4Threads), 0, as_stream(stream), p) != cudaSuccess)
+        return PA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -40,13 +40,36 @@ __device__ __forceinline__ void widen8(uint4 v, float *x) {
     }
 }
 
+// The smaller (larger) of two pairs of 16-bit values, NaN if either is.
+template <bool BF16>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (BF16)
+        asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (BF16)
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// A row's share of one lane: W words of 8 codes, and the row's scale and
+// minimum as 16-bit values (s in the low half).
+template <int W>
 struct Int4Row {
-    uint32_t codes;   // this lane's 8 codes, element e in bits [4e, 4e + 4)
-    uint32_t params;  // the row's s (low half) and m as 16-bit values
+    uint32_t codes[W];  // element e of word w in bits [4e, 4e + 4)
+    uint32_t params;
 };
 
-// Quantise a row held by LANES consecutive lanes (aligned to LANES), 8
-// elements x (exactly 16-bit values) a lane; every lane of the warp calls it.
+// Quantise a row held by LANES consecutive lanes (aligned to LANES), 8 W
+// elements raw (16-bit) a lane; every lane of the warp calls it.
 //
 // s is the smallest 16-bit value with 15 s >= span = fl(max - min): the
 // nearest one to span / 15, or the next one up (15 s is exact in fp32: 11 + 4
@@ -55,70 +78,86 @@ struct Int4Row {
 // Newton step with an exact FMA remainder), so a tie, which is a quotient
 // fp32 holds exactly, is met exactly, and adding 1.5 * 2^23 rounds it to
 // even.  A quotient next to a tie may round onto it; the remainder a - n s,
-// exact there, then passes s / 2 and the element is taken again with that
-// comparison.
-template <bool BF16, int LANES>
-__device__ __forceinline__ Int4Row quantise_row_int4(const float *x) {
-    float lo = x[0], hi = x[0];
-    bool fine = true;
+// exact there, then passes s / 2 and the lane's elements are taken again with
+// that comparison.
+template <bool BF16, int LANES, int W>
+__device__ __forceinline__ Int4Row<W> quantise_row_int4(const uint4 (&raw)[W]) {
+    // minimum and maximum on packed pairs; a lane's as (min, -max), so that one
+    // shuffle and one minimum a step reduce both
+    uint32_t mn = raw[0].x, mx = raw[0].x;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-        fine &= fabsf(x[i]) < INFINITY;
-    }
-    if (!fine) hi = INFINITY, lo = 0.f;
+    for (int w = 0; w < W; ++w) {
+        const uint32_t v[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
 #pragma unroll
-    for (int o = LANES / 2; o >= 1; o >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(kFullMask, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(kFullMask, hi, o));
+        for (int i = w == 0 ? 1 : 0; i < 4; ++i) {
+            mn = min2<BF16>(mn, v[i]);
+            mx = max2<BF16>(mx, v[i]);
+        }
     }
-    Int4Row r;
-    const float span = hi - lo;
-    if (!(span < INFINITY)) {  // the same in every lane of the row
-        r.codes = 0u;
+    mx ^= 0x80008000u;
+    uint32_t ends = min2<BF16>(__byte_perm(mn, mx, 0x5410), __byte_perm(mn, mx, 0x7632));
+#pragma unroll
+    for (int o = LANES / 2; o >= 1; o >>= 1)
+        ends = min2<BF16>(ends, __shfl_xor_sync(kFullMask, ends, o));
+    const float2 e = widen2<BF16>(ends);
+    const float lo = e.x + 0.f;  // -0 becomes +0
+    Int4Row<W> r;
+    const float span = (0.f - e.y) - lo;  // never -0
+    if (!(span < INFINITY)) {  // a NaN, an infinity or past fp32: the same in every lane of the row
+#pragma unroll
+        for (int w = 0; w < W; ++w) r.codes[w] = 0u;
         r.params = BF16 ? 0x7fc07fc0u : 0x7e007e00u;
         return r;
     }
-    lo += 0.f;  // -0 becomes +0
     uint32_t sb = bits16<BF16>(__fdiv_rn(span, 15.f));
     float s = from16<BF16>(sb);
     if (15.f * s < span) s = from16<BF16>(++sb);
     r.params = sb | (bits16<BF16>(lo) << 16);
-    if (span == 0.f) {
-        r.codes = 0u;
-        return r;
-    }
+    // (span = 0: s = 0, 1 / s infinite and every quotient NaN; redone below)
     constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: the sum's low bits are the integer
     const float h = 0.5f * s, inv = __frcp_rn(s);
-    const bool tiny = s < 0x1p-100f;      // 1 / s may pass fp32's range (bf16 only)
-    float off = 0.f;
-    uint32_t codes = 0u;
+    float off = s < 0x1p-100f ? INFINITY : 0.f;  // 1 / s may pass fp32's range (bf16 only)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float a = x[i] - lo;
-        float t = a * inv;
-        t = fmaf(fmaf(-t, s, a), inv, t);
-        const float u = t + kMagic;
-        off = fmaxf(off, fabsf(fmaf(kMagic - u, s, a)));
-        codes += (__float_as_uint(u) & 15u) << (4 * i);
+    for (int w = 0; w < W; ++w) {
+        float x[8];
+        widen8<BF16>(raw[w], x);
+        // sum of (kMagic's bits + n_i) 16^i, modulo 2^32
+        uint32_t codes = 0u;
+#pragma unroll
+        for (int i = 7; i >= 0; --i) {
+            const float a = x[i] - lo;
+            float t = a * inv;
+            t = fmaf(fmaf(-t, s, a), inv, t);
+            const float u = t + kMagic;
+            off = fmaxf(off, fabsf(fmaf(kMagic - u, s, a)));
+            codes = codes * 16u + __float_as_uint(u);
+        }
+        r.codes[w] = codes - 0x4b400000u * 0x11111111u;
     }
-    if (tiny || off > h) {
-        codes = 0u;
+    if (off > h) {
 #pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-            float a = 0.f;
+        for (int w = 0; w < W; ++w) {
+            uint4 v = raw[0];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (i == j) a = x[j] - lo;
-            float n = rintf(__fdiv_rn(a, s));
-            const float d = fmaf(-n, s, a);
-            if (d > h) n += 1.f;
-            if (d < -h) n -= 1.f;
-            codes |= (uint32_t)fminf(fmaxf(n, 0.f), 15.f) << (4 * i);
+            for (int j = 1; j < W; ++j)
+                if (w == j) v = raw[j];
+            const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+            uint32_t codes = 0u;
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t pair = i < 4 ? (i < 2 ? word[0] : word[1]) : (i < 6 ? word[2] : word[3]);
+                const float a = from16<BF16>(i & 1 ? pair >> 16 : pair & 0xffffu) - lo;
+                float n = s > 0.f ? rintf(__fdiv_rn(a, s)) : 0.f;
+                const float d = fmaf(-n, s, a);
+                if (d > h) n += 1.f;
+                if (d < -h) n -= 1.f;
+                codes |= (uint32_t)fminf(fmaxf(n, 0.f), 15.f) << (4 * i);
+            }
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                if (w == j) r.codes[j] = codes;
         }
     }
-    r.codes = codes;
     return r;
 }
 
@@ -127,21 +166,22 @@ __device__ __forceinline__ Int4Row quantise_row_int4(const float *x) {
 // value; NaN where s is NaN.
 template <bool BF16>
 __device__ __forceinline__ uint4 read8_int4(uint32_t codes, uint32_t params) {
-    const float top = BF16 ? 3.38953138925e38f : 65504.f;
-    const float s = from16<BF16>(params & 0xffffu), m = from16<BF16>(params >> 16);
-    uint32_t w[4];
+    constexpr float top = BF16 ? 3.38953138925e38f : 65504.f;
+    const float2 sm = widen2<BF16>(params);
+    const float s = sm.x, m = sm.y;
+    float y[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float v[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float n = (float)((codes >> (8 * i + 4 * j)) & 15u);
-            const float y = fmaf(s, n, m);
-            v[j] = fabsf(y) > top ? copysignf(top, y) : y;  // keeps NaN
-        }
-        w[i] = narrow2<BF16>(v[0], v[1]);
+    for (int i = 0; i < 8; ++i) {  // 0x4b000000 | n is 2^23 + n
+        const uint32_t n = i == 0 ? codes & 15u : (codes >> (4 * i)) & 15u;
+        y[i] = fmaf(s, __uint_as_float(0x4b000000u | n) - 8388608.f, m);
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    if (fabsf(m) > top || !(fmaf(s, 15.f, m) <= top)) {  // rare; keeps NaN
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (fabsf(y[i]) > top) y[i] = copysignf(top, y[i]);
+    }
+    return make_uint4(narrow2<BF16>(y[0], y[1]), narrow2<BF16>(y[2], y[3]),
+                      narrow2<BF16>(y[4], y[5]), narrow2<BF16>(y[6], y[7]));
 }
 
 }  // namespace pa

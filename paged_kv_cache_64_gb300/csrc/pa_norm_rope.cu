@@ -63,20 +63,28 @@ __global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(const NormR
     const int64_t blk = slot >> p.log2_block;
     const int off = (int)(slot & ((1 << p.log2_block) - 1));
 
-    // this lane's cosines and sines: of its 8 elements' angles (halves), or of
-    // its four pairs (interleaved)
+    // this lane's cosines and sines: of its 8 elements' angles (halves: the sine
+    // with the sign of the partner's term), or of its four pairs (interleaved);
+    // 1 and 0 where nothing turns
     const int half = p.rotary_dim >> 1, hc = p.rotary_dim >> 4;  // hc: lanes in a half
     const bool turns = c < 2 * hc;
     float cs[8], sn[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
     if (turns) {
         const float *row = p.cos_sin + pos * p.rotary_dim;
-        const int n4 = p.interleaved ? 1 : 2;
         const float *a = row + (p.interleaved ? 4 * c : 8 * (c < hc ? c : c - hc));
-        for (int i = 0; i < n4; ++i) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (i && p.interleaved) break;
             const float4 u = reinterpret_cast<const float4 *>(a)[i];
             const float4 w = reinterpret_cast<const float4 *>(a + half)[i];
             cs[4 * i] = u.x; cs[4 * i + 1] = u.y; cs[4 * i + 2] = u.z; cs[4 * i + 3] = u.w;
             sn[4 * i] = w.x; sn[4 * i + 1] = w.y; sn[4 * i + 2] = w.z; sn[4 * i + 3] = w.w;
+        }
+        if (!p.interleaved && c < hc) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sn[i] = -sn[i];
         }
     }
     // lane that holds the other element of a pair (itself where nothing turns)
@@ -85,15 +93,22 @@ __global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(const NormR
     const int nq = p.num_q_heads, nk = p.num_kv_heads, heads = nq + 2 * nk;
     const int first = blockIdx.y * p.rows_per_cta;
     const int last = min(first + p.rows_per_cta, heads);
+    auto kind_of = [&](int r) { return r < nq ? 0 : r < nq + nk ? 1 : 2; };
+    auto load = [&](int r) {
+        if (r >= last) return make_uint4(0, 0, 0, 0);
+        const int kind = kind_of(r), head = r - (kind > 0 ? nq : 0) - (kind > 1 ? nk : 0);
+        return reinterpret_cast<const uint4 *>(p.src[kind] + t * p.stride[kind] +
+                                               (int64_t)head * D)[c];
+    };
+    // two heads ahead in flight
+    uint4 next[2] = {load(first + g), load(first + GROUPS + g)};
     for (int r0 = first; r0 < last; r0 += GROUPS) {
         const int r = r0 + g;
         const bool live = r < last;
-        const int kind = r < nq ? 0 : r < nq + nk ? 1 : 2;
-        const int head = kind == 0 ? r : kind == 1 ? r - nq : r - nq - nk;
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (live)
-            raw = reinterpret_cast<const uint4 *>(p.src[kind] + t * p.stride[kind] +
-                                                  (int64_t)head * D)[c];
+        const int kind = kind_of(r), head = r - (kind > 0 ? nq : 0) - (kind > 1 ? nk : 0);
+        const uint4 raw = next[0];
+        next[0] = next[1];
+        next[1] = load(r + 2 * GROUPS);
         uint4 y16 = raw;
         if (__any_sync(kFullMask, live && kind < 2)) {
             float x[8], w[8];
@@ -112,17 +127,13 @@ __global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(const NormR
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float a = x[2 * i], b = x[2 * i + 1];
-                    z[2 * i] = turns ? a * cs[i] - b * sn[i] : a;
-                    z[2 * i + 1] = turns ? b * cs[i] + a * sn[i] : b;
+                    z[2 * i] = a * cs[i] - b * sn[i];
+                    z[2 * i + 1] = b * cs[i] + a * sn[i];
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float other = __shfl_sync(kFullMask, x[i], partner);
-                    z[i] = !turns   ? x[i]
-                           : c < hc ? x[i] * cs[i] - other * sn[i]
-                                    : x[i] * cs[i] + other * sn[i];
-                }
+                for (int i = 0; i < 8; ++i)
+                    z[i] = x[i] * cs[i] + __shfl_sync(kFullMask, x[i], partner) * sn[i];
             }
             if (kind < 2)
                 y16 = make_uint4(narrow2<BF16>(z[0], z[1]), narrow2<BF16>(z[2], z[3]),
@@ -143,12 +154,11 @@ __global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(const NormR
             }
         } else {
             if (__any_sync(kFullMask, store)) {
-                float x[8];
-                widen8<BF16>(y16, x);
-                const Int4Row q = quantise_row_int4<BF16, LANES>(x);
+                const uint4 row[1] = {y16};
+                const Int4Row<1> q = quantise_row_int4<BF16, LANES, 1>(row);
                 if (store) {
                     uint8_t *dst = pool + rec * int4_record_bytes<D>(1 << p.log2_block);
-                    *reinterpret_cast<uint32_t *>(dst + off * (D / 2) + c * 4) = q.codes;
+                    *reinterpret_cast<uint32_t *>(dst + off * (D / 2) + c * 4) = q.codes[0];
                     if (c == 0)
                         *reinterpret_cast<uint32_t *>(dst + ((D / 2) << p.log2_block) + off * 4) =
                             q.params;

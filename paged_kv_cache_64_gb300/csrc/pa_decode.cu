@@ -1071,26 +1071,31 @@ static pa_status decode_impl(void *out, const void *q, const void *k_new, const 
 }
 
 // Balanced ranges of pa_decode_int4 (automatic partitions): the launch's CTAs
-// and, where bounds can cut a head, the workspace: m, l [slot][8], O [slot][G]
-// [d] for two slots a CTA.
+// (those of the first wave) and the workspace: m, l [slot][8], O [slot][G][d] for
+// two slots a CTA.
 struct Int4Balance {
     int ctas;
-    bool cuts;
+    int wave;
     WorkspaceLayout ws;
 };
 static bool int4_balance(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                          int block_size, int max_seq_len, pa_dtype dtype, Int4Balance *b) {
     const int G = num_q_heads / num_kv_heads;
     b->ctas = int4_balanced_ctas(dtype == PA_BF16, head_dim, block_size, G, num_seqs, num_kv_heads,
-                                 max_seq_len);
+                                 max_seq_len, &b->wave);
     if (b->ctas <= 0) return false;
-    b->cuts = int4_balanced_cuts(max_seq_len);
     const size_t slots = 2 * (size_t)b->ctas;
     b->ws = {};
     b->ws.l_off = align256(slots * 8 * sizeof(float));
     b->ws.o_off = 2 * b->ws.l_off;
     b->ws.bytes = b->ws.o_off + align256(slots * G * head_dim * sizeof(float));
     return true;
+}
+
+// Partition size of the batches that balanced ranges are not for: single pass
+// for short heads, the other decodes' choice otherwise.
+static int int4_partition(int partition_tokens, int max_seq_len) {
+    return partition_tokens == 0 && max_seq_len <= kInt4SinglePass ? -1 : partition_tokens;
 }
 
 // Shared-prefix (cascade) decode: chunking of the prefix pass and the tail
@@ -1230,9 +1235,9 @@ size_t pa_decode_int4_workspace_size(int num_seqs, int num_q_heads, int num_kv_h
                 false, true, true) == PA_OK &&
         int4_balance(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len, dtype,
                      &b))
-        return b.cuts ? b.ws.bytes : 0;
+        return b.ws.bytes;
     if (resolve(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len,
-                partition_tokens, dtype, &r, false, true, true) != PA_OK)
+                int4_partition(partition_tokens, max_seq_len), dtype, &r, false, true, true) != PA_OK)
         return 0;
     if (r.P <= 0) return 0;
     return workspace_layout(num_seqs, num_q_heads, head_dim, r.NP, num_kv_heads).bytes;
@@ -1253,8 +1258,9 @@ pa_status pa_decode_int4(void *out, const void *q, const void *k_pool, const voi
                       &b))
         return decode_impl(out, q, nullptr, nullptr, nullptr, k_pool, v_pool, num_blocks,
                            block_tables, max_blocks_per_seq, seq_lens, max_seq_len, num_seqs,
-                           num_q_heads, num_kv_heads, head_dim, block_size, scale, partition_tokens,
-                           workspace, workspace_bytes, dtype, stream, nullptr, true);
+                           num_q_heads, num_kv_heads, head_dim, block_size, scale,
+                           int4_partition(partition_tokens, max_seq_len), workspace, workspace_bytes,
+                           dtype, stream, nullptr, true);
     if (num_seqs > 0 && (!out || !aligned16(out))) return PA_ERR_INVALID;
     DecodeParams prm;
     const pa_status st = fill_common(&prm, q, k_pool, v_pool, num_blocks, block_tables,
@@ -1262,16 +1268,13 @@ pa_status pa_decode_int4(void *out, const void *q, const void *k_pool, const voi
                                      num_q_heads, num_kv_heads, block_size, scale);
     if (st != PA_OK) return st;
     prm.out = out;
-    prm.balanced = 1;
-    if (b.cuts) {
-        if (!workspace || workspace_bytes < b.ws.bytes ||
-            (reinterpret_cast<uintptr_t>(workspace) & 255))
-            return PA_ERR_INVALID;
-        uint8_t *ws = static_cast<uint8_t *>(workspace);
-        prm.part_m = reinterpret_cast<float *>(ws + b.ws.m_off);
-        prm.part_l = reinterpret_cast<float *>(ws + b.ws.l_off);
-        prm.part_o = reinterpret_cast<float *>(ws + b.ws.o_off);
-    }
+    prm.balanced = b.wave;
+    if (!workspace || workspace_bytes < b.ws.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255))
+        return PA_ERR_INVALID;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    prm.part_m = reinterpret_cast<float *>(ws + b.ws.m_off);
+    prm.part_l = reinterpret_cast<float *>(ws + b.ws.l_off);
+    prm.part_o = reinterpret_cast<float *>(ws + b.ws.o_off);
     return launch_decode_int4(prm, dtype == PA_BF16, head_dim, b.ctas, num_kv_heads, num_seqs,
                               as_stream(stream));
 }

@@ -85,7 +85,8 @@ struct DecodeParams {
     float v_inv;
     float v_scale;
     // 4-bit pools: balanced ranges instead of chunks (pa_decode_int4.cu);
-    // part_m, part_l and part_o are then laid out by its slots.
+    // part_m, part_l and part_o are then laid out by its slots, and this is the
+    // number of CTAs in the first wave.
     int balanced;
 };
 
@@ -567,12 +568,13 @@ int fp8_ctas_per_sm(bool bf16, int head_dim, int group);
 pa_status launch_decode_fp8(const DecodeParams &prm, bool bf16, int head_dim, int num_partitions,
                             int num_kv_heads, int num_seqs, cudaStream_t stream);
 
+constexpr int kInt4SinglePass = 1024;  // 4-bit pools: longer heads may be cut
+
 // Decode over 4-bit pools (pa_decode_int4.cu); the pool pointers of prm are
 // those of the records.
 int int4_ctas_per_sm(bool bf16, int head_dim, int block_size, int group);
 int int4_balanced_ctas(bool bf16, int head_dim, int block_size, int group, int num_seqs,
-                       int num_kv_heads, int max_seq_len);
-bool int4_balanced_cuts(int max_seq_len);
+                       int num_kv_heads, int max_seq_len, int *wave);
 pa_status launch_decode_int4(const DecodeParams &prm, bool bf16, int head_dim, int num_partitions,
                              int num_kv_heads, int num_seqs, cudaStream_t stream);
 

@@ -86,15 +86,19 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) { return narrow
 
 // Balanced ranges (automatic partitions).  The batch's work is one line of
 // units of 128 positions, sequence by sequence and head by head; CTA c takes
-// the units from bound(c) to bound(c + 1), where bound(c) = c * share, moved to
-// the next head's border where that is at most `slack` units away, so that no
-// head is cut for a sliver.  Every CTA works the line out from the lengths (one
-// load and a scan), so shares are equal whatever the lengths are, in one wave.
-// The partials of heads that bounds cut are merged by a second kernel.
+// the units from bound(c) to bound(c + 1), moved to the next head's border where
+// that is at most `slack` units away, so that no head is cut for a sliver.  Every
+// CTA works the line out from the lengths (one load and a scan), whatever they
+// are.  A first wave of CTAs takes equal large shares; a second, of smaller
+// shares, is started as the first ends, which the SMs do not do together (equal
+// shares in one wave alone ended between 138 and 222 us).  The partials of heads
+// that bounds cut are merged by a second kernel.
 // A CTA's range: units [unit, end) of the line.  Its next unit is unit `at`
 // of the n units of head kvh of sequence seq.
 struct Int4Range {
-    int share, slack;
+    int wave;          // CTAs of the first wave
+    int share, small;  // units of a share in the first wave, in the second
+    int slack;
     int unit, end;
     int seq, kvh, at, n;
 };
@@ -109,27 +113,40 @@ struct Int4Piece {
 constexpr int kInt4Unit = kInt4Step * kInt4Warps;  // positions
 constexpr int kInt4MinShare = 4;                   // units: smaller shares cost more than they save
 constexpr int kInt4MinSlack = 2;
+// A second wave pays where its shares are still long next to a CTA's start (2 us
+// to its first copies): 256 sequences (115 units a slot) 236 -> 216 us with it,
+// 16 long ones (40 units) 94 -> 98.
+constexpr int kInt4SecondWave = 64;  // units a slot from which on there is one,
+constexpr int kInt4SecondPart = 5;   //   with a fifth of the work,
+constexpr int kInt4SecondCtas = 2;   //   in twice as many CTAs
 constexpr int kInt4BalancedSeqs = 1024;            // longer batches: a CTA an item, by the hardware
 
 __device__ __forceinline__ int int4_units(const DecodeParams &p, int seq) {
     return (item_len(p, seq, false) + kInt4Unit - 1) / kInt4Unit;
 }
 
+// The last bound at or before unit u of the line.
+__device__ __forceinline__ int int4_bound_before(const Int4Range &r, int u) {
+    const int large = r.wave * r.share;
+    return u < large ? u / r.share : r.wave + (u - large) / r.small;
+}
+
 // Pieces that bounds cut the range's present head into, and the first bound
 // inside it: those past its first slack units and before its last.
 __device__ __forceinline__ int int4_parts(const Int4Range &r, int *first) {
     const int a = r.unit - r.at, b = a + r.n;  // the head on the line
-    *first = (a + r.slack) / r.share + 1;
-    const int last = b - r.slack - 1 < 0 ? -1 : (b - r.slack - 1) / r.share;
+    *first = int4_bound_before(r, a + r.slack) + 1;
+    const int last = b <= r.slack ? -1 : int4_bound_before(r, b - r.slack - 1);
     return max(last - *first + 1, 0) + 1;
 }
 
-// The range of CTA `cta` of ncta, or (cta < 0) the place of head `head`
+// The range of CTA `cta` of ncta, `wave` of them in the first wave, or (cta < 0) the place of head `head`
 // (sequence head / Hkv), with n = 0 for one without positions.  Called by all T
 // threads of the block; ends synchronised.
 template <int T>
 __device__ __forceinline__ void int4_plan(const DecodeParams &p, int ncta, int cta, int head,
                                           Int4Range *range) {
+    const int wave = p.balanced;
     __shared__ int sums[T / 32];
     const int tid = threadIdx.x, lane = tid & 31;
     const int per = (p.num_seqs + T - 1) / T;
@@ -151,8 +168,13 @@ __device__ __forceinline__ void int4_plan(const DecodeParams &p, int ncta, int c
         all += sums[w];
     }
     const int H = p.num_kv_heads, total = all * H;
-    const int share = max((total + ncta - 1) / ncta, kInt4MinShare);
-    const int slack = max(share / 16, kInt4MinSlack);
+    // the second wave gets a part of the work if its shares are worth a CTA each
+    int share = max((total + wave - 1) / wave, kInt4MinShare), small = share;
+    if (ncta > wave && share >= kInt4SecondWave) {
+        share -= share / kInt4SecondPart;
+        small = max((total - wave * share + ncta - wave - 1) / (ncta - wave), kInt4MinShare);
+    }
+    const int slack = max(small / 8, kInt4MinSlack);
     if (cta < 0) {
         const int seq = head / H;
         if (seq >= s0 && seq < s1) {
@@ -167,7 +189,8 @@ __device__ __forceinline__ void int4_plan(const DecodeParams &p, int ncta, int c
     } else {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const int u = min((cta + b) * share, total);
+            const int c = cta + b;
+            const int u = min(c < wave ? c * share : wave * share + (c - wave) * small, total);
             if (u == total) {
                 if (tid == 0) {
                     if (b == 0) range->unit = total;
@@ -198,7 +221,9 @@ __device__ __forceinline__ void int4_plan(const DecodeParams &p, int ncta, int c
         }
     }
     if (tid == 0) {
+        range->wave = wave;
         range->share = share;
+        range->small = small;
         range->slack = slack;
     }
     __syncthreads();
@@ -256,11 +281,11 @@ __global__ void __launch_bounds__(HEADS ? kInt4MergeHeads : kInt4MergeBounds)
     const int item = threadIdx.x % ITEMS, row = threadIdx.x / ITEMS;
     // the decode kernel began after all work before it was done, so the lengths
     // are there
-    int4_plan<T>(p, ncta, HEADS ? -1 : blockIdx.x + 1, blockIdx.x, &range);
+    int4_plan<T>(p, ncta, HEADS ? -1 : (int)blockIdx.x + 1, (int)blockIdx.x, &range);
     int first = 0, n = 0;
     const bool mine = (HEADS ? range.n > 0 : range.unit < range.end && range.at > 0 &&
                                                  range.at < range.n) &&
-                      (n = int4_parts(range, &first)) > 1 && (HEADS || first == blockIdx.x + 1);
+                      (n = int4_parts(range, &first)) > 1 && (HEADS || first == (int)blockIdx.x + 1);
     pdl_wait();
     if (!mine) return;
     auto slot = [&](int k) { return k == 0 ? 2 * (first - 1) + 1 : 2 * (first - 1 + k); };
@@ -828,23 +853,23 @@ int int4_ctas_per_sm(bool bf16, int head_dim, int block_size, int group) {
     return slot = n > 0 ? n : 1;
 }
 
-// CTAs of a balanced launch: one wave, or as many as there can be shares; 0
-// where the batch is not for balanced ranges.
+// CTAs of a balanced launch, and those of its first wave (at most one a slot,
+// or as many as there can be shares); 0 where the batch is not for balanced
+// ranges: heads too short to be worth cutting (single pass is as fast up to 1024
+// positions, 13 against 14 us for 8 sequences; at 2048, 19 against 15), or more
+// sequences than a CTA should scan.
 int int4_balanced_ctas(bool bf16, int head_dim, int block_size, int group, int num_seqs,
-                       int num_kv_heads, int max_seq_len) {
+                       int num_kv_heads, int max_seq_len, int *wave) {
+    if (max_seq_len <= kInt4SinglePass) return 0;
     const int64_t units =
         (int64_t)num_seqs * num_kv_heads * (((int64_t)max_seq_len + kInt4Unit - 1) / kInt4Unit);
     if (num_seqs > kInt4BalancedSeqs || units >= (1 << 30)) return 0;
     const int64_t shares = (units + kInt4MinShare - 1) / kInt4MinShare;
     const int64_t slots =
         (int64_t)sm_count() * int4_ctas_per_sm(bf16, head_dim, block_size, group);
-    const int64_t n = shares < slots ? shares : slots;
-    return n < 1 ? 1 : (int)n;
-}
-
-// Whether bounds can cut a head: not when every head is shorter than two slacks.
-bool int4_balanced_cuts(int max_seq_len) {
-    return (max_seq_len + kInt4Unit - 1) / kInt4Unit > 2 * kInt4MinSlack + 1;
+    if (shares < slots) return *wave = shares < 1 ? 1 : (int)shares;
+    *wave = (int)slots;
+    return units >= slots * kInt4SecondWave ? (int)slots * (1 + kInt4SecondCtas) : (int)slots;
 }
 
 pa_status launch_decode_int4(const DecodeParams &prm, bool bf16, int head_dim, int num_partitions,

@@ -21,19 +21,25 @@ struct Int4IoParams {
     int64_t num_slots;
     int rows;             // tokens * KV heads
     int num_kv_heads;
+    // row / num_kv_heads = (row * magic) >> (32 + shift) for row < 2^31 (one
+    // head: magic 0)
+    uint32_t magic;
+    int shift;
     int log2_block;
     int *err;
 };
 
 constexpr int kInt4Threads = 256;
-constexpr int kInt4Unroll = 2;  // rows a lane has in flight
+// Rows a lane has in flight (reading: fewer registers a row).
+template <bool READ>
+constexpr int kInt4Unroll = READ ? 4 : 2;
 
 // blockIdx.y: 0 K, 1 V.  READ: pool -> values; otherwise values -> pool, and
 // the stored values out when dst is given.
 template <bool BF16, int D, bool READ>
 __global__ void __launch_bounds__(kInt4Threads) int4_rows_kernel(const Int4IoParams p) {
     pdl_wait();
-    constexpr int LANES = D / 16, ROWS = kInt4Threads / LANES, U = kInt4Unroll;
+    constexpr int LANES = D / 16, ROWS = kInt4Threads / LANES, U = kInt4Unroll<READ>;
     const int which = blockIdx.y, c = threadIdx.x % LANES;
     const uint4 *src = which ? p.src[1] : p.src[0];
     uint4 *dst = which ? p.dst[1] : p.dst[0];
@@ -42,63 +48,60 @@ __global__ void __launch_bounds__(kInt4Threads) int4_rows_kernel(const Int4IoPar
     for (int64_t r0 = (int64_t)blockIdx.x * (ROWS * U); r0 < p.rows;
          r0 += (int64_t)gridDim.x * (ROWS * U)) {
         int64_t slot[U];
-        int row[U];
-        uint8_t *codes[U], *pair[U];
+        int row[U], head[U];
+        uint4 raw[U][2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t r = r0 + u * ROWS + threadIdx.x / LANES;
             row[u] = r < p.rows ? (int)r : -1;
-            slot[u] = row[u] >= 0 ? p.slots[row[u] / p.num_kv_heads] : -1;
+            if (!READ) raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
+            slot[u] = -1;
+            if (row[u] < 0) continue;
+            const int t = p.magic ? (int)(__umulhi((uint32_t)row[u], p.magic) >> p.shift) : row[u];
+            head[u] = row[u] - t * p.num_kv_heads;
+            slot[u] = p.slots[t];
+            if (!READ) {  // also of skipped tokens: not to wait for the slot
+                const uint4 *from = src + (int64_t)row[u] * (D / 8) + 2 * c;
+                raw[u][0] = from[0];
+                raw[u][1] = from[1];
+            }
         }
+        uint2 q[U];
+        uint32_t sm[U];
+        uint8_t *codes[U], *pair[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (slot[u] >= p.num_slots) {
                 if (c == 0) record_error(p.err, PA_ERR_BAD_INDEX);
                 slot[u] = -1;
             }
-            const int off = (int)(slot[u] & (block - 1));
-            uint8_t *rec = pool + ((slot[u] >> p.log2_block) * p.num_kv_heads +
-                                            row[u] % p.num_kv_heads) * record;
+            if (slot[u] < 0) continue;
+            const int off = (int)slot[u] & (block - 1), blk = (int)(slot[u] >> p.log2_block);
+            uint8_t *rec = pool + ((int64_t)blk * p.num_kv_heads + head[u]) * record;
             codes[u] = rec + off * (D / 2) + c * 8;
             pair[u] = rec + block * (D / 2) + off * 4;
-        }
-        if constexpr (READ) {
-            uint2 q[U];
-            uint32_t sm[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (slot[u] < 0) continue;
+            if (READ) {
                 q[u] = *reinterpret_cast<const uint2 *>(codes[u]);
                 sm[u] = *reinterpret_cast<const uint32_t *>(pair[u]);
             }
+        }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < U; ++u) {
+            uint4 y[2];
+            if constexpr (READ) {
                 if (slot[u] < 0) continue;
-                uint4 *to = dst + (int64_t)row[u] * (D / 8) + 2 * c;
-                to[0] = read8_int4<BF16>(q[u].x, sm[u]);
-                to[1] = read8_int4<BF16>(q[u].y, sm[u]);
-            }
-        } else {
-            uint4 raw[U][2];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
-                if (slot[u] < 0) continue;
-                const uint4 *from = src + (int64_t)row[u] * (D / 8) + 2 * c;
-                raw[u][0] = from[0];
-                raw[u][1] = from[1];
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const Int4Row<2> q = quantise_row_int4<BF16, LANES, 2>(raw[u]);
+                y[0] = read8_int4<BF16>(q[u].x, sm[u]);
+                y[1] = read8_int4<BF16>(q[u].y, sm[u]);
+            } else {
+                const Int4Row<2> z = quantise_row_int4<BF16, LANES, 2, true>(raw[u], y);
                 if (slot[u] < 0) continue;  // after the row's shuffles
-                *reinterpret_cast<uint2 *>(codes[u]) = make_uint2(q.codes[0], q.codes[1]);
-                if (c == 0) *reinterpret_cast<uint32_t *>(pair[u]) = q.params;
-                if (dst) {
-                    uint4 *to = dst + (int64_t)row[u] * (D / 8) + 2 * c;
-                    to[0] = read8_int4<BF16>(q.codes[0], q.params);
-                    to[1] = read8_int4<BF16>(q.codes[1], q.params);
-                }
+                *reinterpret_cast<uint2 *>(codes[u]) = make_uint2(z.codes[0], z.codes[1]);
+                if (c == 0) *reinterpret_cast<uint32_t *>(pair[u]) = z.params;
+            }
+            if (READ || dst) {
+                uint4 *to = dst + (int64_t)row[u] * (D / 8) + 2 * c;
+                to[0] = y[0];
+                to[1] = y[1];
             }
         }
     }
@@ -124,10 +127,18 @@ static pa_status int4_rows(bool read, Int4IoParams p, int num_tokens, const void
     p.num_slots = (int64_t)num_blocks * block_size;
     p.rows = num_tokens * num_kv_heads;
     p.num_kv_heads = num_kv_heads;
+    if (num_kv_heads > 1) {
+        // l = ceil(log2 H), magic = ceil(2^(31 + l) / H) < 2^32: exact below 2^31
+        int l = 1;
+        while ((1 << l) < num_kv_heads) ++l;
+        p.magic = (uint32_t)(((1ull << (31 + l)) + num_kv_heads - 1) / num_kv_heads);
+        p.shift = l - 1;
+    }
     p.log2_block = block_size == 16 ? 4 : 5;
-    const int rows_per_block = kInt4Threads / (head_dim / 16) * kInt4Unroll;
+    const int rows_per_block = kInt4Threads / (head_dim / 16) *
+                               (read ? kInt4Unroll<true> : kInt4Unroll<false>);
     const int64_t blocks = ((int64_t)p.rows + rows_per_block - 1) / rows_per_block;
-    const int64_t cap = 16ll * (sm_count() > 0 ? sm_count() : 152);
+    const int64_t cap = 8ll * (sm_count() > 0 ? sm_count() : 152);
     const dim3 grid((unsigned)(blocks < cap ? blocks : cap), 2);
     auto kern = int4_rows_kernel<false, 64, false>;
 #define PA_CASE(BF, DD, RR) \

@@ -68,6 +68,29 @@ struct Int4Row {
     uint32_t params;
 };
 
+// The 8 values that codes with (s, m) stand for, as 16-bit values: fl(m + s n)
+// (s n is exact) rounded to nearest even, saturating at the largest finite
+// value; NaN where s is NaN.
+template <bool BF16>
+__device__ __forceinline__ uint4 read8_int4(uint32_t codes, uint32_t params) {
+    constexpr float top = BF16 ? 3.38953138925e38f : 65504.f;
+    const float2 sm = widen2<BF16>(params);
+    const float s = sm.x, m = sm.y;
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // 0x4b000000 | n is 2^23 + n
+        const uint32_t n = i == 0 ? codes & 15u : (codes >> (4 * i)) & 15u;
+        y[i] = fmaf(s, __uint_as_float(0x4b000000u | n) - 8388608.f, m);
+    }
+    if (fabsf(m) > top || !(fmaf(s, 15.f, m) <= top)) {  // rare; keeps NaN
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (fabsf(y[i]) > top) y[i] = copysignf(top, y[i]);
+    }
+    return make_uint4(narrow2<BF16>(y[0], y[1]), narrow2<BF16>(y[2], y[3]),
+                      narrow2<BF16>(y[4], y[5]), narrow2<BF16>(y[6], y[7]));
+}
+
 // Quantise a row held by LANES consecutive lanes (aligned to LANES), 8 W
 // elements raw (16-bit) a lane; every lane of the warp calls it.
 //
@@ -79,9 +102,10 @@ struct Int4Row {
 // fp32 holds exactly, is met exactly, and adding 1.5 * 2^23 rounds it to
 // even.  A quotient next to a tie may round onto it; the remainder a - n s,
 // exact there, then passes s / 2 and the lane's elements are taken again with
-// that comparison.
-template <bool BF16, int LANES, int W>
-__device__ __forceinline__ Int4Row<W> quantise_row_int4(const uint4 (&raw)[W]) {
+// that comparison.  With OUT, y receives the values the codes stand for, as
+// read8_int4 gives them.
+template <bool BF16, int LANES, int W, bool OUT>
+__device__ __forceinline__ Int4Row<W> quantise_row_int4(const uint4 (&raw)[W], uint4 *y) {
     // minimum and maximum on packed pairs; a lane's as (min, -max), so that one
     // shuffle and one minimum a step reduce both
     uint32_t mn = raw[0].x, mx = raw[0].x;
@@ -105,7 +129,10 @@ __device__ __forceinline__ Int4Row<W> quantise_row_int4(const uint4 (&raw)[W]) {
     const float span = (0.f - e.y) - lo;  // never -0
     if (!(span < INFINITY)) {  // a NaN, an infinity or past fp32: the same in every lane of the row
 #pragma unroll
-        for (int w = 0; w < W; ++w) r.codes[w] = 0u;
+        for (int w = 0; w < W; ++w) {
+            r.codes[w] = 0u;
+            if (OUT) y[w] = read8_int4<BF16>(0u, BF16 ? 0x7fc07fc0u : 0x7e007e00u);
+        }
         r.params = BF16 ? 0x7fc07fc0u : 0x7e007e00u;
         return r;
     }
@@ -117,24 +144,38 @@ __device__ __forceinline__ Int4Row<W> quantise_row_int4(const uint4 (&raw)[W]) {
     constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: the sum's low bits are the integer
     const float h = 0.5f * s, inv = __frcp_rn(s);
     float off = s < 0x1p-100f ? INFINITY : 0.f;  // 1 / s may pass fp32's range (bf16 only)
+    const float2 inv2 = make_float2(inv, inv), s2 = make_float2(s, s), lo2 = make_float2(lo, lo);
+    const float2 magic2 = make_float2(kMagic, kMagic);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-        float x[8];
-        widen8<BF16>(raw[w], x);
+        const uint32_t word[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+        uint32_t out[4];
         // sum of (kMagic's bits + n_i) 16^i, modulo 2^32
         uint32_t codes = 0u;
 #pragma unroll
-        for (int i = 7; i >= 0; --i) {
-            const float a = x[i] - lo;
-            float t = a * inv;
-            t = fmaf(fmaf(-t, s, a), inv, t);
-            const float u = t + kMagic;
-            off = fmaxf(off, fabsf(fmaf(kMagic - u, s, a)));
-            codes = codes * 16u + __float_as_uint(u);
+        for (int i = 3; i >= 0; --i) {
+            const float2 x = widen2<BF16>(word[i]);
+            const float2 a = __fadd2_rn(x, make_float2(-lo, -lo));
+            float2 q = __fmul2_rn(a, inv2);
+            q = __ffma2_rn(__ffma2_rn(make_float2(-q.x, -q.y), s2, a), inv2, q);
+            const float2 u = __fadd2_rn(q, magic2);
+            const float2 n = __fadd2_rn(u, make_float2(-kMagic, -kMagic));
+            const float2 d = __ffma2_rn(n, make_float2(-s, -s), a);
+            off = fmaxf(off, fmaxf(fabsf(d.x), fabsf(d.y)));
+            codes = codes * 16u + __float_as_uint(u.y);
+            codes = codes * 16u + __float_as_uint(u.x);
+            if (OUT) {
+                const float2 v = __ffma2_rn(n, s2, lo2);
+                out[i] = narrow2<BF16>(v.x, v.y);
+            }
         }
         r.codes[w] = codes - 0x4b400000u * 0x11111111u;
+        if (OUT) y[w] = make_uint4(out[0], out[1], out[2], out[3]);
     }
+    // values that could pass the largest finite one are taken again too
+    bool again = OUT && !(fmaf(s, 15.f, lo) <= (BF16 ? 3.38953138925e38f : 65504.f));
     if (off > h) {
+        again = true;
 #pragma unroll 1
         for (int w = 0; w < W; ++w) {
             uint4 v = raw[0];
@@ -158,30 +199,11 @@ __device__ __forceinline__ Int4Row<W> quantise_row_int4(const uint4 (&raw)[W]) {
                 if (w == j) r.codes[j] = codes;
         }
     }
+    if (OUT && again) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) y[w] = read8_int4<BF16>(r.codes[w], r.params);
+    }
     return r;
-}
-
-// The 8 values that codes with (s, m) stand for, as 16-bit values: fl(m + s n)
-// (s n is exact) rounded to nearest even, saturating at the largest finite
-// value; NaN where s is NaN.
-template <bool BF16>
-__device__ __forceinline__ uint4 read8_int4(uint32_t codes, uint32_t params) {
-    constexpr float top = BF16 ? 3.38953138925e38f : 65504.f;
-    const float2 sm = widen2<BF16>(params);
-    const float s = sm.x, m = sm.y;
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {  // 0x4b000000 | n is 2^23 + n
-        const uint32_t n = i == 0 ? codes & 15u : (codes >> (4 * i)) & 15u;
-        y[i] = fmaf(s, __uint_as_float(0x4b000000u | n) - 8388608.f, m);
-    }
-    if (fabsf(m) > top || !(fmaf(s, 15.f, m) <= top)) {  // rare; keeps NaN
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (fabsf(y[i]) > top) y[i] = copysignf(top, y[i]);
-    }
-    return make_uint4(narrow2<BF16>(y[0], y[1]), narrow2<BF16>(y[2], y[3]),
-                      narrow2<BF16>(y[4], y[5]), narrow2<BF16>(y[6], y[7]));
 }
 
 }  // namespace pa

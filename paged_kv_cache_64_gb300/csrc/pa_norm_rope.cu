@@ -3,13 +3,14 @@
 //
 //   y = x w / sqrt(mean x^2 + eps);  (a, b) -> (a c - b s, b c + a s)
 //
-// A head is D/8 consecutive lanes, 8 elements (16 bytes) a lane; the sum of
-// squares is a shuffle sum over them.  Rotated pairs that lie D apart sit in
-// lanes rotary_dim / 16 apart and change places by shuffles; interleaved pairs
-// sit in one lane.  A CTA works on one token, so the position's cosines and
-// sines are loaded once a lane and kept for all its heads.  Bound by HBM:
-// every element is read and written once (E4M3 and 4-bit pools: 1 and 0.53
-// bytes instead of 2 on the way out).
+// A head is D/16 consecutive lanes; lane c holds its chunks (8 elements, 16
+// bytes) c and c + D/16.  The sum of squares is a shuffle sum.  With the whole
+// head rotated by halves, a pair's elements then lie in one lane, as interleaved
+// pairs always do; with a part of it rotated by halves they change places by
+// shuffles.  A CTA works on one token, so the position's cosines and sines are
+// loaded once a lane and kept for all its heads.  Arithmetic is on packed fp32
+// pairs where it can be.  Bound by HBM: every element is read and written once
+// (E4M3 and 4-bit pools: 1 and 0.53 bytes instead of 2 on the way out).
 #include <cmath>
 #include <cstdint>
 
@@ -33,7 +34,6 @@ struct NormRopeParams {
     float eps;
     int num_positions;
     int rotary_dim;
-    int interleaved;
     int num_q_heads;
     int num_kv_heads;
     int rows_per_cta;        // heads of a token one CTA works on
@@ -44,16 +44,65 @@ struct NormRopeParams {
 
 constexpr int kNormRopeThreads = 128;
 
-template <bool BF16, int D, int FMT>
-__global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(const NormRopeParams p) {
-    constexpr int LANES = D / 8, GROUPS = kNormRopeThreads / LANES;
+// 8 fp32 values as four packed pairs.
+struct Chunk {
+    float2 p[4];
+};
+
+template <bool BF16>
+__device__ __forceinline__ Chunk widen_chunk(uint4 v) {
+    return {{widen2<BF16>(v.x), widen2<BF16>(v.y), widen2<BF16>(v.z), widen2<BF16>(v.w)}};
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 narrow_chunk(const Chunk &x) {
+    return make_uint4(narrow2<BF16>(x.p[0].x, x.p[0].y), narrow2<BF16>(x.p[1].x, x.p[1].y),
+                      narrow2<BF16>(x.p[2].x, x.p[2].y), narrow2<BF16>(x.p[3].x, x.p[3].y));
+}
+
+__device__ __forceinline__ Chunk load_chunk(const float *src) {
+    const float4 a = reinterpret_cast<const float4 *>(src)[0];
+    const float4 b = reinterpret_cast<const float4 *>(src)[1];
+    return {{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y),
+             make_float2(b.z, b.w)}};
+}
+
+__device__ __forceinline__ float2 neg2(float2 x) { return make_float2(-x.x, -x.y); }
+
+// How a lane's chunks are rotated: interleaved pairs; halves of the whole head
+// (chunk c with chunk c + D/16); halves of a part of it.
+enum RopeKind { kRopePairs, kRopeWhole, kRopePart };
+
+template <bool BF16, int D, int FMT, int ROPE>
+__global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(
+    const __grid_constant__ NormRopeParams p) {
+    constexpr int LANES = D / 16, GROUPS = kNormRopeThreads / LANES;
     const int c = threadIdx.x % LANES, g = threadIdx.x / LANES;
     const int64_t t = blockIdx.x;
     pdl_wait();
+    const int nq = p.num_q_heads, nk = p.num_kv_heads, heads = nq + 2 * nk;
+    const int first = blockIdx.y * p.rows_per_cta;
+    const int last = min(first + p.rows_per_cta, heads);
+    struct Row {
+        uint4 v[2];
+    };
+    auto load = [&](int r) {
+        Row x = {{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}};
+        if (r < last) {
+            const uint16_t *src = r < nq ? p.src[0] + t * p.stride[0] + (int64_t)r * D
+                                  : r < nq + nk
+                                      ? p.src[1] + t * p.stride[1] + (int64_t)(r - nq) * D
+                                      : p.src[2] + t * p.stride[2] + (int64_t)(r - nq - nk) * D;
+            x.v[0] = reinterpret_cast<const uint4 *>(src)[c];
+            x.v[1] = reinterpret_cast<const uint4 *>(src)[c + LANES];
+        }
+        return x;
+    };
+    Row next = load(first + g);
     const int64_t pos = p.positions[t];
     int64_t slot = p.slots[t];
     if (pos < 0 || pos >= p.num_positions) {  // the same for the whole CTA
-        if (threadIdx.x == 0) record_error(p.err, PA_ERR_BAD_INDEX);
+        if (threadIdx.x == 0 && blockIdx.y == 0) record_error(p.err, PA_ERR_BAD_INDEX);
         return;
     }
     if (slot >= p.num_slots) {
@@ -61,104 +110,155 @@ __global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(const NormR
         slot = -1;
     }
     const int64_t blk = slot >> p.log2_block;
-    const int off = (int)(slot & ((1 << p.log2_block) - 1));
+    const int off = (int)slot & ((1 << p.log2_block) - 1);
 
-    // this lane's cosines and sines: of its 8 elements' angles (halves: the sine
-    // with the sign of the partner's term), or of its four pairs (interleaved);
-    // 1 and 0 where nothing turns
-    const int half = p.rotary_dim >> 1, hc = p.rotary_dim >> 4;  // hc: lanes in a half
-    const bool turns = c < 2 * hc;
-    float cs[8], sn[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
-    if (turns) {
+    // Cosines and sines of the lane's chunks; 1 and 0 where nothing turns.
+    // kRopePairs: of a chunk's four pairs, each twice, the sine as (-s, s);
+    // kRopeWhole: of its eight pairs in cs[0], sn[0]; kRopePart: of each
+    // chunk's eight elements, the sine with the sign of the partner's term.
+    const int half = p.rotary_dim >> 1, hc = p.rotary_dim >> 4;  // hc: chunks in a half
+    Chunk cs[2], sn[2];
+    int partner[2] = {c, c};  // kRopePart: chunk that holds the pairs' other elements
+    {
         const float *row = p.cos_sin + pos * p.rotary_dim;
-        const float *a = row + (p.interleaved ? 4 * c : 8 * (c < hc ? c : c - hc));
+        if constexpr (ROPE == kRopeWhole) {
+            cs[0] = load_chunk(row + 8 * c);
+            sn[0] = load_chunk(row + half + 8 * c);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (i && p.interleaved) break;
-            const float4 u = reinterpret_cast<const float4 *>(a)[i];
-            const float4 w = reinterpret_cast<const float4 *>(a + half)[i];
-            cs[4 * i] = u.x; cs[4 * i + 1] = u.y; cs[4 * i + 2] = u.z; cs[4 * i + 3] = u.w;
-            sn[4 * i] = w.x; sn[4 * i + 1] = w.y; sn[4 * i + 2] = w.z; sn[4 * i + 3] = w.w;
-        }
-        if (!p.interleaved && c < hc) {
+            for (int i = 0; i < 2; ++i) {
+                const int chunk = c + i * LANES;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sn[i] = -sn[i];
+                for (int j = 0; j < 4; ++j) {
+                    cs[i].p[j] = make_float2(1.f, 1.f);
+                    sn[i].p[j] = make_float2(0.f, 0.f);
+                }
+                partner[i] = chunk;
+                if (chunk >= 2 * hc) continue;
+                if constexpr (ROPE == kRopePairs) {
+                    const float4 u = reinterpret_cast<const float4 *>(row)[chunk];
+                    const float4 w = reinterpret_cast<const float4 *>(row + half)[chunk];
+                    cs[i] = {{make_float2(u.x, u.x), make_float2(u.y, u.y), make_float2(u.z, u.z),
+                              make_float2(u.w, u.w)}};
+                    sn[i] = {{make_float2(-w.x, w.x), make_float2(-w.y, w.y), make_float2(-w.z, w.z),
+                              make_float2(-w.w, w.w)}};
+                } else {
+                    const bool low = chunk < hc;
+                    partner[i] = low ? chunk + hc : chunk - hc;
+                    cs[i] = load_chunk(row + 8 * (low ? chunk : chunk - hc));
+                    sn[i] = load_chunk(row + half + 8 * (low ? chunk : chunk - hc));
+                    if (low) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) sn[i].p[j] = neg2(sn[i].p[j]);
+                    }
+                }
+            }
         }
     }
-    // lane that holds the other element of a pair (itself where nothing turns)
-    const int partner = (threadIdx.x & 31) + (turns ? (c < hc ? hc : -hc) : 0);
 
-    const int nq = p.num_q_heads, nk = p.num_kv_heads, heads = nq + 2 * nk;
-    const int first = blockIdx.y * p.rows_per_cta;
-    const int last = min(first + p.rows_per_cta, heads);
-    auto kind_of = [&](int r) { return r < nq ? 0 : r < nq + nk ? 1 : 2; };
-    auto load = [&](int r) {
-        if (r >= last) return make_uint4(0, 0, 0, 0);
-        const int kind = kind_of(r), head = r - (kind > 0 ? nq : 0) - (kind > 1 ? nk : 0);
-        return reinterpret_cast<const uint4 *>(p.src[kind] + t * p.stride[kind] +
-                                               (int64_t)head * D)[c];
-    };
-    // two heads ahead in flight
-    uint4 next[2] = {load(first + g), load(first + GROUPS + g)};
     for (int r0 = first; r0 < last; r0 += GROUPS) {
         const int r = r0 + g;
         const bool live = r < last;
-        const int kind = kind_of(r), head = r - (kind > 0 ? nq : 0) - (kind > 1 ? nk : 0);
-        const uint4 raw = next[0];
-        next[0] = next[1];
-        next[1] = load(r + 2 * GROUPS);
-        uint4 y16 = raw;
+        const int kind = r < nq ? 0 : r < nq + nk ? 1 : 2;
+        const Row raw = next;
+        next = load(r + GROUPS);
+        uint4 y16[2] = {raw.v[0], raw.v[1]};
         if (__any_sync(kFullMask, live && kind < 2)) {
-            float x[8], w[8];
-            widen8<BF16>(raw, x);
-            float ss = 0.f;
+            Chunk x[2];
+            float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+            for (int i = 0; i < 2; ++i) {
+                x[i] = widen_chunk<BF16>(raw.v[i]);
 #pragma unroll
-            for (int o = LANES / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
-            widen8<BF16>(p.weight[kind == 0 ? 0 : 1][c], w);
-            const float inv = __frsqrt_rn(ss * (1.f / D) + p.eps);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
-            float z[8];
-            if (p.interleaved) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a = x[2 * i], b = x[2 * i + 1];
-                    z[2 * i] = a * cs[i] - b * sn[i];
-                    z[2 * i + 1] = b * cs[i] + a * sn[i];
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    z[i] = x[i] * cs[i] + __shfl_sync(kFullMask, x[i], partner) * sn[i];
+                for (int j = 0; j < 4; ++j) ss = __ffma2_rn(x[i].p[j], x[i].p[j], ss);
             }
-            if (kind < 2)
-                y16 = make_uint4(narrow2<BF16>(z[0], z[1]), narrow2<BF16>(z[2], z[3]),
-                                 narrow2<BF16>(z[4], z[5]), narrow2<BF16>(z[6], z[7]));
+            float sum = ss.x + ss.y;
+#pragma unroll
+            for (int o = LANES / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
+            const float inv = __frsqrt_rn(sum * (1.f / D) + p.eps);
+            const float2 inv2 = make_float2(inv, inv);
+            const uint4 *weight = kind == 0 ? p.weight[0] : p.weight[1];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const Chunk w = widen_chunk<BF16>(weight[c + i * LANES]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    x[i].p[j] = __fmul2_rn(__fmul2_rn(x[i].p[j], inv2), w.p[j]);
+            }
+            Chunk z[2];
+            if constexpr (ROPE == kRopeWhole) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 a = x[0].p[j], b = x[1].p[j];
+                    z[0].p[j] = __ffma2_rn(a, cs[0].p[j], neg2(__fmul2_rn(b, sn[0].p[j])));
+                    z[1].p[j] = __ffma2_rn(b, cs[0].p[j], __fmul2_rn(a, sn[0].p[j]));
+                }
+            } else if constexpr (ROPE == kRopePairs) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 a = x[i].p[j];
+                        z[i].p[j] = __ffma2_rn(a, cs[i].p[j],
+                                               __fmul2_rn(make_float2(a.y, a.x), sn[i].p[j]));
+                    }
+            } else {
+                // chunk k is half k / LANES of lane k % LANES; a chunk of the
+                // second half turns with one of the first only
+                const int base = (threadIdx.x & 31) - c;
+                const int from0 = base + partner[0] % LANES, from1 = base + partner[1] % LANES;
+                auto both = [&](float a, float b, float *q0, float *q1) {
+                    const float u = __shfl_sync(kFullMask, a, from0);
+                    const float w = __shfl_sync(kFullMask, b, from0);
+                    const float v = __shfl_sync(kFullMask, a, from1);
+                    *q0 = partner[0] < LANES ? u : w;
+                    *q1 = v;  // (where chunk c + LANES does not turn its sine is 0)
+                };
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float2 q0, q1;
+                    both(x[0].p[j].x, x[1].p[j].x, &q0.x, &q1.x);
+                    both(x[0].p[j].y, x[1].p[j].y, &q0.y, &q1.y);
+                    z[0].p[j] = __ffma2_rn(x[0].p[j], cs[0].p[j], __fmul2_rn(q0, sn[0].p[j]));
+                    z[1].p[j] = __ffma2_rn(x[1].p[j], cs[1].p[j], __fmul2_rn(q1, sn[1].p[j]));
+                }
+            }
+            if (kind < 2) {
+                y16[0] = narrow_chunk<BF16>(z[0]);
+                y16[1] = narrow_chunk<BF16>(z[1]);
+            }
+        }
+        if (live && kind == 0) {
+            uint4 *to = reinterpret_cast<uint4 *>(p.q_out + t * p.q_out_stride + (int64_t)r * D);
+            to[c] = y16[0];
+            to[c + LANES] = y16[1];
         }
         const bool store = live && kind > 0 && slot >= 0;
-        if (live && kind == 0)
-            reinterpret_cast<uint4 *>(p.q_out + t * p.q_out_stride + (int64_t)head * D)[c] = y16;
-        uint8_t *pool = p.pool[kind == 2];
-        const int64_t rec = blk * nk + head;
+        uint8_t *pool = kind == 1 ? p.pool[0] : p.pool[1];
+        const int64_t rec = blk * nk + (r - (kind == 1 ? nq : nq + nk));
         const int64_t at = (rec << p.log2_block) + off;
         if constexpr (FMT == PA_KV_16BIT) {
-            if (store) reinterpret_cast<uint4 *>(pool)[at * LANES + c] = y16;
+            if (store) {
+                uint4 *to = reinterpret_cast<uint4 *>(pool) + at * (D / 8);
+                to[c] = y16[0];
+                to[c + LANES] = y16[1];
+            }
         } else if constexpr (FMT == PA_KV_E4M3) {
             if (store) {
-                const uint4 q = quantize16_e4m3<BF16>(y16, y16, p.inv_scale[kind == 2]);
-                reinterpret_cast<uint2 *>(pool)[at * LANES + c] = make_uint2(q.x, q.y);
+                const uint4 q = quantize16_e4m3<BF16>(
+                    y16[0], y16[1], kind == 1 ? p.inv_scale[0] : p.inv_scale[1]);
+                uint2 *to = reinterpret_cast<uint2 *>(pool) + at * (D / 8);
+                to[c] = make_uint2(q.x, q.y);
+                to[c + LANES] = make_uint2(q.z, q.w);
             }
         } else {
             if (__any_sync(kFullMask, store)) {
-                const uint4 row[1] = {y16};
-                const Int4Row<1> q = quantise_row_int4<BF16, LANES, 1>(row);
+                const Int4Row<2> q = quantise_row_int4<BF16, LANES, 2, false>(y16, nullptr);
                 if (store) {
                     uint8_t *dst = pool + rec * int4_record_bytes<D>(1 << p.log2_block);
-                    *reinterpret_cast<uint32_t *>(dst + off * (D / 2) + c * 4) = q.codes[0];
+                    uint32_t *to = reinterpret_cast<uint32_t *>(dst + off * (D / 2));
+                    to[c] = q.codes[0];
+                    to[c + LANES] = q.codes[1];
                     if (c == 0)
                         *reinterpret_cast<uint32_t *>(dst + ((D / 2) << p.log2_block) + off * 4) =
                             q.params;
@@ -166,6 +266,27 @@ __global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(const NormR
             }
         }
     }
+}
+
+using NormRopeKernel = void (*)(const NormRopeParams);
+
+template <bool BF16, int D, int FMT>
+static NormRopeKernel rope_variant(int rope) {
+    return rope == kRopePairs   ? norm_rope_kernel<BF16, D, FMT, kRopePairs>
+           : rope == kRopeWhole ? norm_rope_kernel<BF16, D, FMT, kRopeWhole>
+                                : norm_rope_kernel<BF16, D, FMT, kRopePart>;
+}
+
+template <bool BF16, int D>
+static NormRopeKernel format_variant(int fmt, int rope) {
+    return fmt == PA_KV_16BIT  ? rope_variant<BF16, D, PA_KV_16BIT>(rope)
+           : fmt == PA_KV_E4M3 ? rope_variant<BF16, D, PA_KV_E4M3>(rope)
+                               : rope_variant<BF16, D, PA_KV_INT4>(rope);
+}
+
+static NormRopeKernel pick_norm_rope(bool bf16, int D, int fmt, int rope) {
+    if (D == 64) return bf16 ? format_variant<true, 64>(fmt, rope) : format_variant<false, 64>(fmt, rope);
+    return bf16 ? format_variant<true, 128>(fmt, rope) : format_variant<false, 128>(fmt, rope);
 }
 
 }  // namespace pa
@@ -224,12 +345,11 @@ extern "C" pa_status pa_qk_norm_rope(
     p.eps = eps;
     p.num_positions = num_positions;
     p.rotary_dim = rotary_dim;
-    p.interleaved = interleaved != 0;
     p.num_q_heads = num_q_heads;
     p.num_kv_heads = num_kv_heads;
     p.log2_block = block_size == 16 ? 4 : 5;
     p.num_slots = (int64_t)num_blocks * block_size;
-    const int groups = kNormRopeThreads / (head_dim / 8), heads = num_q_heads + 2 * num_kv_heads;
+    const int groups = kNormRopeThreads / (head_dim / 16), heads = num_q_heads + 2 * num_kv_heads;
     // one CTA a token; tokens too few to fill the GPU are split over their heads
     int chunks = 1;
     const int most = (heads + groups - 1) / groups;
@@ -238,15 +358,10 @@ extern "C" pa_status pa_qk_norm_rope(
     p.rows_per_cta = per * groups;
     const dim3 grid((unsigned)num_tokens, (unsigned)((most + per - 1) / per));
     if (grid.y > 65535) return PA_ERR_INVALID;
-    auto kern = norm_rope_kernel<false, 64, PA_KV_16BIT>;
-#define PA_CASE(BF, DD, FF)                                                      \
-    if ((dtype == PA_BF16) == BF && head_dim == DD && kv_format == FF)           \
-        kern = norm_rope_kernel<BF, DD, FF>;
-#define PA_CASES(FF) PA_CASE(false, 64, FF) PA_CASE(false, 128, FF) PA_CASE(true, 64, FF) \
-    PA_CASE(true, 128, FF)
-    PA_CASES(PA_KV_16BIT) PA_CASES(PA_KV_E4M3) PA_CASES(PA_KV_INT4)
-#undef PA_CASES
-#undef PA_CASE
+    const int rope = interleaved               ? kRopePairs
+                     : rotary_dim == head_dim ? kRopeWhole
+                                              : kRopePart;
+    NormRopeKernel kern = pick_norm_rope(dtype == PA_BF16, head_dim, kv_format, rope);
     if (launch_pdl(kern, grid, dim3(kNormRopeThreads), 0, as_stream(stream), p) != cudaSuccess)
         return PA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;

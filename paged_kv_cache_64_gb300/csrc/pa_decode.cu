@@ -1071,18 +1071,19 @@ static pa_status decode_impl(void *out, const void *q, const void *k_new, const 
 }
 
 // Balanced ranges of pa_decode_int4 (automatic partitions): the launch's CTAs
-// (those of the first wave) and the workspace: m, l [slot][8], O [slot][G][d] for
+// (groups of the first wave, heads of a bundle) and the workspace: m, l [slot][8], O [slot][G][d] for
 // two slots a CTA.
 struct Int4Balance {
     int ctas;
     int wave;
+    int bundle;
     WorkspaceLayout ws;
 };
 static bool int4_balance(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                          int block_size, int max_seq_len, pa_dtype dtype, Int4Balance *b) {
     const int G = num_q_heads / num_kv_heads;
     b->ctas = int4_balanced_ctas(dtype == PA_BF16, head_dim, block_size, G, num_seqs, num_kv_heads,
-                                 max_seq_len, &b->wave);
+                                 max_seq_len, &b->wave, &b->bundle);
     if (b->ctas <= 0) return false;
     const size_t slots = 2 * (size_t)b->ctas;
     b->ws = {};
@@ -1269,6 +1270,7 @@ pa_status pa_decode_int4(void *out, const void *q, const void *k_pool, const voi
     if (st != PA_OK) return st;
     prm.out = out;
     prm.balanced = b.wave;
+    prm.bundle = b.bundle;
     if (!workspace || workspace_bytes < b.ws.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255))
         return PA_ERR_INVALID;
     uint8_t *ws = static_cast<uint8_t *>(workspace);

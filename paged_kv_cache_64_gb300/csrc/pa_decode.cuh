@@ -86,8 +86,9 @@ struct DecodeParams {
     float v_scale;
     // 4-bit pools: balanced ranges instead of chunks (pa_decode_int4.cu);
     // part_m, part_l and part_o are then laid out by its slots, and this is the
-    // number of CTAs in the first wave.
+    // number of groups of CTAs in the first wave; a group takes `bundle` heads.
     int balanced;
+    int bundle;
 };
 
 // Length of sequence i, clamped to what the launch covers; a value out of
@@ -574,7 +575,7 @@ constexpr int kInt4SinglePass = 1024;  // 4-bit pools: longer heads may be cut
 // those of the records.
 int int4_ctas_per_sm(bool bf16, int head_dim, int block_size, int group);
 int int4_balanced_ctas(bool bf16, int head_dim, int block_size, int group, int num_seqs,
-                       int num_kv_heads, int max_seq_len, int *wave);
+                       int num_kv_heads, int max_seq_len, int *wave, int *bundle);
 pa_status launch_decode_int4(const DecodeParams &prm, bool bf16, int head_dim, int num_partitions,
                              int num_kv_heads, int num_seqs, cudaStream_t stream);
 

@@ -84,23 +84,26 @@ __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t
 
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) { return narrow2<false>(a, b); }
 
-// Balanced ranges (automatic partitions).  The batch's work is one line of
-// units of 128 positions, sequence by sequence and head by head; CTA c takes
-// the units from bound(c) to bound(c + 1), moved to the next head's border where
+// Balanced ranges (automatic partitions).  The heads go in bundles of up to 8:
+// as many consecutive CTAs take the same positions of a bundle's heads at about
+// the same time, so that the records of a block, which lie together, are read
+// together.  The work is one line of units of 128 positions, sequence by sequence
+// and bundle by bundle; group c of CTAs takes the units from bound(c) to
+// bound(c + 1), moved to the next head's border where
 // that is at most `slack` units away, so that no head is cut for a sliver.  Every
 // CTA works the line out from the lengths (one load and a scan), whatever they
-// are.  A first wave of CTAs takes equal large shares; a second, of smaller
+// are.  A first wave of groups takes equal large shares; a second, of smaller
 // shares, is started as the first ends, which the SMs do not do together (equal
 // shares in one wave alone ended between 138 and 222 us).  The partials of heads
 // that bounds cut are merged by a second kernel.
-// A CTA's range: units [unit, end) of the line.  Its next unit is unit `at`
-// of the n units of head kvh of sequence seq.
+// A group's range: units [unit, end) of the line.  Its next unit is unit `at`
+// of the n units of bundle `bundle` of sequence seq.
 struct Int4Range {
-    int wave;          // CTAs of the first wave
+    int wave;          // groups of the first wave
     int share, small;  // units of a share in the first wave, in the second
     int slack;
     int unit, end;
-    int seq, kvh, at, n;
+    int seq, bundle, at, n;
 };
 
 // A piece of work: `count` positions of a head from `start` on (-1: none
@@ -118,7 +121,7 @@ constexpr int kInt4MinSlack = 2;
 // 16 long ones (40 units) 94 -> 98.
 constexpr int kInt4SecondWave = 64;  // units a slot from which on there is one,
 constexpr int kInt4SecondPart = 5;   //   with a fifth of the work,
-constexpr int kInt4SecondCtas = 2;   //   in twice as many CTAs
+constexpr int kInt4SecondCtas = 2;   //   in twice as many groups
 constexpr int kInt4BalancedSeqs = 1024;            // longer batches: a CTA an item, by the hardware
 
 __device__ __forceinline__ int int4_units(const DecodeParams &p, int seq) {
@@ -131,20 +134,20 @@ __device__ __forceinline__ int int4_bound_before(const Int4Range &r, int u) {
     return u < large ? u / r.share : r.wave + (u - large) / r.small;
 }
 
-// Pieces that bounds cut the range's present head into, and the first bound
+// Pieces that bounds cut the heads of the range's present bundle into, and the first bound
 // inside it: those past its first slack units and before its last.
 __device__ __forceinline__ int int4_parts(const Int4Range &r, int *first) {
-    const int a = r.unit - r.at, b = a + r.n;  // the head on the line
+    const int a = r.unit - r.at, b = a + r.n;  // the bundle on the line
     *first = int4_bound_before(r, a + r.slack) + 1;
     const int last = b <= r.slack ? -1 : int4_bound_before(r, b - r.slack - 1);
     return max(last - *first + 1, 0) + 1;
 }
 
-// The range of CTA `cta` of ncta, `wave` of them in the first wave, or (cta < 0) the place of head `head`
-// (sequence head / Hkv), with n = 0 for one without positions.  Called by all T
+// The range of group `group` of ngroups, or (group < 0) the place of the index-th
+// bundle of the batch, with n = 0 for one without positions.  Called by all T
 // threads of the block; ends synchronised.
 template <int T>
-__device__ __forceinline__ void int4_plan(const DecodeParams &p, int ncta, int cta, int head,
+__device__ __forceinline__ void int4_plan(const DecodeParams &p, int ngroups, int group, int index,
                                           Int4Range *range) {
     const int wave = p.balanced;
     __shared__ int sums[T / 32];
@@ -167,29 +170,29 @@ __device__ __forceinline__ void int4_plan(const DecodeParams &p, int ncta, int c
         if (w < (tid >> 5)) before += sums[w];
         all += sums[w];
     }
-    const int H = p.num_kv_heads, total = all * H;
-    // the second wave gets a part of the work if its shares are worth a CTA each
+    const int H = p.num_kv_heads / p.bundle, total = all * H;
+    // the second wave gets a part of the work if its shares are worth their CTAs
     int share = max((total + wave - 1) / wave, kInt4MinShare), small = share;
-    if (ncta > wave && share >= kInt4SecondWave) {
+    if (ngroups > wave && share >= kInt4SecondWave) {
         share -= share / kInt4SecondPart;
-        small = max((total - wave * share + ncta - wave - 1) / (ncta - wave), kInt4MinShare);
+        small = max((total - wave * share + ngroups - wave - 1) / (ngroups - wave), kInt4MinShare);
     }
     const int slack = max(small / 8, kInt4MinSlack);
-    if (cta < 0) {
-        const int seq = head / H;
+    if (group < 0) {
+        const int seq = index / H;
         if (seq >= s0 && seq < s1) {
             int base = before;
             for (int s = s0; s < seq; ++s) base += int4_units(p, s);
             range->seq = seq;
-            range->kvh = head - seq * H;
+            range->bundle = index - seq * H;
             range->at = 0;
             range->n = int4_units(p, seq);
-            range->unit = base * H + range->kvh * range->n;
+            range->unit = base * H + range->bundle * range->n;
         }
     } else {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const int c = cta + b;
+            const int c = group + b;
             const int u = min(c < wave ? c * share : wave * share + (c - wave) * small, total);
             if (u == total) {
                 if (tid == 0) {
@@ -202,20 +205,20 @@ __device__ __forceinline__ void int4_plan(const DecodeParams &p, int ncta, int c
                     base += n * H;
                     n = int4_units(p, ++seq);
                 }
-                const int kvh = (u - base) / n;
-                int at = u - base - kvh * n;
+                const int bundle = (u - base) / n;
+                int at = u - base - bundle * n;
                 if (at <= slack)
                     at = 0;
                 else if (n - at <= slack)
                     at = n;
                 if (b == 0) {
                     range->seq = seq;
-                    range->kvh = kvh;
+                    range->bundle = bundle;
                     range->at = at;
                     range->n = n;
-                    range->unit = base + kvh * n + at;
+                    range->unit = base + bundle * n + at;
                 } else {
-                    range->end = base + kvh * n + at;
+                    range->end = base + bundle * n + at;
                 }
             }
         }
@@ -237,17 +240,17 @@ __device__ __forceinline__ void int4_next_piece(const DecodeParams &p, Int4Range
         piece->count = -1;
         return;
     }
-    if (r.at == r.n) {  // the next head with anything in it
+    if (r.at == r.n) {  // the next bundle with anything in it
         r.at = 0;
-        if (++r.kvh == p.num_kv_heads) {
-            r.kvh = 0;
+        if (++r.bundle == p.num_kv_heads / p.bundle) {
+            r.bundle = 0;
             do r.n = int4_units(p, ++r.seq);
             while (r.n == 0);
         }
     }
     const int units = min(r.n - r.at, r.end - r.unit);
     piece->seq = r.seq;
-    piece->kvh = r.kvh;
+    piece->kvh = r.bundle * p.bundle + (int)blockIdx.x % p.bundle;
     piece->start = r.at * kInt4Unit;
     piece->count = min(item_len(p, r.seq, false), (r.at + units) * kInt4Unit) - piece->start;
     piece->slot = 2 * (int)blockIdx.x + (r.at == 0 ? 1 : 0);
@@ -257,22 +260,22 @@ __device__ __forceinline__ void int4_next_piece(const DecodeParams &p, Int4Range
     r.at += units;
 }
 
-// Partials of the balanced ranges: CTA c leaves at most two, of the head its
-// range starts inside of (slot 2 c) and of the one it ends inside of, if that
-// one starts in it (slot 2 c + 1): m, l [slot][8] and O [slot][G][D].
+// Partials of the balanced ranges: a CTA leaves at most two, of the head its
+// range starts inside of (slot 2 blockIdx.x) and of the one it ends inside of, if
+// that one starts in it (the slot after): m, l [slot][8] and O [slot][G][D].
 //
 // The merge: out = sum_k w_k O_k / sum_k w_k, w_k = l_k 2^(m_k - max m), over the
 // n partials of every head that bounds cut.  Few heads (HEADS, cut into many
 // partials each): a block a query head, its threads four dimensions each of
-// every SLICES-th partial.  Many heads: a block a bound, at work if that is the
-// first inside a head, its threads four dimensions each of all partials of
+// every SLICES-th partial.  Many heads: a block a bound and head of the bundle, at
+// work if that bound is the first inside the head, its threads four dimensions each of all partials of
 // one or two query heads.  A thread has eight partials' loads in flight and
 // keeps its own running maximum, so nothing waits for the maxima first.
 constexpr int kInt4MergeHeads = 512, kInt4MergeBounds = 128;  // threads
 
 template <bool BF16, int D, bool HEADS>
 __global__ void __launch_bounds__(HEADS ? kInt4MergeHeads : kInt4MergeBounds)
-    int4_merge_kernel(const DecodeParams p, int ncta) {
+    int4_merge_kernel(const DecodeParams p, int ngroups) {
     constexpr int T = HEADS ? kInt4MergeHeads : kInt4MergeBounds;
     constexpr int ITEMS = D / 4, ROWS = T / ITEMS, SLICES = HEADS ? ROWS : 1;
     __shared__ Int4Range range;
@@ -281,14 +284,18 @@ __global__ void __launch_bounds__(HEADS ? kInt4MergeHeads : kInt4MergeBounds)
     const int item = threadIdx.x % ITEMS, row = threadIdx.x / ITEMS;
     // the decode kernel began after all work before it was done, so the lengths
     // are there
-    int4_plan<T>(p, ncta, HEADS ? -1 : (int)blockIdx.x + 1, (int)blockIdx.x, &range);
+    const int in_bundle = (int)blockIdx.x % p.bundle, index = (int)blockIdx.x / p.bundle;
+    int4_plan<T>(p, ngroups, HEADS ? -1 : index + 1, index, &range);
     int first = 0, n = 0;
     const bool mine = (HEADS ? range.n > 0 : range.unit < range.end && range.at > 0 &&
                                                  range.at < range.n) &&
-                      (n = int4_parts(range, &first)) > 1 && (HEADS || first == (int)blockIdx.x + 1);
+                      (n = int4_parts(range, &first)) > 1 && (HEADS || first == index + 1);
     pdl_wait();
     if (!mine) return;
-    auto slot = [&](int k) { return k == 0 ? 2 * (first - 1) + 1 : 2 * (first - 1 + k); };
+    auto slot = [&](int k) {
+        return 2 * ((first - 1 + k) * p.bundle + in_bundle) + (k == 0 ? 1 : 0);
+    };
+    const int kvh = range.bundle * p.bundle + in_bundle;
     for (int g = HEADS ? blockIdx.y : row; g < p.group; g += ROWS) {
         const float4 *rows = reinterpret_cast<const float4 *>(p.part_o) + g * ITEMS + item;
         const int64_t stride = (int64_t)p.group * ITEMS;
@@ -351,7 +358,7 @@ __global__ void __launch_bounds__(HEADS ? kInt4MergeHeads : kInt4MergeBounds)
         }
         const float f = 1.f / total;
         uint16_t *out = static_cast<uint16_t *>(p.out) +
-                        ((int64_t)range.seq * p.num_q_heads + range.kvh * p.group + g) * D;
+                        ((int64_t)range.seq * p.num_q_heads + kvh * p.group + g) * D;
         reinterpret_cast<uint2 *>(out)[item] =
             make_uint2(narrow2<BF16>(o.x * f, o.y * f), narrow2<BF16>(o.z * f, o.w * f));
         if constexpr (HEADS) return;
@@ -383,7 +390,7 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
     __shared__ Int4Piece piece;
     if (p.balanced) {
         pdl_trigger();  // the merge kernel may work out its plan
-        int4_plan<32 * kInt4Warps>(p, gridDim.x, blockIdx.x, 0, &range);
+        int4_plan<32 * kInt4Warps>(p, gridDim.x / p.bundle, blockIdx.x / p.bundle, 0, &range);
     } else {
         int chunk, kvh, seq;
         if (p.compact) {
@@ -853,23 +860,32 @@ int int4_ctas_per_sm(bool bf16, int head_dim, int block_size, int group) {
     return slot = n > 0 ? n : 1;
 }
 
-// CTAs of a balanced launch, and those of its first wave (at most one a slot,
-// or as many as there can be shares); 0 where the batch is not for balanced
-// ranges: heads too short to be worth cutting (single pass is as fast up to 1024
-// positions, 13 against 14 us for 8 sequences; at 2048, 19 against 15), or more
-// sequences than a CTA should scan.
+// Heads of a bundle: the largest divisor of num_kv_heads up to 8.
+static int int4_bundle(int num_kv_heads) {
+    int b = num_kv_heads < 8 ? num_kv_heads : 8;
+    while (num_kv_heads % b) --b;
+    return b;
+}
+
+// CTAs of a balanced launch, the groups of its first wave (as many as there are
+// slots, or shares) and the heads of a bundle; 0 where the batch is not for
+// balanced ranges: heads too short to be worth cutting (single pass is as fast up
+// to 1024 positions, 13 against 14 us for 8 sequences; at 2048, 19 against 15),
+// or more sequences than a CTA should scan.
 int int4_balanced_ctas(bool bf16, int head_dim, int block_size, int group, int num_seqs,
-                       int num_kv_heads, int max_seq_len, int *wave) {
+                       int num_kv_heads, int max_seq_len, int *wave, int *bundle) {
     if (max_seq_len <= kInt4SinglePass) return 0;
-    const int64_t units =
-        (int64_t)num_seqs * num_kv_heads * (((int64_t)max_seq_len + kInt4Unit - 1) / kInt4Unit);
+    *bundle = int4_bundle(num_kv_heads);
+    const int64_t units = (int64_t)num_seqs * (num_kv_heads / *bundle) *
+                          (((int64_t)max_seq_len + kInt4Unit - 1) / kInt4Unit);
     if (num_seqs > kInt4BalancedSeqs || units >= (1 << 30)) return 0;
     const int64_t shares = (units + kInt4MinShare - 1) / kInt4MinShare;
-    const int64_t slots =
-        (int64_t)sm_count() * int4_ctas_per_sm(bf16, head_dim, block_size, group);
-    if (shares < slots) return *wave = shares < 1 ? 1 : (int)shares;
+    int64_t slots =
+        (int64_t)sm_count() * int4_ctas_per_sm(bf16, head_dim, block_size, group) / *bundle;
+    if (slots < 1) slots = 1;
+    if (shares < slots) return (*wave = shares < 1 ? 1 : (int)shares) * *bundle;
     *wave = (int)slots;
-    return units >= slots * kInt4SecondWave ? (int)slots * (1 + kInt4SecondCtas) : (int)slots;
+    return (int)slots * *bundle * (units >= slots * kInt4SecondWave ? 1 + kInt4SecondCtas : 1);
 }
 
 pa_status launch_decode_int4(const DecodeParams &prm, bool bf16, int head_dim, int num_partitions,
@@ -884,15 +900,15 @@ pa_status launch_decode_int4(const DecodeParams &prm, bool bf16, int head_dim, i
         if (launch_pdl(k, dim3((unsigned)num_partitions), dim3(32 * kInt4Warps), (size_t)smem, stream,
                        p) != cudaSuccess)
             return PA_ERR_CUDA;
-        if (p.part_o && num_partitions > 1) {
+        if (num_partitions > p.bundle) {
             // a head cut into 8 partials or more on average: a block a query head
             const int64_t heads = (int64_t)num_seqs * num_kv_heads;
             const bool few = 8 * heads <= num_partitions;
             const dim3 grid = few ? dim3((unsigned)heads, (unsigned)p.group)
-                                  : dim3((unsigned)num_partitions - 1);
+                                  : dim3((unsigned)(num_partitions - p.bundle));
             if (launch_pdl(pick_merge(bf16, head_dim, few), grid,
                            dim3(few ? kInt4MergeHeads : kInt4MergeBounds), 0, stream, p,
-                           num_partitions) != cudaSuccess)
+                           num_partitions / p.bundle) != cudaSuccess)
                 return PA_ERR_CUDA;
         }
         return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;

@@ -434,9 +434,10 @@ def decode_int4(out, q, k_pool, v_pool, block_tables, seq_lens, max_seq_len, sca
             need = int4_workspace_size(S, hq, hkv, d, bs, int(max_seq_len), int(partition_tokens),
                                        q.dtype)
         if need and (workspace is None or workspace.nbytes < need):
-            workspace = alloc_workspace(need, q.device)
-            if stream is not None:
-                workspace.record_stream(stream)
+            # from the stream's own memory: a block freed on another stream may
+            # still be in use there
+            with torch.cuda.stream(stream):
+                workspace = alloc_workspace(need, q.device)
             rc = run(workspace)
     _lib.check("pa_decode_int4", rc)
     return workspace

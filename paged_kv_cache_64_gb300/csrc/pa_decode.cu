@@ -1084,6 +1084,7 @@ static bool int4_balance(int num_seqs, int num_q_heads, int num_kv_heads, int he
     const int G = num_q_heads / num_kv_heads;
     b->ctas = int4_balanced_ctas(dtype == PA_BF16, head_dim, block_size, G, num_seqs, num_kv_heads,
                                  max_seq_len, &b->wave, &b->bundle);
+    if (num_seqs == 0) return b->ws = {}, true;
     if (b->ctas <= 0) return false;
     const size_t slots = 2 * (size_t)b->ctas;
     b->ws = {};
@@ -1267,7 +1268,7 @@ pa_status pa_decode_int4(void *out, const void *q, const void *k_pool, const voi
     const pa_status st = fill_common(&prm, q, k_pool, v_pool, num_blocks, block_tables,
                                      max_blocks_per_seq, seq_lens, max_seq_len, num_seqs,
                                      num_q_heads, num_kv_heads, block_size, scale);
-    if (st != PA_OK) return st;
+    if (st != PA_OK || num_seqs == 0) return st;
     prm.out = out;
     prm.balanced = b.wave;
     prm.bundle = b.bundle;

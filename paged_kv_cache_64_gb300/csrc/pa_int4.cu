@@ -130,7 +130,7 @@ static pa_status int4_rows(bool read, Int4IoParams p, int num_tokens, const void
     if (num_kv_heads > 1) {
         // l = ceil(log2 H), magic = ceil(2^(31 + l) / H) < 2^32: exact below 2^31
         int l = 1;
-        while ((1 << l) < num_kv_heads) ++l;
+        while ((1ll << l) < num_kv_heads) ++l;
         p.magic = (uint32_t)(((1ull << (31 + l)) + num_kv_heads - 1) / num_kv_heads);
         p.shift = l - 1;
     }

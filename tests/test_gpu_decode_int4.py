@@ -81,6 +81,8 @@ class Case:
 
     def gpu(self, partition=0, workspace=None, stream=None):
         out = torch.full_like(self.gq, float("nan"))
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
         api.decode_int4(out, self.gq, self.gk, self.gv, self.gt, self.gl, self.max_len, self.scale,
                         partition_tokens=partition, workspace=workspace, stream=stream)
         return out
@@ -343,3 +345,75 @@ def test_offsets_past_32_bits():
     api.decode_int4(y, q, sk, sv, torch.arange(small, device="cuda", dtype=torch.int32)[None], lens,
                     L, d ** -0.5)
     assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("hkv,group,block", [(5, 2, 16), (11, 1, 32), (16, 3, 16), (2, 8, 32)])
+def test_head_counts_of_every_bundle(hkv, group, block):
+    """Lengths that the automatic choice cuts, for head counts whose bundles
+    are 5, 1, 8 and 2; sequences without tokens between them."""
+    c = Case([0, 4000, 1, 2100, 0, 1300, 130, 0], hkv, group, 64, block, "f16", seed=hkv)
+    c.check(c.gpu(0))
+
+
+@pytest.mark.parametrize("lens", [[1025], [3000] * 3, [0, 0, 9000], [1100] * 40, [20000, 3, 3, 3]])
+def test_automatic_choice_against_single_pass(lens):
+    c = Case(lens, 2, 4, 128, 16, "f16", seed=len(lens))
+    c.check(c.gpu(0))
+    c.check(c.gpu(-1))
+
+
+def test_a_long_batch_with_a_second_wave():
+    """Fifty sequences of 12,000 to 16,384 positions: shares of over 64 units, so
+    two waves of CTAs; single pass gives the same sums in another order, and two
+    sequences go through the oracle."""
+    rng = np.random.default_rng(0)
+    S, hkv, group, d, block = 50, 8, 2, 64, 16
+    lens = rng.integers(12000, 16385, S)
+    lens[7] = 0
+    count = -(-lens // block)
+    nb = int(count.sum())
+    order = rng.permutation(nb)
+    tables = np.zeros((S, count.max()), np.int32)
+    used = np.arange(count.max())[None] < count[:, None]
+    tables[used] = order
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    kp, vp = (torch.empty(api.int4_pool_shape(nb, hkv, block, d), dtype=torch.uint8, device="cuda")
+              for _ in range(2))
+    slots = torch.arange(nb * block, device="cuda")
+    for p in (kp, vp):
+        x = torch.randn(nb * block, hkv, d, generator=g, device="cuda").to(torch.float16)
+        api.cache_write_int4(x, x, slots, p, p.clone())
+    q = torch.randn(S, hkv * group, d, generator=g, device="cuda").to(torch.float16)
+    gt, gl = torch.as_tensor(tables, device="cuda"), torch.as_tensor(lens, device="cuda").int()
+    out, one = torch.empty_like(q), torch.empty_like(q)
+    ws = api.decode_int4(out, q, kp, vp, gt, gl, int(lens.max()), d ** -0.5)
+    api.decode_int4(one, q, kp, vp, gt, gl, int(lens.max()), d ** -0.5, partition_tokens=-1)
+    api.check_error()
+    assert not out[7].any()
+    for _ in range(3):  # the same bits every time, whatever the order of the CTAs
+        again = torch.empty_like(q)
+        api.decode_int4(again, q, kp, vp, gt, gl, int(lens.max()), d ** -0.5, workspace=ws)
+        assert torch.equal(again, out)
+    a, b = out.double(), one.double()
+    # both within half a step and fp32's share of the true value (see above)
+    assert ((a - b).abs() <= 2.0**-10 * 1.01 * b.abs() + 2.0**-14).all()
+    for i in (0, 33):
+        at = tables[i, :count[i]]
+        small = Case.__new__(Case)
+        small.d, small.block, small.dtype, small.scale = d, block, "f16", d ** -0.5
+        small.kp, small.vp = (p[torch.as_tensor(at, device="cuda").long()].cpu().numpy()
+                              for p in (kp, vp))
+        small.tables = np.arange(len(at), dtype=np.int32)[None]
+        small.lens, small.q = lens[i:i + 1], bits(q[i:i + 1])
+        small.check(out[i:i + 1], i)
+
+
+def test_a_given_stream_without_a_workspace():
+    c = Case([4000, 70], 2, 4, 128, 16, "bf16")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = [c.gpu(0, stream=side) for _ in range(3)]
+    side.synchronize()
+    for o in outs:
+        c.check(o)

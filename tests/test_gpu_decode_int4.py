@@ -417,3 +417,17 @@ def test_a_given_stream_without_a_workspace():
     side.synchronize()
     for o in outs:
         c.check(o)
+
+
+@pytest.mark.parametrize("hkv,group", [(2, 4), (1, 8)])
+def test_small_outputs_of_a_long_sequence_keep_their_digits(hkv, group):
+    """Over 120,000 positions the weights average V to about 1/200 of its size,
+    while the sums of codes that the kernel forms are of V's whole range.  What
+    fp32 loses of them has to stay below f16's rounding of the result: in the
+    2-norm, half a step (2^-11)."""
+    c = Case([120000], hkv, group, 128, 16, "f16", seed=hkv)
+    out = int4.widen(bits(c.gpu(0)), "f16")
+    ref = c.oracle()
+    assert np.linalg.norm(out - ref) <= 2.0**-11 * np.linalg.norm(ref)
+    one = int4.widen(bits(c.gpu(-1)), "f16")  # 940 steps of a warp in one sum
+    assert np.linalg.norm(one - ref) <= 2.0**-11 * np.linalg.norm(ref)

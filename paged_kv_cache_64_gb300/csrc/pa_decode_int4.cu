@@ -3,7 +3,7 @@
 // For a KV head with G <= 8 query heads, position p's key is m_p + s_p n_p
 // with codes n in 0 .. 15, so
 //   q . k_p = s_p (q . n_p) + m_p sum(q)
-//   out     = sum_p (P_p s'_p) (n'_p - 7.5) + sum_p P_p (m'_p + 7.5 s'_p)
+//   out     = sum_p (P_p s'_p) n'_p + sum_p P_p m'_p
 // and only the products with the codes touch every element: they go to the
 // matrix unit (mma.sync m16n8k16, f16 operands, fp32 sums), scales and minima
 // are applied to the 16 x 8 score tile and to the weights.
@@ -20,10 +20,11 @@
 // which the transposing register exchange movmatrix brings from the score
 // tile's layout.  The weights P s' are split into two f16 terms (22 bits) and
 // scaled by a power of two kept, like the running maximum, per warp.  The matrix
-// unit cuts sums off instead of rounding them, and sums of codes are all of one
-// sign; so 7.5 times the weights' sum is taken out of them every few steps, which
-// keeps them about zero (without it, a mean over 120,000 positions was off by
-// 2^-10 of itself).
+// unit cuts sums off instead of rounding them, and sums of codes would all be of
+// one sign: every other 16 positions enter as -P s' times 15 - n (a mask with an
+// exclusive or), which leaves 15 s' for their minimum to take over and keeps the
+// sums about zero.  (Without it a mean over 120,000 positions in one warp's sum
+// was off by 9e-2 of itself; with it by 2.0e-4, which is f16's own rounding.)
 //
 // Why not tcgen05: its A operand comes from shared memory, where codes would
 // have to be stored again as 8- or 16-bit values, four to eight times the
@@ -47,13 +48,6 @@ constexpr int kInt4Warps = 4;
 constexpr int kInt4MaxG = 8;
 
 constexpr int kInt4Step = 32;   // positions a warp takes at a time: two score tiles
-// Steps between two centrings of the codes' sums.  Both weight terms in one sum
-// (more than four heads) cut off twice as often.  Over 120,000 positions the error
-// was 2.4e-4 (four heads) and 2.9e-4 (eight) of the result, 2.0e-4 of it f16's own
-// rounding; without centring 6e-4 to 9e-4 after 16 steps, 9e-2 after 940.
-template <bool H4>
-constexpr int kInt4Centre = H4 ? 4 : 2;
-
 template <int D>
 struct Int4Shape {
     static constexpr int HALF = kInt4Step * (D / 2 + 4);  // a step's K (or V) records
@@ -541,29 +535,8 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
     float O[4 * VW][4];
 #pragma unroll
     for (int a = 0; a < 4 * VW; ++a) O[a][0] = O[a][1] = O[a][2] = O[a][3] = 0.f;
-    // sx: the weights P s' fe that O's codes have not been centred for yet; pm:
-    // sum of P times the middles of the rows' ranges
-    float M[2] = {0.f, 0.f}, l[2] = {0.f, 0.f}, pm[2] = {0.f, 0.f}, sx[2] = {0.f, 0.f};
-    // O's codes become n - 7.5 (a whole byte's 16 n + n 17 times that)
-    auto centre = [&]() {
-#pragma unroll
-        for (int o = 4; o <= 16; o <<= 1) {
-            sx[0] += __shfl_xor_sync(kFullMask, sx[0], o);
-            sx[1] += __shfl_xor_sync(kFullMask, sx[1], o);
-        }
-        // H4: the first terms' columns take all of it
-        const float c = !H4 || t < 2 ? -7.5f * 0x1p-24f : 0.f;
-        sx[0] *= c;
-        sx[1] *= c;
-#pragma unroll
-        for (int a = 0; a < 4 * VW; ++a) {
-            O[a][0] += sx[0];
-            O[a][1] += sx[1];
-            O[a][2] = fmaf(17.f, sx[0], O[a][2]);
-            O[a][3] = fmaf(17.f, sx[1], O[a][3]);
-        }
-        sx[0] = sx[1] = 0.f;
-    };
+    // pm: sum of P times what the rows' codes are counted from
+    float M[2] = {0.f, 0.f}, l[2] = {0.f, 0.f}, pm[2] = {0.f, 0.f};
     int ve = -110;                  // scales of V seen so far are at most 2^ve
     float vtop = pow2i(ve);
     float fe = pow2i(7 - ve);       // weights are P s' fe, at most 2^8 2^7
@@ -572,7 +545,7 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
     // rows a quarter warp) nor the value loads (four rows a half warp) meet in
     // a bank more than they must.
     const int pr = r ^ ((r >> 1) & 1);
-    constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
+    constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u, kByte = 0x00ff00ffu;
     // offsets of position `pos` of a step in its half of a stage
     constexpr int U = B == 32 ? 16 * (D / 2) : REC;       // 16 positions on
     constexpr int PU = B == 32 ? 16 * 4 : REC;            // the same for the (s, m) pairs
@@ -627,7 +600,8 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
                 const uint32_t pv = *reinterpret_cast<const uint32_t *>(par + S::HALF);
                 const float sk = from16<BF16>(pk & 0xffffu), mk = from16<BF16>(pk >> 16);
                 sv[u][h] = from16<BF16>(pv & 0xffffu);
-                mv[u][h] = fmaf(7.5f, sv[u][h], from16<BF16>(pv >> 16));
+                mv[u][h] = from16<BF16>(pv >> 16);
+                if (u == 1) mv[u][h] = fmaf(15.f, sv[u][h], mv[u][h]);
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     s[u][2 * h + i] = fmaf(c[2 * h + i], sk * cs[i], fmaf(mk, qs[i], -M[i]));
@@ -677,7 +651,6 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
                 l[i] *= f[i];
                 pm[i] *= f[i];
                 f[i] *= shrink;
-                sx[i] *= f[i];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     s[u][i] -= up;
@@ -701,15 +674,13 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
             uint32_t bh[2], bl[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float g = sv[u][h] * fe;
+                const float g = sv[u][h] * (u == 0 ? fe : -fe);
                 const float p0 = fast_exp2(s[u][2 * h]), p1 = fast_exp2(s[u][2 * h + 1]);
                 l[0] += p0;
                 l[1] += p1;
                 pm[0] = fmaf(p0, mv[u][h], pm[0]);
                 pm[1] = fmaf(p1, mv[u][h], pm[1]);
                 const float x0 = p0 * g, x1 = p1 * g;
-                sx[0] += x0;
-                sx[1] += x1;
                 const uint32_t hi = half2_bits(x0, x1);
                 const float2 y = widen2<false>(hi);
                 const uint32_t lo = half2_bits(x0 - y.x, x1 - y.y);
@@ -744,10 +715,13 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
                     const uint32_t y = __byte_perm(v[2][j], v[3][j], sel);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        // a whole byte, 16 n(odd) + n(even), and its low half
-                        const uint32_t xb = q ? __byte_perm(x, 0u, 0x4341) : x & 0x00ff00ffu;
-                        const uint32_t yb = q ? __byte_perm(y, 0u, 0x4341) : y & 0x00ff00ffu;
-                        const uint32_t xl = (q ? xb : x) & kLo, yl = (q ? yb : y) & kLo;
+                        // a whole byte, 16 n(odd) + n(even), and its low half; of
+                        // the second 16 positions both from 255 and 15 down
+                        const uint32_t nb = u == 0 ? 0u : kByte, nl = u == 0 ? 0u : kLo;
+                        const uint32_t xb = q ? __byte_perm(x, 0u, 0x4341) ^ nb : (x & kByte) ^ nb;
+                        const uint32_t yb = q ? __byte_perm(y, 0u, 0x4341) ^ nb : (y & kByte) ^ nb;
+                        const uint32_t xl = q ? xb & kLo : (x & kLo) ^ nl;
+                        const uint32_t yl = q ? yb & kLo : (y & kLo) ^ nl;
                         float(&acc)[4] = O[4 * j + 2 * half + q];
                         mma_f16(acc, xl, xb, yl, yb, bh[0], bh[1]);
                         if constexpr (!H4) mma_f16(acc, xl, xb, yl, yb, bl[0], bl[1]);
@@ -755,9 +729,7 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
                 }
             }
         }
-        if (k % kInt4Centre<H4> == kInt4Centre<H4> - 1) centre();
     }
-    centre();
 
     // -------------------------------------------------------------- merge
     if (!arrived && lane == 0) {

@@ -299,29 +299,32 @@ def decode_fp8(out, q, k_pool, v_pool, block_tables, seq_lens, max_seq_len, scal
     return workspace
 
 
-def _addr(t, name, dev, dtype=None):
-    """Address of a dense tensor on device `dev` (its index), checked."""
-    if t.get_device() != dev or not t.is_contiguous() or (dtype is not None and t.dtype is not dtype):
-        _cuda(t, name, dtype)  # says what is wrong, or:
-        raise ValueError(f"{name} must be on the device of the other tensors (cuda:{dev})")
-    return t.data_ptr()
+# The checks below are written out in each wrapper as one condition (a call
+# costs more than the kernel of a small batch); when it fails, _explain finds
+# the argument and says what is wrong with it.
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _device_of(t, name):
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return dev
+def _explain(dev, **tensors):
+    """Raise for the first of name=(tensor, dtype or None) that is not a dense
+    CUDA tensor of that type on device `dev` (the first tensor's)."""
+    for name, (t, dtype) in tensors.items():
+        if t is None:
+            continue
+        _cuda(t, name, dtype)
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on the device of the other tensors (cuda:{dev})")
+    raise ValueError("arguments must be dense CUDA tensors on one device")
 
 
-def _on_device(dev, stream, fn, *args):
+def _run(dev, stream, fn, args):
     """fn(*args, stream handle) with `dev` current; stream None: its current
     stream."""
-    if dev != torch._C._cuda_getDevice():
+    if dev != _current_device():
         with torch.cuda.device(dev):
-            return _on_device(dev, stream, fn, *args)
-    return fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
-              else stream.cuda_stream)
+            return _run(dev, stream, fn, args)
+    return fn(*args, _current_stream(dev) if stream is None else stream.cuda_stream)
 
 
 def int4_pool_shape(num_blocks, num_kv_heads, block_size, head_dim):
@@ -335,15 +338,15 @@ def int4_pool_shape(num_blocks, num_kv_heads, block_size, head_dim):
 
 def _int4_pools(k_pool, v_pool, hkv, d):
     """(blocks, block size) of a pair of 4-bit pools."""
-    if k_pool.dtype != torch.uint8 or v_pool.dtype != torch.uint8:
+    if k_pool.dtype is not torch.uint8 or v_pool.dtype is not torch.uint8:
         raise TypeError("4-bit pools are uint8 tensors of records")
-    if k_pool.dim() != 3 or v_pool.shape != k_pool.shape or k_pool.shape[1] != hkv:
+    shape = k_pool.shape
+    if len(shape) != 3 or shape[1] != hkv or v_pool.shape != shape:
         raise ValueError(f"4-bit pools must both be [blocks, {hkv}, record bytes] (int4_pool_shape)")
-    row = d // 2 + 4
-    if k_pool.shape[2] not in (16 * row, 32 * row):
-        raise ValueError(f"a record of {k_pool.shape[2]} bytes is no block of 16 or 32 rows of "
-                         f"head_dim {d}")
-    return k_pool.shape[0], k_pool.shape[2] // row
+    bs, rest = divmod(shape[2], d // 2 + 4)
+    if rest or (bs != 16 and bs != 32):
+        raise ValueError(f"a record of {shape[2]} bytes is no block of 16 or 32 rows of head_dim {d}")
+    return shape[0], bs
 
 
 def cache_write_int4(k_new, v_new, slot_mapping, k_pool, v_pool, k_out=None, v_out=None,
@@ -352,43 +355,62 @@ def cache_write_int4(k_new, v_new, slot_mapping, k_pool, v_pool, k_out=None, v_o
     of k_new / v_new (16-bit [T, Hkv, d]) quantised with its own scale and
     minimum at its slot (int64 [T]; < 0 skips; distinct).  k_out / v_out (like
     k_new; may be k_new / v_new) receive the values the stored rows stand for."""
-    if k_new.dim() != 3 or v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
+    shape, dtype = k_new.shape, k_new.dtype
+    if len(shape) != 3 or v_new.shape != shape or v_new.dtype is not dtype:
         raise ValueError("k_new and v_new must both be [T, Hkv, d] of one type")
-    T, hkv, d = k_new.shape
+    T, hkv, d = shape
     nb, bs = _int4_pools(k_pool, v_pool, hkv, d)
     if slot_mapping.shape != (T,):
         raise ValueError("slot_mapping must be [T]")
     if (k_out is None) != (v_out is None):
         raise ValueError("k_out and v_out go together")
-    for t in (k_out, v_out):
-        if t is not None and (t.shape != k_new.shape or t.dtype != k_new.dtype):
-            raise ValueError("k_out and v_out must be like k_new")
-    dt = _dt(k_new)
-    dev = _device_of(k_new, "k_new")
-    rc = _on_device(
-        dev, stream, _lib.load().pa_cache_write_int4, _addr(k_new, "k_new", dev),
-        _addr(v_new, "v_new", dev), _addr(slot_mapping, "slot_mapping", dev, torch.int64), T,
-        _addr(k_pool, "k_pool", dev), _addr(v_pool, "v_pool", dev), nb, hkv, d, bs,
-        None if k_out is None else _addr(k_out, "k_out", dev),
-        None if v_out is None else _addr(v_out, "v_out", dev), dt)
+    code = _dt(k_new)
+    dev = k_new.get_device()
+    if not (dev >= 0 and k_new.is_contiguous() and v_new.is_contiguous()
+            and slot_mapping.is_contiguous() and k_pool.is_contiguous() and v_pool.is_contiguous()
+            and v_new.get_device() == dev and slot_mapping.get_device() == dev
+            and k_pool.get_device() == dev and v_pool.get_device() == dev
+            and slot_mapping.dtype is torch.int64):
+        _explain(dev, k_new=(k_new, None), v_new=(v_new, None),
+                 slot_mapping=(slot_mapping, torch.int64), k_pool=(k_pool, None),
+                 v_pool=(v_pool, None))
+    ko = vo = None
+    if k_out is not None:
+        for t in (k_out, v_out):
+            if t.shape != shape or t.dtype is not dtype:
+                raise ValueError("k_out and v_out must be like k_new")
+            if t.get_device() != dev or not t.is_contiguous():
+                _explain(dev, k_out=(k_out, None), v_out=(v_out, None))
+        ko, vo = k_out.data_ptr(), v_out.data_ptr()
+    rc = _run(dev, stream, _lib.load().pa_cache_write_int4,
+              (k_new.data_ptr(), v_new.data_ptr(), slot_mapping.data_ptr(), T, k_pool.data_ptr(),
+               v_pool.data_ptr(), nb, hkv, d, bs, ko, vo, code))
     _lib.check("pa_cache_write_int4", rc)
 
 
 def cache_read_int4(k_out, v_out, slot_mapping, k_pool, v_pool, stream=None):
     """Rows of 4-bit pools back as 16-bit values: k_out / v_out [T, Hkv, d]
     at slot_mapping (int64 [T]; rows of a negative slot are left alone)."""
-    if k_out.dim() != 3 or v_out.shape != k_out.shape or v_out.dtype != k_out.dtype:
+    shape, dtype = k_out.shape, k_out.dtype
+    if len(shape) != 3 or v_out.shape != shape or v_out.dtype is not dtype:
         raise ValueError("k_out and v_out must both be [T, Hkv, d] of one type")
-    T, hkv, d = k_out.shape
+    T, hkv, d = shape
     nb, bs = _int4_pools(k_pool, v_pool, hkv, d)
     if slot_mapping.shape != (T,):
         raise ValueError("slot_mapping must be [T]")
-    dt = _dt(k_out)
-    dev = _device_of(k_out, "k_out")
-    rc = _on_device(
-        dev, stream, _lib.load().pa_cache_read_int4, _addr(k_out, "k_out", dev),
-        _addr(v_out, "v_out", dev), _addr(slot_mapping, "slot_mapping", dev, torch.int64), T,
-        _addr(k_pool, "k_pool", dev), _addr(v_pool, "v_pool", dev), nb, hkv, d, bs, dt)
+    code = _dt(k_out)
+    dev = k_out.get_device()
+    if not (dev >= 0 and k_out.is_contiguous() and v_out.is_contiguous()
+            and slot_mapping.is_contiguous() and k_pool.is_contiguous() and v_pool.is_contiguous()
+            and v_out.get_device() == dev and slot_mapping.get_device() == dev
+            and k_pool.get_device() == dev and v_pool.get_device() == dev
+            and slot_mapping.dtype is torch.int64):
+        _explain(dev, k_out=(k_out, None), v_out=(v_out, None),
+                 slot_mapping=(slot_mapping, torch.int64), k_pool=(k_pool, None),
+                 v_pool=(v_pool, None))
+    rc = _run(dev, stream, _lib.load().pa_cache_read_int4,
+              (k_out.data_ptr(), v_out.data_ptr(), slot_mapping.data_ptr(), T, k_pool.data_ptr(),
+               v_pool.data_ptr(), nb, hkv, d, bs, code))
     _lib.check("pa_cache_read_int4", rc)
 
 
@@ -405,34 +427,44 @@ def decode_int4(out, q, k_pool, v_pool, block_tables, seq_lens, max_seq_len, sca
     out [S, Hq, d]; q / out 16-bit.  partition_tokens and workspace as for
     decode (a workspace allocated here is of int4_workspace_size bytes and
     tied to the stream)."""
-    if q.dim() != 3 or out.shape != q.shape or out.dtype != q.dtype:
+    shape = q.shape
+    if len(shape) != 3 or out.shape != shape or out.dtype is not q.dtype:
         raise ValueError("q and out must both be [S, Hq, d] of one type")
-    S, hq, d = q.shape
+    S, hq, d = shape
     if k_pool.dim() != 3:
         raise ValueError("4-bit pools are [blocks, Hkv, record bytes] (int4_pool_shape)")
     hkv = k_pool.shape[1]
     nb, bs = _int4_pools(k_pool, v_pool, hkv, d)
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or seq_lens.shape != (S,):
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] != S or seq_lens.shape != (S,):
         raise ValueError("block_tables must be [S, max_blocks], seq_lens [S]")
-    dt = _dt(q)
-    dev = _device_of(q, "q")
-    lib = _lib.load()
-    args = (_addr(out, "out", dev), _addr(q, "q", dev), _addr(k_pool, "k_pool", dev),
-            _addr(v_pool, "v_pool", dev), nb, _addr(block_tables, "block_tables", dev, torch.int32),
-            block_tables.shape[1], _addr(seq_lens, "seq_lens", dev, torch.int32), int(max_seq_len), S,
-            hq, hkv, d, bs, float(scale), int(partition_tokens))
+    code = _dt(q)
+    dev = q.get_device()
+    if not (dev >= 0 and q.is_contiguous() and out.is_contiguous() and k_pool.is_contiguous()
+            and v_pool.is_contiguous() and block_tables.is_contiguous() and seq_lens.is_contiguous()
+            and out.get_device() == dev and k_pool.get_device() == dev
+            and v_pool.get_device() == dev and block_tables.get_device() == dev
+            and seq_lens.get_device() == dev and block_tables.dtype is torch.int32
+            and seq_lens.dtype is torch.int32):
+        _explain(dev, q=(q, None), out=(out, None), k_pool=(k_pool, None), v_pool=(v_pool, None),
+                 block_tables=(block_tables, torch.int32), seq_lens=(seq_lens, torch.int32))
+    fn = _lib.load().pa_decode_int4
+    max_len, part = int(max_seq_len), int(partition_tokens)
+    args = (out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), nb,
+            block_tables.data_ptr(), tables[1], seq_lens.data_ptr(), max_len, S, hq, hkv, d, bs,
+            float(scale), part)
 
     def run(ws):
         if ws is None:
-            return _on_device(dev, stream, lib.pa_decode_int4, *args, None, 0, dt)
-        return _on_device(dev, stream, lib.pa_decode_int4, *args, _addr(ws, "workspace", dev),
-                          ws.nbytes, dt)
+            return _run(dev, stream, fn, args + (None, 0, code))
+        if ws.get_device() != dev or not ws.is_contiguous():
+            _explain(dev, workspace=(ws, None))
+        return _run(dev, stream, fn, args + (ws.data_ptr(), ws.nbytes, code))
 
     rc = run(workspace)
     if rc == _lib.PA_ERR_INVALID:  # perhaps for want of a workspace: nothing was launched
         with torch.cuda.device(dev):
-            need = int4_workspace_size(S, hq, hkv, d, bs, int(max_seq_len), int(partition_tokens),
-                                       q.dtype)
+            need = int4_workspace_size(S, hq, hkv, d, bs, max_len, part, q.dtype)
         if need and (workspace is None or workspace.nbytes < need):
             # from the stream's own memory: a block freed on another stream may
             # still be in use there
@@ -443,18 +475,15 @@ def decode_int4(out, q, k_pool, v_pool, block_tables, seq_lens, max_seq_len, sca
     return workspace
 
 
-def _token_rows(t, name, dev, T, heads, d):
-    """(address, elements from a token to the next) of t [T, heads, d] whose
-    heads are dense."""
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of the others (cuda:{dev})")
-    own = heads * d
+def _token_step(t, name, T, own, d):
+    """Elements from a token to the next of t [T, heads, d] whose heads, `own`
+    elements, are dense."""
     step, head, one = t.stride()
     if T <= 1:
         step = own
-    if one != 1 or (heads > 1 and head != d) or step < own:
+    if one != 1 or (head != d and own != d) or step < own:
         raise ValueError(f"{name}: each token's heads must be dense and apart from the next's")
-    return t.data_ptr(), step
+    return step
 
 
 def qk_norm_rope(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, positions, slot_mapping, k_pool,
@@ -466,50 +495,66 @@ def qk_norm_rope(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, positions, sl
     positions, slot_mapping int64 [T].  The pools' form is theirs: like q
     [NB, Hkv, B, d], E4M3 codes (uint8, the same shape, with k_scale and
     v_scale) or 4-bit records (uint8, int4_pool_shape)."""
-    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or q_out.shape != q.shape:
+    qs, ks_, dt = q.shape, k.shape, q.dtype
+    if len(qs) != 3 or len(ks_) != 3 or v.shape != ks_ or q_out.shape != qs or ks_[0] != qs[0] \
+            or ks_[2] != qs[2]:
         raise ValueError("q and q_out must be [T, Hq, d], k and v [T, Hkv, d]")
-    T, hq, d = q.shape
-    hkv = k.shape[1]
-    if k.shape[0] != T or k.shape[2] != d:
-        raise ValueError("q and q_out must be [T, Hq, d], k and v [T, Hkv, d]")
-    dt = q.dtype
-    if not (dt == k.dtype == v.dtype == q_out.dtype == q_weight.dtype == k_weight.dtype):
+    T, hq, d = qs
+    hkv = ks_[1]
+    if not (k.dtype is dt and v.dtype is dt and q_out.dtype is dt and q_weight.dtype is dt
+            and k_weight.dtype is dt):
         raise TypeError("q, q_out, k, v and the weights must have one type")
     if q_weight.shape != (d,) or k_weight.shape != (d,):
         raise ValueError("the weights must be [head_dim]")
     if positions.shape != (T,) or slot_mapping.shape != (T,):
         raise ValueError("positions and slot_mapping must be [T]")
+    table = cos_sin.shape
+    if len(table) != 2:
+        raise ValueError("cos_sin must be [positions, rotary_dim]")
     ks = vs = 1.0
-    if k_pool.dtype == torch.uint8 and k_pool.dim() == 3:
+    pool = k_pool.shape
+    if len(pool) == 3:
         fmt = _lib.PA_KV_INT4
         nb, bs = _int4_pools(k_pool, v_pool, hkv, d)
     else:
-        if k_pool.dim() != 4 or v_pool.shape != k_pool.shape or k_pool.shape[1] != hkv \
-                or k_pool.shape[3] != d:
+        if len(pool) != 4 or v_pool.shape != pool or pool[1] != hkv or pool[3] != d:
             raise ValueError(f"pools must both be [blocks, {hkv}, block size, {d}] or 4-bit records")
-        nb, _, bs, _ = k_pool.shape
-        if k_pool.dtype == torch.uint8 and v_pool.dtype == torch.uint8:
+        nb, bs = pool[0], pool[2]
+        if k_pool.dtype is dt and v_pool.dtype is dt:
+            fmt = _lib.PA_KV_16BIT
+        elif k_pool.dtype is torch.uint8 and v_pool.dtype is torch.uint8:
             fmt = _lib.PA_KV_E4M3
             if k_scale is None or v_scale is None:
                 raise ValueError("E4M3 pools need k_scale and v_scale")
             ks, vs = float(k_scale), float(v_scale)
-        elif k_pool.dtype == dt and v_pool.dtype == dt:
-            fmt = _lib.PA_KV_16BIT
         else:
             raise TypeError("pools must have q's type or be uint8 codes")
-    if cos_sin.dim() != 2:
-        raise ValueError("cos_sin must be [positions, rotary_dim]")
     code = _dt(q)
-    dev = _device_of(q, "q")
-    rc = _on_device(
-        dev, stream, _lib.load().pa_qk_norm_rope, *_token_rows(q_out, "q_out", dev, T, hq, d),
-        *_token_rows(q, "q", dev, T, hq, d), *_token_rows(k, "k", dev, T, hkv, d),
-        *_token_rows(v, "v", dev, T, hkv, d), _addr(q_weight, "q_weight", dev),
-        _addr(k_weight, "k_weight", dev), float(eps), _addr(cos_sin, "cos_sin", dev, torch.float32),
-        cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)),
-        _addr(positions, "positions", dev, torch.int64),
-        _addr(slot_mapping, "slot_mapping", dev, torch.int64), T, _addr(k_pool, "k_pool", dev),
-        _addr(v_pool, "v_pool", dev), nb, hq, hkv, d, bs, fmt, ks, vs, code)
+    dev = q.get_device()
+    if not (dev >= 0 and k.get_device() == dev and v.get_device() == dev
+            and q_out.get_device() == dev and q_weight.get_device() == dev
+            and k_weight.get_device() == dev and cos_sin.get_device() == dev
+            and positions.get_device() == dev and slot_mapping.get_device() == dev
+            and k_pool.get_device() == dev and v_pool.get_device() == dev
+            and q_weight.is_contiguous() and k_weight.is_contiguous() and cos_sin.is_contiguous()
+            and positions.is_contiguous() and slot_mapping.is_contiguous()
+            and k_pool.is_contiguous() and v_pool.is_contiguous()
+            and cos_sin.dtype is torch.float32 and positions.dtype is torch.int64
+            and slot_mapping.dtype is torch.int64):
+        for name, t in (("q", q), ("k", k), ("v", v), ("q_out", q_out)):  # may be strided
+            if t.get_device() != dev or dev < 0:
+                raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
+        _explain(dev, q_weight=(q_weight, None), k_weight=(k_weight, None),
+                 cos_sin=(cos_sin, torch.float32), positions=(positions, torch.int64),
+                 slot_mapping=(slot_mapping, torch.int64), k_pool=(k_pool, None),
+                 v_pool=(v_pool, None))
+    rc = _run(dev, stream, _lib.load().pa_qk_norm_rope,
+              (q_out.data_ptr(), _token_step(q_out, "q_out", T, hq * d, d), q.data_ptr(),
+               _token_step(q, "q", T, hq * d, d), k.data_ptr(), _token_step(k, "k", T, hkv * d, d),
+               v.data_ptr(), _token_step(v, "v", T, hkv * d, d), q_weight.data_ptr(),
+               k_weight.data_ptr(), float(eps), cos_sin.data_ptr(), table[0], table[1],
+               1 if interleaved else 0, positions.data_ptr(), slot_mapping.data_ptr(), T,
+               k_pool.data_ptr(), v_pool.data_ptr(), nb, hq, hkv, d, bs, fmt, ks, vs, code))
     _lib.check("pa_qk_norm_rope", rc)
 
 

@@ -42,7 +42,7 @@ struct NormRopeParams {
     int *err;
 };
 
-constexpr int kNormRopeThreads = 128;
+constexpr int kNormRopeThreads = 64;
 
 // 8 fp32 values as four packed pairs.
 struct Chunk {
@@ -73,8 +73,15 @@ __device__ __forceinline__ float2 neg2(float2 x) { return make_float2(-x.x, -x.y
 // (chunk c with chunk c + D/16); halves of a part of it.
 enum RopeKind { kRopePairs, kRopeWhole, kRopePart };
 
+// CTAs an SM, at least: two warps of 64 registers a thread (16,411 tokens of 32 +
+// 8 + 8 heads of 128: 69.6 us; four warps a CTA 71 to 73 us, 80 registers 77 us,
+// 48 registers 76 us); up to 96 where 64 would spill, for the quantiser (85 us)
+// and the shuffles of partly rotated heads (83 us, 105 with 64).
+template <int FMT, int ROPE>
+constexpr int kNormRopeCtas = FMT == PA_KV_INT4 || ROPE == kRopePart ? 10 : 16;
+
 template <bool BF16, int D, int FMT, int ROPE>
-__global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(
+__global__ void __launch_bounds__(kNormRopeThreads, (kNormRopeCtas<FMT, ROPE>)) norm_rope_kernel(
     const __grid_constant__ NormRopeParams p) {
     constexpr int LANES = D / 16, GROUPS = kNormRopeThreads / LANES;
     const int c = threadIdx.x % LANES, g = threadIdx.x / LANES;
@@ -98,7 +105,12 @@ __global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(
         }
         return x;
     };
-    Row next = load(first + g);
+    // heads ahead in flight: two where fewer CTAs share an SM and the quantiser
+    // does not set the pace (half the head turned: 83 us for 98 with one)
+    constexpr int AHEAD = kNormRopeCtas<FMT, ROPE> < 16 && FMT != PA_KV_INT4 ? 2 : 1;
+    Row next[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) next[i] = load(first + i * GROUPS + g);
     const int64_t pos = p.positions[t];
     int64_t slot = p.slots[t];
     if (pos < 0 || pos >= p.num_positions) {  // the same for the whole CTA
@@ -160,8 +172,9 @@ __global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(
         const int r = r0 + g;
         const bool live = r < last;
         const int kind = r < nq ? 0 : r < nq + nk ? 1 : 2;
-        const Row raw = next;
-        next = load(r + GROUPS);
+        const Row raw = next[0];
+        if (AHEAD > 1) next[0] = next[AHEAD - 1];
+        next[AHEAD - 1] = load(r + AHEAD * GROUPS);
         uint4 y16[2] = {raw.v[0], raw.v[1]};
         if (__any_sync(kFullMask, live && kind < 2)) {
             Chunk x[2];
@@ -203,24 +216,35 @@ __global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(
                                                __fmul2_rn(make_float2(a.y, a.x), sn[i].p[j]));
                     }
             } else {
-                // chunk k is half k / LANES of lane k % LANES; a chunk of the
-                // second half turns with one of the first only
+                // chunk k is half k / LANES of lane k % LANES
                 const int base = (threadIdx.x & 31) - c;
                 const int from0 = base + partner[0] % LANES, from1 = base + partner[1] % LANES;
-                auto both = [&](float a, float b, float *q0, float *q1) {
-                    const float u = __shfl_sync(kFullMask, a, from0);
-                    const float w = __shfl_sync(kFullMask, b, from0);
-                    const float v = __shfl_sync(kFullMask, a, from1);
-                    *q0 = partner[0] < LANES ? u : w;
-                    *q1 = v;  // (where chunk c + LANES does not turn its sine is 0)
-                };
+                if (2 * hc <= LANES) {  // at most half the head turns: first halves only
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float2 q0, q1;
-                    both(x[0].p[j].x, x[1].p[j].x, &q0.x, &q1.x);
-                    both(x[0].p[j].y, x[1].p[j].y, &q0.y, &q1.y);
-                    z[0].p[j] = __ffma2_rn(x[0].p[j], cs[0].p[j], __fmul2_rn(q0, sn[0].p[j]));
-                    z[1].p[j] = __ffma2_rn(x[1].p[j], cs[1].p[j], __fmul2_rn(q1, sn[1].p[j]));
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 q =
+                            make_float2(__shfl_sync(kFullMask, x[0].p[j].x, from0),
+                                        __shfl_sync(kFullMask, x[0].p[j].y, from0));
+                        z[0].p[j] = __ffma2_rn(x[0].p[j], cs[0].p[j], __fmul2_rn(q, sn[0].p[j]));
+                        z[1].p[j] = x[1].p[j];
+                    }
+                } else {
+                    // a chunk of the second half turns with one of the first (where
+                    // it does not turn its sine is 0)
+                    auto both = [&](float a, float b, float *q0, float *q1) {
+                        const float u = __shfl_sync(kFullMask, a, from0);
+                        const float w = __shfl_sync(kFullMask, b, from0);
+                        *q0 = partner[0] < LANES ? u : w;
+                        *q1 = __shfl_sync(kFullMask, a, from1);
+                    };
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float2 q0, q1;
+                        both(x[0].p[j].x, x[1].p[j].x, &q0.x, &q1.x);
+                        both(x[0].p[j].y, x[1].p[j].y, &q0.y, &q1.y);
+                        z[0].p[j] = __ffma2_rn(x[0].p[j], cs[0].p[j], __fmul2_rn(q0, sn[0].p[j]));
+                        z[1].p[j] = __ffma2_rn(x[1].p[j], cs[1].p[j], __fmul2_rn(q1, sn[1].p[j]));
+                    }
                 }
             }
             if (kind < 2) {

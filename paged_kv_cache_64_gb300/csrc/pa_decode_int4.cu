@@ -26,11 +26,20 @@
 // sums about zero.  (Without it a mean over 120,000 positions in one warp's sum
 // was off by 9e-2 of itself; with it by 2.0e-4, which is f16's own rounding.)
 //
-// Why not tcgen05: its A operand comes from shared memory, where codes would
-// have to be stored again as 8- or 16-bit values, four to eight times the
+// Why not tcgen05: its operands come from shared or tensor memory, where codes
+// would have to be stored again as 8- or 16-bit values, two to four times the
 // bytes that were read, and its smallest tile is 64 rows of a CTA-wide
-// pipeline; with 8 columns a position costs a warp one MMA here (K and V
-// together two), and the masks feed it from the registers the loads filled.
+// pipeline; with 8 columns 16 positions cost a warp 24 MMAs here (16 with up to
+// four heads), and the masks feed them from the registers the loads filled.
+//
+// Bounds: 136 bytes a position and KV head (D = 128).  256 sequences of 32 + 8
+// heads and 513 to 8192 positions: 215 us, 5.7 TB/s, 84% of the copy rate; 16 of
+// 64 + 8 heads and 16,385 to 32,768: 94 us, 67%; one of 200,003: 46 us, 69%.  The
+// first without its arithmetic takes 191 us.  No pipe is full (ALU 54%, issue 50%,
+// matrix unit 25% of cycles; eight heads: 50, 48 and 36%), but neither fewer
+// instructions (12 of 240 for 16 positions: 1%) nor more warps (five or six CTAs an
+// SM with the queries in shared memory: 12 to 39% slower) nor the next keys'
+// products beside this step's values (4 to 7% slower) bring them together better.
 //
 // A warp works alone: every fourth 32 positions of the CTA's piece, its own
 // ring of stages filled by bulk copies of whole records, its own running
@@ -46,8 +55,8 @@ namespace pa {
 
 constexpr int kInt4Warps = 4;
 constexpr int kInt4MaxG = 8;
+constexpr int kInt4Step = 32;  // positions a warp takes at a time: two score tiles
 
-constexpr int kInt4Step = 32;   // positions a warp takes at a time: two score tiles
 template <int D>
 struct Int4Shape {
     static constexpr int HALF = kInt4Step * (D / 2 + 4);  // a step's K (or V) records
@@ -89,17 +98,18 @@ __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) { return narrow2<false>(a, b); }
 
 // Balanced ranges (automatic partitions).  The heads go in bundles of up to 8:
-// as many consecutive CTAs take the same positions of a bundle's heads at about
-// the same time, so that the records of a block, which lie together, are read
-// together.  The work is one line of units of 128 positions, sequence by sequence
-// and bundle by bundle; group c of CTAs takes the units from bound(c) to
-// bound(c + 1), moved to the next head's border where
-// that is at most `slack` units away, so that no head is cut for a sliver.  Every
-// CTA works the line out from the lengths (one load and a scan), whatever they
-// are.  A first wave of groups takes equal large shares; a second, of smaller
-// shares, is started as the first ends, which the SMs do not do together (equal
-// shares in one wave alone ended between 138 and 222 us).  The partials of heads
-// that bounds cut are merged by a second kernel.
+// as many consecutive CTAs, a group, take the same positions of a bundle's heads
+// at about the same time, so that the records of a block, which lie together, are
+// read together (a small gain: 93.8 -> 93.3 us for 16 long sequences).  The work is
+// one line of units of 128 positions, sequence by sequence and bundle by bundle;
+// group c takes the units from bound(c) to bound(c + 1), moved to the next head's
+// border where that is at most `slack` units away, so that no head is cut for a
+// sliver.  Every CTA works the line out from the lengths (one load and a scan),
+// whatever they are.  A first wave of groups takes equal large shares; a second,
+// of smaller shares, is started as the first ends, which the SMs do not do
+// together (equal shares in one wave alone ended between 138 and 222 us).  The
+// partials of heads that bounds cut are merged by a second kernel.
+
 // A group's range: units [unit, end) of the line.  Its next unit is unit `at`
 // of the n units of bundle `bundle` of sequence seq.
 struct Int4Range {
@@ -408,7 +418,8 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
             piece.seq = seq;
             piece.kvh = kvh;
             piece.start = chunk * P;
-            piece.count = L == 0 ? (chunk == 0 ? 0 : -1) : max(min(L - chunk * P, P), -1);
+            const int left = L - chunk * P;
+            piece.count = left > 0 ? min(left, P) : L == 0 && chunk == 0 ? 0 : -1;
             piece.nparts = L == 0 ? 1 : (L - 1) / P + 1;
             piece.slot = chunk;
         }
@@ -430,7 +441,7 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::BARS) + warp * S::STAGES;
     const int G = p.group;
     const int seq = piece.seq, kvh = piece.kvh, start = piece.start, count = piece.count;
-    if (count == 0) {  // a sequence without tokens
+    if (count == 0) {  // a sequence without tokens (chunk 0 of it)
         uint16_t *out = static_cast<uint16_t *>(p.out) + ((int64_t)seq * p.num_q_heads + kvh * G) * D;
         for (int i = threadIdx.x; i < G * D; i += blockDim.x) out[i] = 0;
         return;

@@ -431,3 +431,21 @@ def test_small_outputs_of_a_long_sequence_keep_their_digits(hkv, group):
     assert np.linalg.norm(out - ref) <= 2.0**-11 * np.linalg.norm(ref)
     one = int4.widen(bits(c.gpu(-1)), "f16")  # 940 steps of a warp in one sum
     assert np.linalg.norm(one - ref) <= 2.0**-11 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("d,block", [(64, 16), (128, 32)])
+def test_more_sequences_than_a_compact_grid(d, block):
+    """Over 128 sequences a CTA stands for every chunk of the longest; chunks
+    that begin at a sequence's end must not touch its output."""
+    lens = [0, 64, 128, 192, 1, 63, 65, 127, 129, 191] * 14
+    c = Case(lens, 2, 3, d, block, "f16", seed=d)
+    for partition in (64, 128, -1, 0):
+        c.check(c.gpu(partition), partition)
+
+
+def test_more_sequences_than_balanced_ranges_take():
+    lens = [3, 0, 17, 1, 40] * 210
+    lens[7], lens[1000], lens[1049] = 2048, 1500, 1024
+    c = Case(lens, 1, 4, 64, 16, "bf16")
+    c.check(c.gpu(0))
+    c.check(c.gpu(512))

@@ -449,3 +449,32 @@ def test_more_sequences_than_balanced_ranges_take():
     c = Case(lens, 1, 4, 64, 16, "bf16")
     c.check(c.gpu(0))
     c.check(c.gpu(512))
+
+
+def test_a_captured_call_follows_the_lengths():
+    """The lengths are read on the device: a graph captured once serves them as
+    they grow and shrink under the maximum it was captured with."""
+    c = Case([3000, 2900, 1500, 10], 2, 4, 64, 16, "f16", seed=3)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    c.gpu(0, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = c.gpu(0, workspace=ws)
+    for lens in ([3000, 2900, 1500, 10], [1, 2900, 0, 10], [0, 0, 0, 0], [2999, 17, 1500, 1]):
+        c.lens = np.asarray(lens, np.int32)
+        c.gl.copy_(torch.as_tensor(c.lens))
+        g.replay()
+        c.check(out, lens)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 4.0, 1e-6])
+def test_scales_of_every_kind(scale):
+    c = Case([700, 2000, 3], 2, 4, 64, 16, "f16", seed=4)
+    c.scale = scale
+    ref = c.oracle()
+    c.scale = abs(scale)  # the bound on a score goes by its size
+    tol = c.allowed(ref)
+    c.scale = scale
+    for partition in (0, -1):
+        assert (np.abs(int4.widen(bits(c.gpu(partition)), "f16") - ref) <= tol).all()

@@ -183,3 +183,24 @@ def test_captured_and_replayed():
         fresh = [torch.zeros_like(p) for p in pools]
         api.cache_write_int4(k, k, slots, *fresh, k_out=a, v_out=b)
         assert torch.equal(ko, a) and torch.equal(vo, b)
+
+
+@pytest.mark.parametrize("hkv", [5, 7, 12, 31, 33, 100])
+def test_every_row_finds_its_token(hkv):
+    """Row to token and head for head counts that are no power of two."""
+    T, d, block = 67, 64, 16
+    nb = -(-T // block) + 1
+    k = torch.arange(T * hkv, device="cuda").view(T, hkv, 1).expand(T, hkv, d)
+    k = (k % 2048).to(torch.float16).contiguous()  # rows of one value each: exact
+    v = (k + 1).contiguous()
+    slots = torch.randperm(nb * block, device="cuda")[:T]
+    pools = [torch.zeros(api.int4_pool_shape(nb, hkv, block, d), dtype=torch.uint8, device="cuda")
+             for _ in range(2)]
+    api.cache_write_int4(k, v, slots, *pools)
+    rows = [int4.values(p.cpu().numpy(), d, block, "f16") for p in pools]
+    at = slots.cpu().numpy()
+    for got, want in zip(rows, (k, v)):
+        assert np.array_equal(got[at // block, :, at % block], want.double().cpu().numpy())
+    a, b = torch.empty_like(k), torch.empty_like(v)
+    api.cache_read_int4(a, b, slots, *pools)
+    assert torch.equal(a, k) and torch.equal(b, v)

@@ -804,7 +804,6 @@ struct ResolvedDecode {
     int part_tokens;  // the partition size asked for (or chosen when automatic)
     bool fp8 = false;  // E4M3 pools: the E4M3 variants of the tensor-core kernel
     int span = 1;      // partitions per CTA (tensor-core kernel); grid.x = ceil(NP / span)
-    bool int4 = false;  // 4-bit pools: the kernel of pa_decode_int4.cu
 };
 
 // Scales of E4M3 pools (element = scale * code value).
@@ -829,8 +828,7 @@ static bool use_tensor_cores(int head_dim, int group) {
 
 static pa_status resolve(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                          int block_size, int max_seq_len, int partition_tokens, pa_dtype dtype,
-                         ResolvedDecode *r, bool fp8 = false, bool merge_span = true,
-                         bool int4 = false) {
+                         ResolvedDecode *r, bool fp8 = false, bool merge_span = true) {
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_seq_len < 0)
         return PA_ERR_INVALID;
     if (num_seqs > 65535 || num_kv_heads > 65535) return PA_ERR_INVALID;  // grid y and z
@@ -841,16 +839,14 @@ static pa_status resolve(int num_seqs, int num_q_heads, int num_kv_heads, int he
     if (G > 8 || (head_dim != 64 && head_dim != 128) || (block_size != 16 && block_size != 32))
         return PA_ERR_UNSUPPORTED;
     if (!pick_decode(dtype, head_dim, group_pad(G), &r->entry)) return PA_ERR_UNSUPPORTED;
-    r->tc = use_tensor_cores(head_dim, G) && !int4;
+    r->tc = use_tensor_cores(head_dim, G);
     r->fp8 = fp8;
-    r->int4 = int4;
     if (fp8 && !fp8_supported(head_dim, G)) return PA_ERR_UNSUPPORTED;
     r->bf16 = dtype == PA_BF16;
     r->head_dim = head_dim;
     int P = partition_tokens;
     if (P == 0) {
         const int per_sm = r->fp8  ? fp8_ctas_per_sm(dtype == PA_BF16, head_dim, G)
-                           : r->int4 ? int4_ctas_per_sm(dtype == PA_BF16, head_dim, block_size, G)
                            : r->tc ? tc_ctas_per_sm(dtype == PA_BF16, head_dim)
                                    : decode_ctas_per_sm(r->entry);
         P = auto_partition(num_seqs, num_kv_heads, max_seq_len, per_sm, block_size, 4.0, 512);
@@ -917,8 +913,6 @@ static pa_status launch_decode(const ResolvedDecode &r, DecodeParams prm, int nu
         prm.one_wave = (r.tc || r.fp8) &&
                        (int64_t)chunks * num_kv_heads * num_seqs <= (int64_t)sm_count() * per_sm;
     }
-    if (r.int4)
-        return launch_decode_int4(prm, r.bf16, r.head_dim, chunks, num_kv_heads, num_seqs, stream);
     if (r.fp8) {
         if (prm.prefix_parts) return PA_ERR_UNSUPPORTED;  // no cascade over E4M3 pools
         prm.span = span;
@@ -994,13 +988,13 @@ static pa_status decode_impl(void *out, const void *q, const void *k_new, const 
                              int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                              float scale, int partition_tokens, void *workspace,
                              size_t workspace_bytes, pa_dtype dtype, void *stream,
-                             const KvFp8 *fp8 = nullptr, bool int4 = false) {
+                             const KvFp8 *fp8 = nullptr) {
     ResolvedDecode r;
     if (fp8 && (!(fp8->k_scale > 0.f) || !(fp8->v_scale > 0.f) || !std::isfinite(fp8->k_scale) ||
                 !std::isfinite(fp8->v_scale)))
         return PA_ERR_INVALID;
     pa_status st = resolve(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
-                           max_seq_len, partition_tokens, dtype, &r, fp8 != nullptr, true, int4);
+                           max_seq_len, partition_tokens, dtype, &r, fp8 != nullptr);
     if (st != PA_OK) return st;
     if (num_seqs > 0 && (!out || !aligned16(out))) return PA_ERR_INVALID;
     DecodeParams prm;
@@ -1068,36 +1062,6 @@ static pa_status decode_impl(void *out, const void *q, const void *k_new, const 
                    rp) != cudaSuccess)
         return PA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
-}
-
-// Balanced ranges of pa_decode_int4 (automatic partitions): the launch's CTAs
-// (groups of the first wave, heads of a bundle) and the workspace: m, l [slot][8], O [slot][G][d] for
-// two slots a CTA.
-struct Int4Balance {
-    int ctas;
-    int wave;
-    int bundle;
-    WorkspaceLayout ws;
-};
-static bool int4_balance(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
-                         int block_size, int max_seq_len, pa_dtype dtype, Int4Balance *b) {
-    const int G = num_q_heads / num_kv_heads;
-    b->ctas = int4_balanced_ctas(dtype == PA_BF16, head_dim, block_size, G, num_seqs, num_kv_heads,
-                                 max_seq_len, &b->wave, &b->bundle);
-    if (num_seqs == 0) return b->ws = {}, true;
-    if (b->ctas <= 0) return false;
-    const size_t slots = 2 * (size_t)b->ctas;
-    b->ws = {};
-    b->ws.l_off = align256(slots * 8 * sizeof(float));
-    b->ws.o_off = 2 * b->ws.l_off;
-    b->ws.bytes = b->ws.o_off + align256(slots * G * head_dim * sizeof(float));
-    return true;
-}
-
-// Partition size of the batches that balanced ranges are not for: single pass
-// for short heads, the other decodes' choice otherwise.
-static int int4_partition(int partition_tokens, int max_seq_len) {
-    return partition_tokens == 0 && max_seq_len <= kInt4SinglePass ? -1 : partition_tokens;
 }
 
 // Shared-prefix (cascade) decode: chunking of the prefix pass and the tail
@@ -1225,61 +1189,6 @@ pa_status pa_decode_fp8(void *out, const void *q, const void *k_new, const void 
                        block_tables, max_blocks_per_seq, seq_lens, max_seq_len, num_seqs,
                        num_q_heads, num_kv_heads, head_dim, block_size, scale, partition_tokens,
                        workspace, workspace_bytes, dtype, stream, &fp8);
-}
-
-size_t pa_decode_int4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
-                                     int block_size, int max_seq_len, int partition_tokens,
-                                     pa_dtype dtype) {
-    ResolvedDecode r;
-    Int4Balance b;
-    if (partition_tokens == 0 &&
-        resolve(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len, -1, dtype, &r,
-                false, true, true) == PA_OK &&
-        int4_balance(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len, dtype,
-                     &b))
-        return b.ws.bytes;
-    if (resolve(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len,
-                int4_partition(partition_tokens, max_seq_len), dtype, &r, false, true, true) != PA_OK)
-        return 0;
-    if (r.P <= 0) return 0;
-    return workspace_layout(num_seqs, num_q_heads, head_dim, r.NP, num_kv_heads).bytes;
-}
-
-pa_status pa_decode_int4(void *out, const void *q, const void *k_pool, const void *v_pool,
-                         int num_blocks, const int32_t *block_tables, int max_blocks_per_seq,
-                         const int32_t *seq_lens, int max_seq_len, int num_seqs, int num_q_heads,
-                         int num_kv_heads, int head_dim, int block_size, float scale,
-                         int partition_tokens, void *workspace, size_t workspace_bytes,
-                         pa_dtype dtype, void *stream) {
-    Int4Balance b;
-    ResolvedDecode r;
-    if (partition_tokens != 0 ||
-        resolve(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len, -1, dtype, &r,
-                false, true, true) != PA_OK ||
-        !int4_balance(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len, dtype,
-                      &b))
-        return decode_impl(out, q, nullptr, nullptr, nullptr, k_pool, v_pool, num_blocks,
-                           block_tables, max_blocks_per_seq, seq_lens, max_seq_len, num_seqs,
-                           num_q_heads, num_kv_heads, head_dim, block_size, scale,
-                           int4_partition(partition_tokens, max_seq_len), workspace, workspace_bytes,
-                           dtype, stream, nullptr, true);
-    if (num_seqs > 0 && (!out || !aligned16(out))) return PA_ERR_INVALID;
-    DecodeParams prm;
-    const pa_status st = fill_common(&prm, q, k_pool, v_pool, num_blocks, block_tables,
-                                     max_blocks_per_seq, seq_lens, max_seq_len, num_seqs,
-                                     num_q_heads, num_kv_heads, block_size, scale);
-    if (st != PA_OK || num_seqs == 0) return st;
-    prm.out = out;
-    prm.balanced = b.wave;
-    prm.bundle = b.bundle;
-    if (!workspace || workspace_bytes < b.ws.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255))
-        return PA_ERR_INVALID;
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
-    prm.part_m = reinterpret_cast<float *>(ws + b.ws.m_off);
-    prm.part_l = reinterpret_cast<float *>(ws + b.ws.l_off);
-    prm.part_o = reinterpret_cast<float *>(ws + b.ws.o_off);
-    return launch_decode_int4(prm, dtype == PA_BF16, head_dim, b.ctas, num_kv_heads, num_seqs,
-                              as_stream(stream));
 }
 
 pa_status pa_decode_step(void *out, const void *q, const void *k_new, const void *v_new,

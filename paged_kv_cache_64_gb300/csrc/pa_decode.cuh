@@ -84,11 +84,6 @@ struct DecodeParams {
     float k_inv;
     float v_inv;
     float v_scale;
-    // 4-bit pools: balanced ranges instead of chunks (pa_decode_int4.cu);
-    // part_m, part_l and part_o are then laid out by its slots, and this is the
-    // number of groups of CTAs in the first wave; a group takes `bundle` heads.
-    int balanced;
-    int bundle;
 };
 
 // Length of sequence i, clamped to what the launch covers; a value out of
@@ -568,16 +563,6 @@ bool fp8_supported(int head_dim, int group);
 int fp8_ctas_per_sm(bool bf16, int head_dim, int group);
 pa_status launch_decode_fp8(const DecodeParams &prm, bool bf16, int head_dim, int num_partitions,
                             int num_kv_heads, int num_seqs, cudaStream_t stream);
-
-constexpr int kInt4SinglePass = 1024;  // 4-bit pools: longer heads may be cut
-
-// Decode over 4-bit pools (pa_decode_int4.cu); the pool pointers of prm are
-// those of the records.
-int int4_ctas_per_sm(bool bf16, int head_dim, int block_size, int group);
-int int4_balanced_ctas(bool bf16, int head_dim, int block_size, int group, int num_seqs,
-                       int num_kv_heads, int max_seq_len, int *wave, int *bundle);
-pa_status launch_decode_int4(const DecodeParams &prm, bool bf16, int head_dim, int num_partitions,
-                             int num_kv_heads, int num_seqs, cudaStream_t stream);
 
 // Prefix pass of the shared-prefix (cascade) decode (pa_cascade.cu): the
 // positions [0, prefix_len) that every sequence reaches through the same

@@ -44,7 +44,9 @@
 // A warp works alone: every fourth 32 positions of the CTA's piece, its own
 // ring of stages filled by bulk copies of whole records, its own running
 // maximum and sums; the four warps merge at the end through shared memory.
+#include <cmath>
 #include <cstdint>
+#include <cstring>
 #include <mutex>
 
 #include "pa_decode.cuh"
@@ -52,6 +54,13 @@
 #include "pa_internal.h"
 
 namespace pa {
+
+// The parameters the decodes share (the pools are those of the records; the
+// counters, flags and the fused write are not used), and:
+struct Int4Params : DecodeParams {
+    int balanced;  // balanced ranges: groups of CTAs in the first wave (0: chunks)
+    int bundle;    // heads of a group
+};
 
 constexpr int kInt4Warps = 4;
 constexpr int kInt4MaxG = 8;
@@ -128,6 +137,7 @@ struct Int4Piece {
 };
 
 constexpr int kInt4Unit = kInt4Step * kInt4Warps;  // positions
+constexpr int kInt4SinglePass = 1024;              // positions: longer heads may be cut
 constexpr int kInt4MinShare = 4;                   // units: smaller shares cost more than they save
 constexpr int kInt4MinSlack = 2;
 // A second wave pays where its shares are still long next to a CTA's start (2 us
@@ -136,9 +146,9 @@ constexpr int kInt4MinSlack = 2;
 constexpr int kInt4SecondWave = 64;  // units a slot from which on there is one,
 constexpr int kInt4SecondPart = 5;   //   with a fifth of the work,
 constexpr int kInt4SecondCtas = 2;   //   in twice as many groups
-constexpr int kInt4BalancedSeqs = 1024;            // longer batches: a CTA an item, by the hardware
+constexpr int kInt4BalancedSeqs = 1024;  // sequences
 
-__device__ __forceinline__ int int4_units(const DecodeParams &p, int seq) {
+__device__ __forceinline__ int int4_units(const Int4Params &p, int seq) {
     return (item_len(p, seq, false) + kInt4Unit - 1) / kInt4Unit;
 }
 
@@ -161,7 +171,7 @@ __device__ __forceinline__ int int4_parts(const Int4Range &r, int *first) {
 // bundle of the batch, with n = 0 for one without positions.  Called by all T
 // threads of the block; ends synchronised.
 template <int T>
-__device__ __forceinline__ void int4_plan(const DecodeParams &p, int ngroups, int group, int index,
+__device__ __forceinline__ void int4_plan(const Int4Params &p, int ngroups, int group, int index,
                                           Int4Range *range) {
     const int wave = p.balanced;
     __shared__ int sums[T / 32];
@@ -247,7 +257,7 @@ __device__ __forceinline__ void int4_plan(const DecodeParams &p, int ngroups, in
 }
 
 // The next piece of the range (one thread).
-__device__ __forceinline__ void int4_next_piece(const DecodeParams &p, Int4Range *range,
+__device__ __forceinline__ void int4_next_piece(const Int4Params &p, Int4Range *range,
                                              Int4Piece *piece) {
     Int4Range &r = *range;
     if (r.unit >= r.end) {
@@ -274,42 +284,65 @@ __device__ __forceinline__ void int4_next_piece(const DecodeParams &p, Int4Range
     r.at += units;
 }
 
-// Partials of the balanced ranges: a CTA leaves at most two, of the head its
-// range starts inside of (slot 2 blockIdx.x) and of the one it ends inside of, if
-// that one starts in it (the slot after): m, l [slot][8] and O [slot][G][D].
+// Partials, m, l [slot][8] and O [slot][G][D].  Balanced ranges: a CTA leaves at
+// most two, of the head its range starts inside of (slot 2 blockIdx.x) and of the
+// one it ends inside of, if that one starts in it (the slot after).  Chunks: chunk
+// c of a head has slot head * num_partitions + c.
 //
 // The merge: out = sum_k w_k O_k / sum_k w_k, w_k = l_k 2^(m_k - max m), over the
-// n partials of every head that bounds cut.  Few heads (HEADS, cut into many
-// partials each): a block a query head, its threads four dimensions each of
-// every SLICES-th partial.  Many heads: a block a bound and head of the bundle, at
-// work if that bound is the first inside the head, its threads four dimensions each of all partials of
-// one or two query heads.  A thread has eight partials' loads in flight and
-// keeps its own running maximum, so nothing waits for the maxima first.
-constexpr int kInt4MergeHeads = 512, kInt4MergeBounds = 128;  // threads
+// n partials of every head that was cut.  Few heads (kMergeHeads, many partials
+// each): a block a query head, its threads four dimensions each of every
+// SLICES-th partial.  Many heads: a block a bound and head of the bundle
+// (kMergeBounds; at work if that bound is the first inside the head) or a block a
+// head (kMergeChunks), its threads four dimensions each of all partials of one or
+// two query heads.  A thread has eight partials' loads in flight and keeps its own
+// running maximum, so nothing waits for the maxima first.
+enum Int4MergeKind { kMergeHeads, kMergeBounds, kMergeChunks };
+__host__ __device__ constexpr int int4_merge_threads(Int4MergeKind kind) {
+    return kind == kMergeHeads ? 512 : 128;
+}
 
-template <bool BF16, int D, bool HEADS>
-__global__ void __launch_bounds__(HEADS ? kInt4MergeHeads : kInt4MergeBounds)
-    int4_merge_kernel(const DecodeParams p, int ngroups) {
-    constexpr int T = HEADS ? kInt4MergeHeads : kInt4MergeBounds;
+template <bool BF16, int D, Int4MergeKind KIND>
+__global__ void __launch_bounds__(int4_merge_threads(KIND))
+    int4_merge_kernel(const Int4Params p, int ngroups) {
+    constexpr bool HEADS = KIND == kMergeHeads;
+    constexpr int T = int4_merge_threads(KIND);
     constexpr int ITEMS = D / 4, ROWS = T / ITEMS, SLICES = HEADS ? ROWS : 1;
     __shared__ Int4Range range;
     __shared__ float4 sums[HEADS ? T : 1];
     __shared__ float tops[ROWS], totals[ROWS];
     const int item = threadIdx.x % ITEMS, row = threadIdx.x / ITEMS;
-    // the decode kernel began after all work before it was done, so the lengths
-    // are there
-    const int in_bundle = (int)blockIdx.x % p.bundle, index = (int)blockIdx.x / p.bundle;
-    int4_plan<T>(p, ngroups, HEADS ? -1 : index + 1, index, &range);
-    int first = 0, n = 0;
-    const bool mine = (HEADS ? range.n > 0 : range.unit < range.end && range.at > 0 &&
-                                                 range.at < range.n) &&
-                      (n = int4_parts(range, &first)) > 1 && (HEADS || first == index + 1);
-    pdl_wait();
-    if (!mine) return;
-    auto slot = [&](int k) {
-        return 2 * ((first - 1 + k) * p.bundle + in_bundle) + (k == 0 ? 1 : 0);
-    };
-    const int kvh = range.bundle * p.bundle + in_bundle;
+    // the first partial's slot and those from one to the next of the rest, the
+    // number of partials, and the head
+    int64_t slot0 = 0, slot1 = 0;
+    int stride1 = 1, n = 0, seq, kvh;
+    if constexpr (KIND == kMergeChunks) {
+        pdl_wait();
+        seq = blockIdx.x / p.num_kv_heads;
+        kvh = blockIdx.x % p.num_kv_heads;
+        const int L = item_len(p, seq, false);
+        n = L == 0 ? 0 : (L - 1) / p.partition_tokens + 1;
+        slot0 = (int64_t)blockIdx.x * p.num_partitions;
+        slot1 = slot0 + 1;
+        if (n <= 1) return;  // written by the decode itself
+    } else {
+        // the decode kernel began after all work before it was done, so the
+        // lengths are there
+        const int in_bundle = (int)blockIdx.x % p.bundle, index = (int)blockIdx.x / p.bundle;
+        int4_plan<T>(p, ngroups, HEADS ? -1 : index + 1, index, &range);
+        int first = 0;
+        const bool mine = (HEADS ? range.n > 0 : range.unit < range.end && range.at > 0 &&
+                                                     range.at < range.n) &&
+                          (n = int4_parts(range, &first)) > 1 && (HEADS || first == index + 1);
+        pdl_wait();
+        if (!mine) return;
+        slot0 = 2 * ((int64_t)(first - 1) * p.bundle + in_bundle) + 1;
+        stride1 = 2 * p.bundle;
+        slot1 = slot0 - 1 + stride1;
+        seq = range.seq;
+        kvh = range.bundle * p.bundle + in_bundle;
+    }
+    auto slot = [&](int k) { return k == 0 ? slot0 : slot1 + (int64_t)(k - 1) * stride1; };
     for (int g = HEADS ? blockIdx.y : row; g < p.group; g += ROWS) {
         const float4 *rows = reinterpret_cast<const float4 *>(p.part_o) + g * ITEMS + item;
         const int64_t stride = (int64_t)p.group * ITEMS;
@@ -320,7 +353,7 @@ __global__ void __launch_bounds__(HEADS ? kInt4MergeHeads : kInt4MergeBounds)
             float m[8], l[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int s = slot(min(k0 + j * SLICES, n - 1));
+                const int64_t s = slot(min(k0 + j * SLICES, n - 1));
                 v[j] = __ldcg(rows + s * stride);
                 m[j] = __ldcg(p.part_m + s * kInt4MaxG + g);
                 l[j] = __ldcg(p.part_l + s * kInt4MaxG + g);
@@ -372,7 +405,7 @@ __global__ void __launch_bounds__(HEADS ? kInt4MergeHeads : kInt4MergeBounds)
         }
         const float f = 1.f / total;
         uint16_t *out = static_cast<uint16_t *>(p.out) +
-                        ((int64_t)range.seq * p.num_q_heads + kvh * p.group + g) * D;
+                        ((int64_t)seq * p.num_q_heads + kvh * p.group + g) * D;
         reinterpret_cast<uint2 *>(out)[item] =
             make_uint2(narrow2<BF16>(o.x * f, o.y * f), narrow2<BF16>(o.z * f, o.w * f));
         if constexpr (HEADS) return;
@@ -381,7 +414,7 @@ __global__ void __launch_bounds__(HEADS ? kInt4MergeHeads : kInt4MergeBounds)
 
 template <bool BF16, int D, int B, bool H4>
 __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
-    const __grid_constant__ DecodeParams p) {
+    const __grid_constant__ Int4Params p) {
     using S = Int4Shape<D>;
     constexpr int KW = D / 32;  // words of a key row a lane holds (8 codes each)
     constexpr int VW = D / 64;  // words of a value row a lane holds
@@ -421,7 +454,6 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
             const int left = L - chunk * P;
             piece.count = left > 0 ? min(left, P) : L == 0 && chunk == 0 ? 0 : -1;
             piece.nparts = L == 0 ? 1 : (L - 1) / P + 1;
-            piece.slot = chunk;
         }
         __syncthreads();
         if (piece.count < 0) return;
@@ -783,7 +815,10 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
         }
     }
     __syncthreads();
-    const int nparts = piece.nparts, slot = piece.slot;
+    const int nparts = piece.nparts;
+    const int64_t slot = p.balanced ? piece.slot
+                                    : ((int64_t)seq * p.num_kv_heads + kvh) * p.num_partitions +
+                                          start / p.partition_tokens;
     uint16_t *out = static_cast<uint16_t *>(p.out) + ((int64_t)seq * p.num_q_heads + kvh * G) * D;
     for (int i = threadIdx.x; i < G * (D / 2); i += blockDim.x) {
         const int g = i / (D / 2), x0 = i % (D / 2) * 2;
@@ -803,14 +838,12 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
         if (nparts == 1) {
             *reinterpret_cast<uint32_t *>(out + g * D + x0) = narrow2<BF16>(o0 * inv, o1 * inv);
         } else {
-            const int64_t row =
-                p.balanced ? (int64_t)slot * G + g : part_row(p, seq, kvh * G + g, slot);
-            const int64_t ml = p.balanced ? (int64_t)slot * kInt4MaxG + g : row;
             if (x0 == 0) {
-                p.part_m[ml] = M;
-                p.part_l[ml] = lsum;
+                p.part_m[slot * kInt4MaxG + g] = M;
+                p.part_l[slot * kInt4MaxG + g] = lsum;
             }
-            *reinterpret_cast<float2 *>(p.part_o + row * D + x0) = make_float2(o0 * inv, o1 * inv);
+            *reinterpret_cast<float2 *>(p.part_o + (slot * G + g) * D + x0) =
+                make_float2(o0 * inv, o1 * inv);
         }
     }
     if (!p.balanced) break;
@@ -818,13 +851,7 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
     __syncthreads();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }  // pieces
-    if (!p.balanced) {
-        pdl_trigger();
-        if (piece.nparts > 1 && p.counters != nullptr)
-            finish_item<BF16, D>(p, piece.seq, piece.kvh, piece.nparts, piece.slot, piece.nparts, false,
-                                 reinterpret_cast<float *>(smem), S::BARS);
-        return;
-    }
+    if (!p.balanced) return;
     // every sequence's length is reported on by one CTA, which also writes the
     // rows of those without tokens
     for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
@@ -835,7 +862,9 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
     }
 }
 
-using Int4Kernel = void (*)(const DecodeParams);
+// ------------------------------------------------------------------ host side
+using Int4Kernel = void (*)(const Int4Params);
+using Int4Merge = void (*)(const Int4Params, int);
 
 template <bool BF16, int D>
 static Int4Kernel int4_variant(int block_size, bool h4) {
@@ -852,20 +881,20 @@ static Int4Kernel pick_int4(bool bf16, int D, int block_size, int group, int *sm
     return bf16 ? int4_variant<true, 128>(block_size, h4) : int4_variant<false, 128>(block_size, h4);
 }
 
-using Int4Merge = void (*)(const DecodeParams, int);
-
 template <bool BF16, int D>
-static Int4Merge merge_variant(bool few) {
-    return few ? int4_merge_kernel<BF16, D, true> : int4_merge_kernel<BF16, D, false>;
+static Int4Merge merge_variant(Int4MergeKind kind) {
+    return kind == kMergeHeads    ? int4_merge_kernel<BF16, D, kMergeHeads>
+           : kind == kMergeBounds ? int4_merge_kernel<BF16, D, kMergeBounds>
+                                  : int4_merge_kernel<BF16, D, kMergeChunks>;
 }
 
-static Int4Merge pick_merge(bool bf16, int D, bool few) {
-    if (D == 64) return bf16 ? merge_variant<true, 64>(few) : merge_variant<false, 64>(few);
-    return bf16 ? merge_variant<true, 128>(few) : merge_variant<false, 128>(few);
+static Int4Merge pick_merge(bool bf16, int D, Int4MergeKind kind) {
+    if (D == 64) return bf16 ? merge_variant<true, 64>(kind) : merge_variant<false, 64>(kind);
+    return bf16 ? merge_variant<true, 128>(kind) : merge_variant<false, 128>(kind);
 }
 
 // Resident CTAs per SM; asked of the runtime once per variant and device.
-int int4_ctas_per_sm(bool bf16, int head_dim, int block_size, int group) {
+static int int4_ctas_per_sm(bool bf16, int head_dim, int block_size, int group) {
     static std::mutex mu;
     static int known[128][16] = {};
     int smem = 0, n = 0, dev = 0;
@@ -887,57 +916,163 @@ static int int4_bundle(int num_kv_heads) {
     return b;
 }
 
-// CTAs of a balanced launch, the groups of its first wave (as many as there are
-// slots, or shares) and the heads of a bundle; 0 where the batch is not for
-// balanced ranges: heads too short to be worth cutting (single pass is as fast up
-// to 1024 positions, 13 against 14 us for 8 sequences; at 2048, 19 against 15),
-// or more sequences than a CTA should scan.
-int int4_balanced_ctas(bool bf16, int head_dim, int block_size, int group, int num_seqs,
-                       int num_kv_heads, int max_seq_len, int *wave, int *bundle) {
-    if (max_seq_len <= kInt4SinglePass) return 0;
-    *bundle = int4_bundle(num_kv_heads);
-    const int64_t units = (int64_t)num_seqs * (num_kv_heads / *bundle) *
-                          (((int64_t)max_seq_len + kInt4Unit - 1) / kInt4Unit);
-    if (num_seqs > kInt4BalancedSeqs || units >= (1 << 30)) return 0;
-    const int64_t shares = (units + kInt4MinShare - 1) / kInt4MinShare;
-    int64_t slots =
-        (int64_t)sm_count() * int4_ctas_per_sm(bf16, head_dim, block_size, group) / *bundle;
-    if (slots < 1) slots = 1;
-    if (shares < slots) return (*wave = shares < 1 ? 1 : (int)shares) * *bundle;
-    *wave = (int)slots;
-    return (int)slots * *bundle * (units >= slots * kInt4SecondWave ? 1 + kInt4SecondCtas : 1);
-}
+// How a call is cut, and its workspace.
+struct Int4Cut {
+    int ctas = 0;    // balanced ranges: CTAs of the launch (0: chunks)
+    int wave = 0;    //   groups of its first wave
+    int bundle = 1;  //   heads of a group
+    int P = -1;      // chunks: positions of one, or -1 for single pass
+    int chunks = 1;  //   of the longest sequence
+    size_t l_off = 0, o_off = 0, bytes = 0;
+};
 
-pa_status launch_decode_int4(const DecodeParams &prm, bool bf16, int head_dim, int num_partitions,
-                             int num_kv_heads, int num_seqs, cudaStream_t stream) {
+// Checks the shapes and chooses.  Automatic: single pass up to 1024 positions,
+// where cutting gains nothing (13 against 14 us for 8 sequences; at 2048, 19
+// against 15); balanced ranges; eight chunks for more sequences than a CTA should
+// scan the lengths of.
+static pa_status int4_cut(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                          int block_size, int max_seq_len, int partition_tokens, pa_dtype dtype,
+                          Int4Cut *c) {
+    if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_seq_len < 0)
+        return PA_ERR_INVALID;
+    if (num_seqs > 65535 || num_kv_heads > 65535) return PA_ERR_INVALID;  // grid y and z
+    if ((int64_t)num_seqs * num_q_heads > 0x7fffffff) return PA_ERR_INVALID;
+    if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_INVALID;
+    if (num_q_heads % num_kv_heads) return PA_ERR_INVALID;
+    const int G = num_q_heads / num_kv_heads;
+    if (G > kInt4MaxG || (head_dim != 64 && head_dim != 128) || (block_size != 16 && block_size != 32))
+        return PA_ERR_UNSUPPORTED;
+    if (partition_tokens < -1 || (partition_tokens > 0 && partition_tokens % block_size))
+        return PA_ERR_INVALID;
+    *c = {};
     if (num_seqs == 0) return PA_OK;
-    int smem = 0;
-    Int4Kernel k = pick_int4(bf16, head_dim, prm.block_size, prm.group, &smem);
-    if (!ensure_smem_attr(reinterpret_cast<const void *>(k), smem)) return PA_ERR_CUDA;
-    DecodeParams p = prm;
-    if (p.balanced) {
-        p.compact = 0;
-        if (launch_pdl(k, dim3((unsigned)num_partitions), dim3(32 * kInt4Warps), (size_t)smem, stream,
-                       p) != cudaSuccess)
-            return PA_ERR_CUDA;
-        if (num_partitions > p.bundle) {
-            // a head cut into 8 partials or more on average: a block a query head
-            const int64_t heads = (int64_t)num_seqs * num_kv_heads;
-            const bool few = 8 * heads <= num_partitions;
-            const dim3 grid = few ? dim3((unsigned)heads, (unsigned)p.group)
-                                  : dim3((unsigned)(num_partitions - p.bundle));
-            if (launch_pdl(pick_merge(bf16, head_dim, few), grid,
-                           dim3(few ? kInt4MergeHeads : kInt4MergeBounds), 0, stream, p,
-                           num_partitions / p.bundle) != cudaSuccess)
-                return PA_ERR_CUDA;
+    int64_t slots = 0;
+    if (partition_tokens == 0 && max_seq_len > kInt4SinglePass) {
+        c->bundle = int4_bundle(num_kv_heads);
+        const int64_t units = (int64_t)num_seqs * (num_kv_heads / c->bundle) *
+                              (((int64_t)max_seq_len + kInt4Unit - 1) / kInt4Unit);
+        if (num_seqs <= kInt4BalancedSeqs && units < (1 << 30)) {
+            const int64_t shares = (units + kInt4MinShare - 1) / kInt4MinShare;
+            int64_t wave = (int64_t)sm_count() *
+                           int4_ctas_per_sm(dtype == PA_BF16, head_dim, block_size, G) / c->bundle;
+            if (wave < 1) wave = 1;
+            const bool second = units >= wave * kInt4SecondWave;
+            if (shares < wave) wave = shares;
+            c->wave = (int)wave;
+            c->ctas = (int)wave * c->bundle * (second ? 1 + kInt4SecondCtas : 1);
+            slots = 2ll * c->ctas;
+        } else {
+            partition_tokens = (int)(((int64_t)max_seq_len + 7) / 8);
+            if (partition_tokens < 4096) partition_tokens = 4096;
+            partition_tokens = (partition_tokens + 31) / 32 * 32;
         }
-        return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     }
-    if (p.compact) p.compact = 2;  // full chunks first, the short last ones at the end
-    const dim3 grid = decode_grid(p, num_partitions, num_kv_heads, num_seqs);
-    if (launch_pdl(k, grid, dim3(32 * kInt4Warps), (size_t)smem, stream, p) != cudaSuccess)
-        return PA_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    if (partition_tokens > 0 && max_seq_len > partition_tokens) {
+        c->P = partition_tokens;
+        c->chunks = (int)(((int64_t)max_seq_len + partition_tokens - 1) / partition_tokens);
+        slots = (int64_t)num_seqs * num_kv_heads * c->chunks;
+    }
+    auto align256 = [](size_t x) { return (x + 255) & ~size_t(255); };
+    if (slots) {
+        c->l_off = align256((size_t)slots * kInt4MaxG * sizeof(float));
+        c->o_off = 2 * c->l_off;
+        c->bytes = c->o_off + align256((size_t)slots * G * head_dim * sizeof(float));
+    }
+    return PA_OK;
 }
 
 }  // namespace pa
+
+using namespace pa;
+
+extern "C" {
+
+size_t pa_decode_int4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int block_size, int max_seq_len, int partition_tokens,
+                                     pa_dtype dtype) {
+    Int4Cut c;
+    if (int4_cut(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len,
+                 partition_tokens, dtype, &c) != PA_OK)
+        return 0;
+    return c.bytes;
+}
+
+pa_status pa_decode_int4(void *out, const void *q, const void *k_pool, const void *v_pool,
+                         int num_blocks, const int32_t *block_tables, int max_blocks_per_seq,
+                         const int32_t *seq_lens, int max_seq_len, int num_seqs, int num_q_heads,
+                         int num_kv_heads, int head_dim, int block_size, float scale,
+                         int partition_tokens, void *workspace, size_t workspace_bytes,
+                         pa_dtype dtype, void *stream) {
+    Int4Cut c;
+    const pa_status st = int4_cut(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                  max_seq_len, partition_tokens, dtype, &c);
+    if (st != PA_OK) return st;
+    if (num_blocks <= 0 || max_blocks_per_seq < 0 || !std::isfinite(scale)) return PA_ERR_INVALID;
+    if (num_seqs == 0) return PA_OK;
+    if (!out || !q || !k_pool || !v_pool || !block_tables || !seq_lens || !aligned16(out) ||
+        !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool))
+        return PA_ERR_INVALID;
+    if (c.bytes && (!workspace || workspace_bytes < c.bytes ||
+                    (reinterpret_cast<uintptr_t>(workspace) & 255)))
+        return PA_ERR_INVALID;
+    const bool bf16 = dtype == PA_BF16;
+    Int4Params p;
+    std::memset(&p, 0, sizeof p);
+    p.out = out;
+    p.q = static_cast<const uint16_t *>(q);
+    p.k_pool = static_cast<const uint16_t *>(k_pool);
+    p.v_pool = static_cast<const uint16_t *>(v_pool);
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.num_seqs = num_seqs;
+    p.num_blocks = num_blocks;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.max_seq_len = max_seq_len;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group = num_q_heads / num_kv_heads;
+    p.block_size = block_size;
+    p.log2_block = block_size == 16 ? 4 : 5;
+    p.scale_log2 = scale * kLog2e;
+    p.partition_tokens = c.P > 0 ? c.P : kSinglePassTokens;
+    p.num_partitions = c.chunks;
+    p.balanced = c.wave;
+    p.bundle = c.bundle;
+    if (c.bytes) {
+        uint8_t *ws = static_cast<uint8_t *>(workspace);
+        p.part_m = reinterpret_cast<float *>(ws);
+        p.part_l = reinterpret_cast<float *>(ws + c.l_off);
+        p.part_o = reinterpret_cast<float *>(ws + c.o_off);
+    }
+    p.err = error_word();
+    if (!p.err) return PA_ERR_CUDA;
+
+    int smem = 0;
+    Int4Kernel k = pick_int4(bf16, head_dim, block_size, p.group, &smem);
+    if (!ensure_smem_attr(reinterpret_cast<const void *>(k), smem)) return PA_ERR_CUDA;
+    const int64_t heads = (int64_t)num_seqs * num_kv_heads;
+    dim3 grid((unsigned)c.ctas);
+    if (!c.ctas) {
+        // small batches: only the chunks that exist, the short last ones at the end
+        if (num_seqs <= kCompactMaxSeqs && heads * c.chunks < (1ll << 31)) p.compact = 2;
+        grid = decode_grid(p, c.chunks, num_kv_heads, num_seqs);
+    }
+    cudaStream_t s = as_stream(stream);
+    if (launch_pdl(k, grid, dim3(32 * kInt4Warps), (size_t)smem, s, p) != cudaSuccess)
+        return PA_ERR_CUDA;
+    if (c.ctas > c.bundle || c.P > 0) {
+        // a head cut into 8 partials or more on average: a block a query head
+        const Int4MergeKind kind = c.P > 0                ? kMergeChunks
+                                   : 8 * heads <= c.ctas ? kMergeHeads
+                                                          : kMergeBounds;
+        const dim3 blocks = kind == kMergeChunks  ? dim3((unsigned)heads)
+                            : kind == kMergeHeads ? dim3((unsigned)heads, (unsigned)p.group)
+                                                  : dim3((unsigned)(c.ctas - c.bundle));
+        if (launch_pdl(pick_merge(bf16, head_dim, kind), blocks, dim3(int4_merge_threads(kind)), 0, s,
+                       p, c.ctas / c.bundle) != cudaSuccess)
+            return PA_ERR_CUDA;
+    }
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // extern "C"

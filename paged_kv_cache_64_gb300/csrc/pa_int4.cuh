@@ -97,9 +97,10 @@ __device__ __forceinline__ uint4 read8_int4(uint32_t codes, uint32_t params) {
 // s is the smallest 16-bit value with 15 s >= span = fl(max - min): the
 // nearest one to span / 15, or the next one up (15 s is exact in fp32: 11 + 4
 // bits).  Codes are the integers nearest to a / s, a = fl(x - m), ties to
-// even.  The quotient t' = t + (a - t s) / s is the correctly rounded one (a
-// Newton step with an exact FMA remainder), so a tie, which is a quotient
-// fp32 holds exactly, is met exactly, and adding 1.5 * 2^23 rounds it to
+// even.  The quotient t' = t + (a - t s) / s, with the remainder exact by FMA, is
+// Markstein's correction of a product with the reciprocal (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990): a tie, which is a quotient fp32 holds exactly, is met exactly, and adding 1.5 * 2^23 rounds it to
 // even.  A quotient next to a tie may round onto it; the remainder a - n s,
 // exact there, then passes s / 2 and the lane's elements are taken again with
 // that comparison.  With OUT, y receives the values the codes stand for, as

@@ -352,10 +352,9 @@ pa_status pa_cache_read_int4(void *k_out, void *v_out, const int64_t *slot_mappi
  * as pa_decode (pools as above, workspace size from
  * pa_decode_int4_workspace_size); the group size is at most 8.  A row of NaN
  * that a sequence reaches makes the outputs of its query heads NaN.
- * partition_tokens = 0: the batch's positions are shared out evenly over the
- * GPU from the lengths on the device (up to 1024 sequences, heads longer than
- * 1024 positions) and the pieces of heads that this cuts merged by a second
- * launch; the result does not depend on the order in which they run.  Calls
+ * partition_tokens = 0: where heads are long, the batch's positions are shared
+ * out evenly over the GPU from the lengths on the device (up to 1024 sequences)
+ * and the pieces of heads that this cuts merged by a second launch; the result does not depend on the order in which they run.  Calls
  * that may overlap need workspaces of their own. */
 pa_status pa_decode_int4(void *out, const void *q, const void *k_pool, const void *v_pool,
                          int num_blocks, const int32_t *block_tables, int max_blocks_per_seq,

@@ -137,7 +137,13 @@ struct Int4Piece {
 };
 
 constexpr int kInt4Unit = kInt4Step * kInt4Warps;  // positions
-constexpr int kInt4SinglePass = 1024;              // positions: longer heads may be cut
+// Longest heads that one CTA each takes whole, of few and of many (sequence, KV
+// head) pairs.  Single pass against balanced ranges: 8 x 2 heads of 1024 13 and 14
+// us, of 2048 19 and 15; 128 x 2 of up to 2049 12.9 and 14.4 (chat lengths) or 16.6
+// and 15.5 (even ones), 32 x 2 8.7 and 10.6, 64 x 8 27 and 29, 256 x 8 68 and 75; 128
+// x 8 of up to 4096 77 and 68.
+constexpr int kInt4SinglePass = 1024, kInt4SinglePassMany = 2176;
+constexpr int kInt4ManyHeads = 64;
 constexpr int kInt4MinShare = 4;                   // units: smaller shares cost more than they save
 constexpr int kInt4MinSlack = 2;
 // A second wave pays where its shares are still long next to a CTA's start (2 us
@@ -926,10 +932,9 @@ struct Int4Cut {
     size_t l_off = 0, o_off = 0, bytes = 0;
 };
 
-// Checks the shapes and chooses.  Automatic: single pass up to 1024 positions,
-// where cutting gains nothing (13 against 14 us for 8 sequences; at 2048, 19
-// against 15); balanced ranges; eight chunks for more sequences than a CTA should
-// scan the lengths of.
+// Checks the shapes and chooses.  Automatic: single pass for short heads, else
+// balanced ranges, or up to eight chunks for more sequences than a CTA should scan
+// the lengths of.
 static pa_status int4_cut(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                           int block_size, int max_seq_len, int partition_tokens, pa_dtype dtype,
                           Int4Cut *c) {
@@ -947,7 +952,9 @@ static pa_status int4_cut(int num_seqs, int num_q_heads, int num_kv_heads, int h
     *c = {};
     if (num_seqs == 0) return PA_OK;
     int64_t slots = 0;
-    if (partition_tokens == 0 && max_seq_len > kInt4SinglePass) {
+    const int whole = (int64_t)num_seqs * num_kv_heads >= kInt4ManyHeads ? kInt4SinglePassMany
+                                                                         : kInt4SinglePass;
+    if (partition_tokens == 0 && max_seq_len > whole) {
         c->bundle = int4_bundle(num_kv_heads);
         const int64_t units = (int64_t)num_seqs * (num_kv_heads / c->bundle) *
                               (((int64_t)max_seq_len + kInt4Unit - 1) / kInt4Unit);

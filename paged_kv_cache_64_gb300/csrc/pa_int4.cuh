@@ -100,10 +100,10 @@ __device__ __forceinline__ uint4 read8_int4(uint32_t codes, uint32_t params) {
 // even.  The quotient t' = t + (a - t s) / s, with the remainder exact by FMA, is
 // Markstein's correction of a product with the reciprocal (P. Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000 processor",
-// 1990): a tie, which is a quotient fp32 holds exactly, is met exactly, and adding 1.5 * 2^23 rounds it to
-// even.  A quotient next to a tie may round onto it; the remainder a - n s,
-// exact there, then passes s / 2 and the lane's elements are taken again with
-// that comparison.  With OUT, y receives the values the codes stand for, as
+// 1990): a tie, which is a quotient fp32 holds exactly, is met exactly, and
+// adding 1.5 * 2^23 rounds it to even.  A quotient next to a tie may round onto
+// it; the remainder a - n s, exact there, then passes s / 2 and the lane's
+// elements are taken again with that comparison.  With OUT, y receives the values the codes stand for, as
 // read8_int4 gives them.
 template <bool BF16, int LANES, int W, bool OUT>
 __device__ __forceinline__ Int4Row<W> quantise_row_int4(const uint4 (&raw)[W], uint4 *y) {

@@ -253,14 +253,15 @@ def test_a_missing_small_or_crooked_workspace_is_refused():
         assert rc == 1  # PA_ERR_INVALID
 
 
-def test_two_graphs_share_a_workspace_and_replay():
+@pytest.mark.parametrize("cut", [256, 0])
+def test_two_graphs_share_a_workspace_and_replay(cut):
     a = Case([700, 90, 1500], 2, 4, 128, 16, "bf16", seed=1)
-    b = Case([900, 33], 3, 8, 64, 32, "f16", seed=2)
+    b = Case([1900, 33], 3, 8, 64, 32, "f16", seed=2)
     ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
     a.gpu(0, workspace=ws), b.gpu(0, workspace=ws)
     torch.cuda.synchronize()
     graphs, outs = [], []
-    for c, partition in ((a, 256), (b, 256)):
+    for c, partition in ((a, cut), (b, cut)):
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             outs.append(c.gpu(partition, workspace=ws))
@@ -274,17 +275,18 @@ def test_two_graphs_share_a_workspace_and_replay():
         b.check(outs[1])
 
 
-def test_two_streams_with_workspaces_of_their_own():
+@pytest.mark.parametrize("cut", [256, 0])
+def test_two_streams_with_workspaces_of_their_own(cut):
     a = Case([700, 90, 1500], 2, 4, 128, 16, "bf16", seed=1)
-    b = Case([900, 33], 2, 4, 128, 16, "bf16", seed=2)
+    b = Case([1900, 33], 2, 4, 128, 16, "bf16", seed=2)
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
     torch.cuda.synchronize()
     outs = []
     for _ in range(5):
         with torch.cuda.stream(s1):
-            x = a.gpu(256)
+            x = a.gpu(cut)
         with torch.cuda.stream(s2):
-            y = b.gpu(256)
+            y = b.gpu(cut)
         outs.append((x, y))
     torch.cuda.synchronize()
     for x, y in outs:

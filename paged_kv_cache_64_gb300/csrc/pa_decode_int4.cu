@@ -784,7 +784,9 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
     if (!arrived && lane == 0) {
         // A bounded wait ran out: let copies still in flight land (bounded
         // again) before the shared memory goes; the output is then unspecified.
+        // There is no further piece: its waits would run out one after the other.
         record_error(p.err, PA_ERR_DEVICE_TIMEOUT);
+        range.end = 0;
         for (int i = 0; i < S::STAGES; ++i) (void)mbar_wait(&bars[i], i >= stage ? parity : parity ^ 1);
     }
     __syncwarp();

@@ -18,8 +18,12 @@
 // its columns positions, so two positions' words are interleaved by halves
 // (two byte permutes for 16 codes) before the same masks; B is the weights,
 // which the transposing register exchange movmatrix brings from the score
-// tile's layout.  The weights P s' are split into two f16 terms (22 bits) and
-// scaled by a power of two kept, like the running maximum, per warp.  The matrix
+// tile's layout.  The weights P s' are split into two f16 terms (22 bits).  f16's
+// grid ends at 2^-24, so a power of two that each warp keeps for each head, like
+// the running maximum, brings the largest product P s' to 2^6 .. 2^15: the grid is
+// then 2^-30 of it or finer.  (It goes by the products and not by the scales s'
+// alone, and falls when the maximum moves: a row of large values that has no weight
+// must not push the others onto the grid.)  The matrix
 // unit cuts sums off instead of rounding them, and sums of codes would all be of
 // one sign: every other 16 positions enter as -P s' times 15 - n (a mask with an
 // exclusive or), which leaves 15 s' for their minimum to take over and keeps the
@@ -40,6 +44,10 @@
 // instructions (12 of 240 for 16 positions: 1%) nor more warps (five or six CTAs an
 // SM with the queries in shared memory: 12 to 39% slower) nor the next keys'
 // products beside this step's values (4 to 7% slower) bring them together better.
+// Taking the weights' scale from the products, which are held across the check,
+// costs nothing against one taken from the scales (218 us for 219; the variants of
+// five to eight heads of 128 spill 20 bytes outside of the products, 94.6 for 94.0);
+// products formed anew after the check 224, a check of their own 224.
 //
 // A warp works alone: every fourth 32 positions of the CTA's piece, its own
 // ring of stages filled by bulk copies of whole records, its own running
@@ -65,6 +73,10 @@ struct Int4Params : DecodeParams {
 constexpr int kInt4Warps = 4;
 constexpr int kInt4MaxG = 8;
 constexpr int kInt4Step = 32;  // positions a warp takes at a time: two score tiles
+// A column's factor fe = 2^(7 - ve) keeps its products P s' fe below this (f16 ends at
+// 65504), ve at least kInt4LeastExponent (fe in fp32).
+constexpr float kInt4Product = 32768.f;
+constexpr int kInt4LeastExponent = -119;
 
 template <int D>
 struct Int4Shape {
@@ -103,6 +115,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// ve of a factor 2^(7 - ve).
+__device__ __forceinline__ int int4_weight_exponent(float fe) {
+    return 7 + 127 - (int)(__float_as_uint(fe) >> 23);
+}
 
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) { return narrow2<false>(a, b); }
 
@@ -580,15 +597,13 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
 
     // ---------------------------------------------------------- main loop
     // O[a][...]: of this lane's D/8 dimensions, 2a, and 2a + 1 16 times with 2a
-    // added, columns 2t and 2t + 1, in units of 2^-24 / fe.
+    // added, columns 2t and 2t + 1, in units of 2^-24 / fe of the column.
     float O[4 * VW][4];
 #pragma unroll
     for (int a = 0; a < 4 * VW; ++a) O[a][0] = O[a][1] = O[a][2] = O[a][3] = 0.f;
     // pm: sum of P times what the rows' codes are counted from
     float M[2] = {0.f, 0.f}, l[2] = {0.f, 0.f}, pm[2] = {0.f, 0.f};
-    int ve = -110;                  // scales of V seen so far are at most 2^ve
-    float vtop = pow2i(ve);
-    float fe = pow2i(7 - ve);       // weights are P s' fe, at most 2^8 2^7
+    float fe[2] = {1.f, 1.f};  // the weights are P s' fe (the first step sets it)
     // Fragment row r is position pr of its half tile: pairs of rows (r, r + 1)
     // and rows of equal t differ in parity, so that neither the key loads (two
     // rows a quarter warp) nor the value loads (four rows a half warp) meet in
@@ -668,42 +683,58 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
                     }
         }
 
-        // The running maximum moves only when a score passes it by more than
-        // kLazyRescale (and with the first step), the running scale when one
-        // passes it.
-        float top = fmaxf(fmaxf(sv[0][0], sv[0][1]), fmaxf(sv[1][0], sv[1][1]));
-        float mx[2];
+        // The weights P and their products with the scales of V.  The running
+        // maximum moves only when a score passes it by more than kLazyRescale, a
+        // column's fe only when a product passes kInt4Product (and both with the
+        // first step).
+        float P[2][4], x[2][4];
+        float top = 0.f, mx = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            mx[i] = fmaxf(fmaxf(s[0][i], s[0][2 + i]), fmaxf(s[1][i], s[1][2 + i]));
-        const bool moves = fmaxf(mx[0], mx[1]) > kLazyRescale || top > vtop || k == 0;
-        if (__any_sync(kFullMask, moves)) {
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int o = 4; o <= 16; o <<= 1) {
-                top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
-                mx[0] = fmaxf(mx[0], __shfl_xor_sync(kFullMask, mx[0], o));
-                mx[1] = fmaxf(mx[1], __shfl_xor_sync(kFullMask, mx[1], o));
+            for (int i = 0; i < 4; ++i) {
+                P[u][i] = fast_exp2(s[u][i]);
+                x[u][i] = P[u][i] * (sv[u][i >> 1] * fe[i & 1]);
+                top = fmaxf(top, fabsf(x[u][i]));
+                mx = fmaxf(mx, s[u][i]);
             }
-            int e = (int)(__float_as_uint(top) >> 23) - 126;  // top < 2^e
-            e = e > 127 ? 127 : e < ve ? ve : e;
-            const float shrink = pow2i(ve - e < -126 ? -126 : ve - e);
-            ve = e;
-            vtop = pow2i(ve);
-            fe = pow2i(7 - ve);
+        if (__any_sync(kFullMask, mx > kLazyRescale || top > kInt4Product || k == 0)) {
             float f[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float up = k == 0 ? mx[i] : fmaxf(mx[i], 0.f);
+                float up = fmaxf(fmaxf(s[0][i], s[0][2 + i]), fmaxf(s[1][i], s[1][2 + i]));
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1) up = fmaxf(up, __shfl_xor_sync(kFullMask, up, o));
+                if (k > 0) up = fmaxf(up, 0.f);
                 M[i] += up;
-                f[i] = fast_exp2(-up);
-                if (k == 0) f[i] = 0.f;  // nothing summed yet
+                f[i] = k == 0 ? 0.f : fast_exp2(-up);  // nothing summed yet
                 l[i] *= f[i];
                 pm[i] *= f[i];
-                f[i] *= shrink;
+                // the column's largest product now, below 2^e
+                float most = 0.f;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        s[u][2 * h + i] -= up;
+                        P[u][2 * h + i] = fast_exp2(s[u][2 * h + i]);
+                        x[u][2 * h + i] = P[u][2 * h + i] * sv[u][h];
+                        most = fmaxf(most, fabsf(x[u][2 * h + i]));
+                    }
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1)
+                    most = fmaxf(most, __shfl_xor_sync(kFullMask, most, o));
+                int e = (int)(__float_as_uint(most) >> 23) - 126;
+                // that of the sums so far, which have shrunk by 2^up: below 2^(ve - up)
+                const int ve = int4_weight_exponent(fe[i]);
+                if (k > 0) e = max(e, ve - (int)fminf(up, 512.f));
+                e = min(max(e, kInt4LeastExponent), 127);
+                f[i] *= pow2i(max(min(ve - e, 126), -126));
+                fe[i] = pow2i(7 - e);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    s[u][i] -= up;
-                    s[u][2 + i] -= up;
+                    x[u][i] *= fe[i];
+                    x[u][2 + i] *= fe[i];
                 }
             }
 #pragma unroll
@@ -717,19 +748,19 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
 
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            // weights, their sums, and the two f16 terms of P s' fe, transposed
+            // the weights' sums, and the two f16 terms of P s' fe, transposed
             // to B fragments (rows: positions, columns: heads; H4: the second
             // terms of heads 0 .. 3 are columns 4 .. 7)
             uint32_t bh[2], bl[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float g = sv[u][h] * (u == 0 ? fe : -fe);
-                const float p0 = fast_exp2(s[u][2 * h]), p1 = fast_exp2(s[u][2 * h + 1]);
+                const float p0 = P[u][2 * h], p1 = P[u][2 * h + 1];
                 l[0] += p0;
                 l[1] += p1;
                 pm[0] = fmaf(p0, mv[u][h], pm[0]);
                 pm[1] = fmaf(p1, mv[u][h], pm[1]);
-                const float x0 = p0 * g, x1 = p1 * g;
+                const float x0 = u == 0 ? x[u][2 * h] : -x[u][2 * h];
+                const float x1 = u == 0 ? x[u][2 * h + 1] : -x[u][2 * h + 1];
                 const uint32_t hi = half2_bits(x0, x1);
                 const float2 y = widen2<false>(hi);
                 const uint32_t lo = half2_bits(x0 - y.x, x1 - y.y);
@@ -807,13 +838,13 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
     float *red = reinterpret_cast<float *>(smem);  // [W][8][D]
     float *red_m = red + kInt4Warps * kInt4MaxG * D, *red_l = red_m + kInt4Warps * kInt4MaxG;
     if (!H4 || t < 2) {
-        const float unit = pow2i(ve);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+            const float unit = pow2i(int4_weight_exponent(fe[h]));
             const int g = warp * kInt4MaxG + 2 * t + h;
             float2 *dst = reinterpret_cast<float2 *>(red + g * D + r * (8 * VW));
 #pragma unroll
-            for (int a = 0; a < 4 * VW; ++a)  // 2^24 / fe = 2^(17 + ve)
+            for (int a = 0; a < 4 * VW; ++a)  // 2^24 / fe = 2^17 unit
                 dst[a] = make_float2(fmaf(O[a][h] * 0x1p17f, unit, pm[h]),
                                      fmaf((O[a][2 + h] - O[a][h]) * 0x1p13f, unit, pm[h]));
             if (r == 0) {

@@ -46,12 +46,13 @@
 // products beside this step's values (4 to 7% slower) bring them together better.
 // Taking the weights' scale from the products, which are held across the check,
 // costs nothing against one taken from the scales (218 us for 219; the variants of
-// five to eight heads of 128 spill 20 bytes outside of the products, 94.6 for 94.0);
+// five to eight heads of 128 spill 20 bytes by it, 94.6 us for 94.0);
 // products formed anew after the check 224, a check of their own 224.
 //
 // A warp works alone: every fourth 32 positions of the CTA's piece, its own
 // ring of stages filled by bulk copies of whole records, its own running
 // maximum and sums; the four warps merge at the end through shared memory.
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -552,9 +553,13 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
     // B fragments: column r is head r (H4, at most four heads: r mod 4), this
     // lane's elements are those of its key words.  2^kq brings the head's
     // largest |q| below 2^15; elements that meet codes in the high four bits
-    // are divided by 16.
+    // are divided by 16.  What takes scores back, 2^(24 - kq) scale, may pass
+    // fp32's range while they do not (|q| of 2^100 and keys of 2^-100): a warp with
+    // a head of such a size forms them, and keeps M, in units of 2^64 (full batch 218
+    // -> 222 us, long and one long within 1%; a factor in every step the same).
     uint32_t qf[KW][4];
     float cs[2], qs[2];  // of the score tile's columns 2t, 2t + 1
+    int careful;  // steps that take the branch below in any case: the first, or all
     {
         const int head = H4 ? r & 3 : r;
         float x[KW][8];
@@ -569,17 +574,23 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 top = fmaxf(top, fabsf(x[j][i]));
-                sum += x[j][i];
             }
         }
-#pragma unroll
-        for (int o = 1; o <= 2; o <<= 1) {
-            top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
-            sum += __shfl_xor_sync(kFullMask, sum, o);
-        }
-        int kq = 14 - ((int)(__float_as_uint(top) >> 23) - 127);
-        kq = kq > 100 ? 100 : kq < -100 ? -100 : kq;
+        top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
+        const int e = (int)(__float_as_uint(top) >> 23) - 127;  // top < 2^(e + 1)
+        const int es = (int)(__float_as_uint(fabsf(p.scale_log2)) >> 23) - 127;
+        const bool big = __any_sync(kFullMask, e + max(es, 0) > 80);
+        careful = big ? INT_MAX : 1;
+        const float unit = big ? 0x1p-64f : 1.f;
+        const int kq = min(14 - e, 127);  // -113 .. 127
         const float even = pow2i(kq), odd = pow2i(kq - 4);
+#pragma unroll
+        for (int j = 0; j < KW; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum = fmaf(x[j][i], unit, sum);
+        sum += __shfl_xor_sync(kFullMask, sum, 1);
+        sum += __shfl_xor_sync(kFullMask, sum, 2);
 #pragma unroll
         for (int j = 0; j < KW; ++j)
 #pragma unroll
@@ -587,7 +598,9 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
                 const float f = i & 1 ? odd : even;
                 qf[j][i] = half2_bits(x[j][i] * f, x[j][i + 4] * f);
             }
-        const float c = p.scale_log2 * pow2i(24 - kq), s = sum * p.scale_log2;
+        const int back = 24 - kq, half = back >> 1;  // -103 .. 137, in two steps
+        const float c = p.scale_log2 * unit * pow2i(half) * pow2i(back - half);
+        const float s = sum * p.scale_log2;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             cs[h] = __shfl_sync(kFullMask, c, 4 * (2 * t + h));
@@ -698,15 +711,22 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
                 top = fmaxf(top, fabsf(x[u][i]));
                 mx = fmaxf(mx, s[u][i]);
             }
-        if (__any_sync(kFullMask, mx > kLazyRescale || top > kInt4Product || k == 0)) {
+        if (__any_sync(kFullMask, mx > kLazyRescale || top > kInt4Product || k < careful)) {
             float f[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
+                if (careful > 1) {  // scores in units of 2^64
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        s[u][i] *= 0x1p64f;
+                        s[u][2 + i] *= 0x1p64f;
+                    }
+                }
                 float up = fmaxf(fmaxf(s[0][i], s[0][2 + i]), fmaxf(s[1][i], s[1][2 + i]));
 #pragma unroll
                 for (int o = 4; o <= 16; o <<= 1) up = fmaxf(up, __shfl_xor_sync(kFullMask, up, o));
                 if (k > 0) up = fmaxf(up, 0.f);
-                M[i] += up;
+                M[i] = fmaf(up, careful > 1 ? 0x1p-64f : 1.f, M[i]);
                 f[i] = k == 0 ? 0.f : fast_exp2(-up);  // nothing summed yet
                 l[i] *= f[i];
                 pm[i] *= f[i];
@@ -848,7 +868,7 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 4) decode_int4_kernel(
                 dst[a] = make_float2(fmaf(O[a][h] * 0x1p17f, unit, pm[h]),
                                      fmaf((O[a][2 + h] - O[a][h]) * 0x1p13f, unit, pm[h]));
             if (r == 0) {
-                red_m[g] = my_steps > 0 ? M[h] : -INFINITY;
+                red_m[g] = my_steps > 0 ? M[h] * (careful > 1 ? 0x1p64f : 1.f) : -INFINITY;
                 red_l[g] = l[h];
             }
         }

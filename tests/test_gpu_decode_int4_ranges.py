@@ -123,3 +123,26 @@ def test_ordinary_rows_keep_the_bound():
     c = Case([700, 0, 90, 1500, 1], 2, 4, 128, 16, "bf16")
     for partition in (-1, 256, 0):
         check(c, c.gpu(partition), partition)
+
+
+@pytest.mark.parametrize("d,group", [(64, 3), (128, 6)])
+@pytest.mark.parametrize("eq,ek,escale", [
+    (127, -127, -3), (122, -122, -3), (116, -118, -3), (110, -110, -3), (92, -92, -3), (88, -90, 0),
+    (70, -118, 40), (20, -118, 90), (-20, 20, -3), (-100, 100, -3), (-115, 115, -3), (-124, 125, -3),
+    (-130, 126, -3), (-60, -40, 97)])
+def test_queries_of_every_size_bf16_holds(d, group, eq, ek, escale):
+    """Queries around 2^eq (from bf16's subnormals to its largest), keys and scale
+    such that the scores are ordinary; some heads' queries are 2^20 smaller."""
+    def q(rng, shape):
+        x = rng.uniform(-1, 1, shape) * 2.0**eq
+        x[:, 1::4] *= 2.0**-20 if eq > -100 else 1.0
+        x[0, 0] = 0.0
+        x[0, -1, 0] = 0.99 * 2.0**eq
+        return x
+    c = Case([150, 1, 40], 2, group, d, 16, "bf16", seed=5, q=q,
+             k_rows=lambda r, s: r.uniform(-1, 1, s) * 2.0**ek)
+    c.scale = 2.0**escale
+    assert np.isfinite(int4.widen(c.q, "bf16")).all() and np.isfinite(
+        int4.values(c.kp, d, 16, "bf16")[c.tables[0, :9]]).all()
+    for partition in (-1, 32):
+        check(c, c.gpu(partition), partition)

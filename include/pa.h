@@ -351,8 +351,10 @@ pa_status pa_cache_read_int4(void *k_out, void *v_out, const int64_t *slot_mappi
  * a row of V is formed).  q finite, |scale q| below 2^170 and
  * the scores in fp32's range.  Arguments, partition_tokens and workspace as
  * pa_decode (pools as above, workspace size from
- * pa_decode_int4_workspace_size); the group size is at most 8.  A row of NaN
- * that a sequence reaches makes the outputs of its query heads NaN.
+ * pa_decode_int4_workspace_size); the group size is at most 8;
+ * max_blocks_per_seq * block_size below 2^31, and that or max_seq_len at most
+ * 2^30.  A row of NaN that a sequence reaches makes the outputs of its query heads
+ * NaN.
  * partition_tokens = 0: where heads are long, the batch's positions are shared
  * out evenly over the GPU from the lengths on the device (up to 1024 sequences)
  * and the pieces of heads that this cuts merged by a second launch; the result does not depend on the order in which they run.  Calls

@@ -1068,6 +1068,11 @@ pa_status pa_decode_int4(void *out, const void *q, const void *k_pool, const voi
                                   max_seq_len, partition_tokens, dtype, &c);
     if (st != PA_OK) return st;
     if (num_blocks <= 0 || max_blocks_per_seq < 0 || !std::isfinite(scale)) return PA_ERR_INVALID;
+    // Positions are ints: a table's must be, and a sequence's (by its table and
+    // max_seq_len) at most a single pass's.
+    const int64_t table = (int64_t)max_blocks_per_seq * block_size;
+    if (table > 0x7fffffff || (table > kSinglePassTokens && max_seq_len > kSinglePassTokens))
+        return PA_ERR_INVALID;
     if (num_seqs == 0) return PA_OK;
     if (!out || !q || !k_pool || !v_pool || !block_tables || !seq_lens || !aligned16(out) ||
         !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool))

@@ -302,8 +302,6 @@ def decode_fp8(out, q, k_pool, v_pool, block_tables, seq_lens, max_seq_len, scal
 # The checks below are written out in each wrapper as one condition (a call
 # costs more than the kernel of a small batch); when it fails, _explain finds
 # the argument and says what is wrong with it.
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _explain(dev, **tensors):
@@ -320,11 +318,13 @@ def _explain(dev, **tensors):
 
 def _run(dev, stream, fn, args):
     """fn(*args, stream handle) with `dev` current; stream None: its current
-    stream."""
-    if dev != _current_device():
+    stream.  (What torch.cuda's own calls end in, looked up here: builds of torch
+    without CUDA lack them, and the host parts of this module need none.)"""
+    cuda = torch._C
+    if dev != cuda._cuda_getDevice():
         with torch.cuda.device(dev):
             return _run(dev, stream, fn, args)
-    return fn(*args, _current_stream(dev) if stream is None else stream.cuda_stream)
+    return fn(*args, cuda._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
 
 
 def int4_pool_shape(num_blocks, num_kv_heads, block_size, head_dim):

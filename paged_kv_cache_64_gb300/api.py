@@ -316,6 +316,16 @@ def _explain(dev, **tensors):
     raise ValueError("arguments must be dense CUDA tensors on one device")
 
 
+def _check(fn_name, rc, **tensors):
+    """Raise unless rc is PA_OK; for PA_ERR_INVALID name the first of the tensors
+    that the library refuses for its address."""
+    if rc == _lib.PA_ERR_INVALID:
+        for name, t in tensors.items():
+            if t is not None and t.data_ptr() % 16:
+                raise ValueError(f"{name} must start on a 16-byte boundary")
+    _lib.check(fn_name, rc)
+
+
 def _run(dev, stream, fn, args):
     """fn(*args, stream handle) with `dev` current; stream None: its current
     stream.  (What torch.cuda's own calls end in, looked up here: builds of torch
@@ -385,7 +395,8 @@ def cache_write_int4(k_new, v_new, slot_mapping, k_pool, v_pool, k_out=None, v_o
     rc = _run(dev, stream, _lib.load().pa_cache_write_int4,
               (k_new.data_ptr(), v_new.data_ptr(), slot_mapping.data_ptr(), T, k_pool.data_ptr(),
                v_pool.data_ptr(), nb, hkv, d, bs, ko, vo, code))
-    _lib.check("pa_cache_write_int4", rc)
+    _check("pa_cache_write_int4", rc, k_new=k_new, v_new=v_new, k_pool=k_pool, v_pool=v_pool,
+           k_out=k_out, v_out=v_out)
 
 
 def cache_read_int4(k_out, v_out, slot_mapping, k_pool, v_pool, stream=None):
@@ -411,7 +422,7 @@ def cache_read_int4(k_out, v_out, slot_mapping, k_pool, v_pool, stream=None):
     rc = _run(dev, stream, _lib.load().pa_cache_read_int4,
               (k_out.data_ptr(), v_out.data_ptr(), slot_mapping.data_ptr(), T, k_pool.data_ptr(),
                v_pool.data_ptr(), nb, hkv, d, bs, code))
-    _lib.check("pa_cache_read_int4", rc)
+    _check("pa_cache_read_int4", rc, k_out=k_out, v_out=v_out, k_pool=k_pool, v_pool=v_pool)
 
 
 def int4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len,
@@ -471,7 +482,9 @@ def decode_int4(out, q, k_pool, v_pool, block_tables, seq_lens, max_seq_len, sca
             with torch.cuda.stream(stream):
                 workspace = alloc_workspace(need, q.device)
             rc = run(workspace)
-    _lib.check("pa_decode_int4", rc)
+        elif need and workspace.data_ptr() % 256:
+            raise ValueError("workspace must start on a 256-byte boundary")
+    _check("pa_decode_int4", rc, out=out, q=q, k_pool=k_pool, v_pool=v_pool)
     return workspace
 
 
@@ -483,6 +496,8 @@ def _token_step(t, name, T, own, d):
         step = own
     if one != 1 or (head != d and own != d) or step < own:
         raise ValueError(f"{name}: each token's heads must be dense and apart from the next's")
+    if step % 8:
+        raise ValueError(f"{name}: the step from a token to the next must be a multiple of 8 elements")
     return step
 
 
@@ -555,7 +570,8 @@ def qk_norm_rope(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, positions, sl
                k_weight.data_ptr(), float(eps), cos_sin.data_ptr(), table[0], table[1],
                1 if interleaved else 0, positions.data_ptr(), slot_mapping.data_ptr(), T,
                k_pool.data_ptr(), v_pool.data_ptr(), nb, hq, hkv, d, bs, fmt, ks, vs, code))
-    _lib.check("pa_qk_norm_rope", rc)
+    _check("pa_qk_norm_rope", rc, q_out=q_out, q=q, k=k, v=v, q_weight=q_weight, k_weight=k_weight,
+           cos_sin=cos_sin, k_pool=k_pool, v_pool=v_pool)
 
 
 def cascade_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,

@@ -156,12 +156,21 @@ struct Int4Piece {
 
 constexpr int kInt4Unit = kInt4Step * kInt4Warps;  // positions
 // Longest heads that one CTA each takes whole, of few and of many (sequence, KV
-// head) pairs.  Single pass against balanced ranges: 8 x 2 heads of 1024 13 and 14
-// us, of 2048 19 and 15; 128 x 2 of up to 2049 12.9 and 14.4 (chat lengths) or 16.6
-// and 15.5 (even ones), 32 x 2 8.7 and 10.6, 64 x 8 27 and 29, 256 x 8 68 and 75; 128
-// x 8 of up to 4096 77 and 68.
-constexpr int kInt4SinglePass = 1024, kInt4SinglePassMany = 2176;
-constexpr int kInt4ManyHeads = 64;
+// head) pairs.  Single pass against balanced ranges in us, of lengths that are all
+// the longest / spread from half of it on / log-normal about a tenth of it (x 2: 14
+// query heads of 64, x 8: 32 of 128, f16; 1024 heads and more than that stay faster
+// in one pass further on, to 4096 for even lengths):
+//            longest 1024                    2048                      2304
+//    8 x 2   9 9 / 9 10 / 9 11       14 10 / 14 11 / 14 13     15 11 / 15 11 / 15 11
+//    8 x 8   10 10 / 10 12 / 10 13   16 13 / 16 13 / 16 15     18 14 / 17 14 / 17 13
+//   16 x 8   10 12 / 10 14 / 10 15   16 17 / 16 16 / 16 16     18 20 / 17 16 / 17 15
+//   64 x 2   9 11 / 9 13 / 9 16      14 14 / 14 14 / 14 15     16 16 / 16 15 / 16 14
+//  128 x 2   12 14 / 12 14 / 10 16   18 20 / 17 18 / 15 16     20 22 / 19 18 / 17 15
+//   64 x 8   21 27 / 19 25 / 12 19   35 39 / 32 34 / 19 19     38 42 / 35 37 / 22 19
+//  128 x 8   37 40 / 35 36 / 19 22   60 65 / 54 55 / 28 29     65 71 / 61 59 / 33 28
+//  256 x 8   60 72 / 52 61 / 25 34   103 122 / 86 98 / 38 43   114 132 / 95 106 / 40 44
+constexpr int kInt4SinglePass = 1024, kInt4SinglePassMany = 2048;
+constexpr int kInt4ManyHeads = 128;
 constexpr int kInt4MinShare = 4;                   // units: smaller shares cost more than they save
 constexpr int kInt4MinSlack = 2;
 // A second wave pays where its shares are still long next to a CTA's start (2 us

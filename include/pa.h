@@ -357,8 +357,12 @@ pa_status pa_cache_read_int4(void *k_out, void *v_out, const int64_t *slot_mappi
  * NaN.
  * partition_tokens = 0: where heads are long, the batch's positions are shared
  * out evenly over the GPU from the lengths on the device (up to 1024 sequences)
- * and the pieces of heads that this cuts merged by a second launch; the result does not depend on the order in which they run.  Calls
- * that may overlap need workspaces of their own. */
+ * and the pieces of heads that this cuts merged by a second launch; the result
+ * does not depend on the order in which they run.  Calls that may overlap need
+ * workspaces of their own.
+ * Errors besides the output's rounding: as of an fp32 sum of terms of the size
+ * softmax(s)_p * max_j |V_i[p][j]| (a few 2^-21 of their sum), the weights as
+ * of scores rounded in fp32. */
 pa_status pa_decode_int4(void *out, const void *q, const void *k_pool, const void *v_pool,
                          int num_blocks, const int32_t *block_tables, int max_blocks_per_seq,
                          const int32_t *seq_lens, int max_seq_len, int num_seqs, int num_q_heads,

@@ -28,7 +28,10 @@
 // one sign: every other 16 positions enter as -P s' times 15 - n (a mask with an
 // exclusive or), which leaves 15 s' for their minimum to take over and keeps the
 // sums about zero.  (Without it a mean over 120,000 positions in one warp's sum
-// was off by 9e-2 of itself; with it by 2.0e-4, which is f16's own rounding.)
+// was off by 9e-2 of itself; with it by 2.0e-4, which is f16's own rounding.)  What
+// is left of the cut-off sums is about 2^-21 of the largest |v|, several times an fp32
+// sum's error and a fortieth of half a step of a bf16 output of 20,000 positions: 1.2%
+// of the outputs round to the other side than the exact value, 0.2% of an fp32 sum's.
 //
 // Why not tcgen05: its operands come from shared or tensor memory, where codes
 // would have to be stored again as 8- or 16-bit values, two to four times the
@@ -37,16 +40,16 @@
 // four heads), and the masks feed them from the registers the loads filled.
 //
 // Bounds: 136 bytes a position and KV head (D = 128).  256 sequences of 32 + 8
-// heads and 513 to 8192 positions: 215 us, 5.7 TB/s, 84% of the copy rate; 16 of
-// 64 + 8 heads and 16,385 to 32,768: 94 us, 67%; one of 200,003: 46 us, 69%.  The
-// first without its arithmetic takes 191 us.  No pipe is full (ALU 54%, issue 50%,
-// matrix unit 25% of cycles; eight heads: 50, 48 and 36%), but neither fewer
+// heads and 513 to 8192 positions: 219 us, 5.6 TB/s, 83% of the copy rate; 16 of
+// 64 + 8 heads and 16,385 to 32,768: 94 to 97 us, 66%; one of 200,003: 47 us, 68%.
+// The first without its arithmetic takes 191 us.  No pipe is full (ALU 53%, issue 51%,
+// matrix unit 25% of cycles; eight heads: 49, 49 and 36%), but neither fewer
 // instructions (12 of 240 for 16 positions: 1%) nor more warps (five or six CTAs an
 // SM with the queries in shared memory: 12 to 39% slower) nor the next keys'
 // products beside this step's values (4 to 7% slower) bring them together better.
 // Taking the weights' scale from the products, which are held across the check,
 // costs nothing against one taken from the scales (218 us for 219; the variants of
-// five to eight heads of 128 spill 20 bytes by it, 94.6 us for 94.0);
+// five to eight heads of 128 spill 24 bytes by it, 94.6 us for 94.0);
 // products formed anew after the check 224, a check of their own 224.
 //
 // A warp works alone: every fourth 32 positions of the CTA's piece, its own

@@ -75,8 +75,9 @@ enum RopeKind { kRopePairs, kRopeWhole, kRopePart };
 
 // CTAs an SM, at least: two warps of 64 registers a thread (16,411 tokens of 32 +
 // 8 + 8 heads of 128: 69.6 us; four warps a CTA 71 to 73 us, 80 registers 77 us,
-// 48 registers 76 us); up to 96 where 64 would spill, for the quantiser (85 us)
-// and the shuffles of partly rotated heads (83 us, 105 with 64).
+// 48 registers 76 us); up to 96 for the quantiser (78 us) and the shuffles of partly
+// rotated heads (half the head 77 us, 105 with 64; seven eighths 80), which would
+// spill much in 64.  Interleaved pairs keep 64 and spill 20 bytes: 71 us, 76 in 96.
 template <int FMT, int ROPE>
 constexpr int kNormRopeCtas = FMT == PA_KV_INT4 || ROPE == kRopePart ? 10 : 16;
 

@@ -347,8 +347,9 @@ pa_status pa_cache_read_int4(void *k_out, void *v_out, const int64_t *slot_mappi
 
 /* pa_decode_int4: pa_decode over 4-bit pools: out[i][h] =
  * sum_p softmax(s)_p * (m + s n)(V_i[p]) with s_p = scale * dot(q[i][h],
- * (m + s n)(K_i[p])), the stored values unrounded (and within fp32: m + 15 s of
- * a row of V is formed).  q finite, |scale q| below 2^170 and
+ * (m + s n)(K_i[p])), the stored values unrounded; m + 15 s of a row of V and the
+ * sum before its division are formed in fp32 (|V| L_i below 2^127 is safe).
+ * q finite, |scale q| below 2^170 and
  * the scores in fp32's range.  Arguments, partition_tokens and workspace as
  * pa_decode (pools as above, workspace size from
  * pa_decode_int4_workspace_size); the group size is at most 8;

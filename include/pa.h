@@ -348,14 +348,13 @@ pa_status pa_cache_read_int4(void *k_out, void *v_out, const int64_t *slot_mappi
 /* pa_decode_int4: pa_decode over 4-bit pools: out[i][h] =
  * sum_p softmax(s)_p * (m + s n)(V_i[p]) with s_p = scale * dot(q[i][h],
  * (m + s n)(K_i[p])), the stored values unrounded; m + 15 s of a row of V and the
- * sum before its division are formed in fp32 (|V| L_i below 2^127 is safe).
- * q finite, |scale q| below 2^170 and
- * the scores in fp32's range.  Arguments, partition_tokens and workspace as
- * pa_decode (pools as above, workspace size from
+ * sum before its division are formed in fp32 (|V| L_i below 2^116 is safe).
+ * q finite, |scale q| below 2^170 and the scores in fp32's range.  Arguments,
+ * partition_tokens and workspace as pa_decode (pools as above, workspace size from
  * pa_decode_int4_workspace_size); the group size is at most 8;
  * max_blocks_per_seq * block_size below 2^31, and that or max_seq_len at most
- * 2^30.  A row of NaN that a sequence reaches makes the outputs of its query heads
- * NaN.
+ * 2^30 (else PA_ERR_INVALID).  A row of NaN that a sequence reaches makes the
+ * outputs of its query heads NaN.
  * partition_tokens = 0: where heads are long, the batch's positions are shared
  * out evenly over the GPU from the lengths on the device (up to 1024 sequences)
  * and the pieces of heads that this cuts merged by a second launch; the result

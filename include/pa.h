@@ -418,6 +418,117 @@ pa_status pa_qk_norm_rope(void *q_out, int64_t q_out_stride, const void *q, int6
                           pa_kv_format kv_format, float k_scale, float v_scale, pa_dtype dtype,
                           void *stream);
 
+/* ------------------------------------------------------------------------
+ * Latent cache (a variant): one row a token and layer, shared by all heads:
+ * `rank` latent values c, which every head's own key and value are products
+ * of, and 64 rotated key values e that the heads share.
+ * Pool layout: dtype [num_blocks][block_size][rank + 64], 16-byte aligned; a
+ * block is a multiple of 16 bytes, so pa_copy_blocks copies such pools (the
+ * layers' pools given as K, the same or other layers' as V; block_bytes =
+ * block_size * (rank + 64) * 2).  rank in {256, 512}; block_size in
+ * {16, 32, 64}.
+ *
+ * pa_latent_norm_rope: what lies between a layer's projections and its
+ * attention, in one pass:
+ *   c = x * w / sqrt(mean(x^2) + eps)     over x = latent[t][0 .. rank)
+ *   for i < 32, with (a, b) = (y[i], y[i + 32]), or (y[2i], y[2i + 1]) when
+ *   interleaved, and cos, sin the position's table row:
+ *       (a, b) becomes (a cos_i - b sin_i, b cos_i + a sin_i)
+ *   for y = latent[t][rank .. rank + 64) and every head q[t][h][0 .. 64)
+ * in fp32 throughout, rounded to dtype once.  The turned queries go to q_out,
+ * the row (c, turned y) to the token's slot and to rows_out.
+ * Device pointers, 16-byte aligned:
+ *   q, q_out: 64 dense values a head; *_token_stride and *_head_stride
+ *     elements from a token and a head to the next (multiples of 8, at least
+ *     64), so that they may be the ends of wider heads; q_out may be q itself
+ *     with the same strides; its heads overlap neither one another nor any
+ *     other argument;
+ *   latent: rank + 64 dense values a token, latent_stride elements from a
+ *     token to the next (a multiple of 8, at least rank + 64);
+ *   weight [rank] of dtype;
+ *   cos_sin float [num_positions][64]: 32 cosines, then 32 sines (a position's
+ *     scaling for long contexts, of angles or of lengths, is the table's);
+ *   positions int64 [num_tokens], each in [0, num_positions): another value is
+ *     a bad index and its token is skipped (q_out, cache and rows_out left);
+ *   slot_mapping int64 [num_tokens] as in pa_cache_write, distinct (a negative
+ *     slot, or one past the pool, which is a bad index: no cache write, q_out
+ *     and rows_out still written);
+ *   rows_out: NULL, or [num_tokens][rank + 64] dense; overlaps nothing else.
+ * num_heads below 2^23; eps >= 0 and finite.
+ * ---------------------------------------------------------------------- */
+pa_status pa_latent_norm_rope(void *q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                              const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                              const void *latent, int64_t latent_stride, const void *weight,
+                              float eps, const float *cos_sin, int num_positions,
+                              int interleaved, const int64_t *positions,
+                              const int64_t *slot_mapping, int num_tokens, void *rows_out,
+                              void *pool, int num_blocks, int num_heads, int rank,
+                              int block_size, pa_dtype dtype, void *stream);
+
+/* pa_cache_read_latent: rows_out[t] = the row at slot slot_mapping[t], bit for
+ * bit ([num_tokens][rank + 64] dense).  A negative slot leaves its row as it
+ * was; a slot past the pool is a bad index (its row left too).  The same slot
+ * may be named more than once. */
+pa_status pa_cache_read_latent(void *rows_out, const int64_t *slot_mapping, int num_tokens,
+                               const void *pool, int num_blocks, int rank, int block_size,
+                               pa_dtype dtype, void *stream);
+
+/* pa_decode_latent: decode attention, one query token a sequence, in the
+ * absorbed form: with q[i][h] a head's query multiplied by its key expansion
+ * (rank values) and its turned rotary part (64), R_i[p] the row of position p
+ * of sequence i through its block table, L_i = seq_lens[i]:
+ *   s_p = scale * dot(q[i][h], R_i[p]),  p < L_i
+ *   out[i][h][:] = sum_p softmax(s)_p * R_i[p][0 .. rank)
+ * (the caller multiplies out by the head's value expansion).  L_i = 0 gives
+ * zero rows; slots past L_i are never read into the result, whatever they
+ * hold.  q [num_seqs][num_heads][rank + 64], out [num_seqs][num_heads][rank],
+ * dense, 16-byte aligned; block_tables, seq_lens, max_seq_len as in pa_decode;
+ * num_heads in 1 .. 1024, num_seqs up to 65535, num_blocks * block_size below
+ * 2^31, max_blocks_per_seq * block_size below 2^31 (else PA_ERR_INVALID).
+ * workspace: device memory of pa_decode_latent_workspace_size bytes, 256-byte
+ * aligned, no initialisation needed; calls that may overlap on the GPU need
+ * workspaces of their own.  The batch's positions are shared out evenly over
+ * the GPU from the lengths on the device, and the pieces of sequences that this
+ * cuts merged by a second launch; the result does not depend on the order in
+ * which they run.  The weights are rounded to dtype before they meet the
+ * values; their sum is not. */
+pa_status pa_decode_latent(void *out, const void *q, const void *pool, int num_blocks,
+                           const int32_t *block_tables, int max_blocks_per_seq,
+                           const int32_t *seq_lens, int max_seq_len, int num_seqs, int num_heads,
+                           int rank, int block_size, float scale, void *workspace,
+                           size_t workspace_bytes, pa_dtype dtype, void *stream);
+
+size_t pa_decode_latent_workspace_size(int num_seqs, int num_heads, int rank, int block_size,
+                                       int max_seq_len, pa_dtype dtype);
+
+/* pa_prefill_latent: attention of ragged prompts in the expanded form.  The
+ * queries of sequence i are tokens q_starts[i] .. q_starts[i + 1) of q, its keys
+ * and values (what is cached before them, then their own) tokens k_starts[i] ..
+ * k_starts[i + 1) of k, v and k_pe; n_q and n_k their counts.  For head h:
+ *   s_j = scale * (dot(q[a][h][0 .. 128), k[j][h]) + dot(q[a][h][128 .. 192), k_pe[j]))
+ *   out[a][h][:] = sum_j softmax(s)_j * v[j][h][:]
+ * over all j < n_k, or with causal != 0 those j <= n_k - n_q + (a's index in
+ * its sequence): the last query meets every key.  A query that meets no key
+ * gives a zero row.  Tokens outside every sequence's range are neither read
+ * into a result nor written.
+ * Device pointers, 16-byte aligned, of dtype: q [total_q][num_heads][192], k
+ * and v [total_k][num_heads][128], k_pe [total_k][64]: the innermost values
+ * dense, *_stride elements from a token or head to the next (multiples of 8, at
+ * least the inner size, below 2^38), so that k and v may be the halves of one
+ * product and k_pe the end of cached rows; out [total_q][num_heads][128] dense.
+ * k, v and k_pe may be NULL when total_k is 0.  Every v that a sequence of
+ * queries reaches must be finite.
+ * q_starts, k_starts int32 [num_seqs + 1].  A sequence whose starts decrease or
+ * leave [0, total], or with n_q > max_q_len, is a bad index (its rows left as
+ * they were).  num_heads in 1 .. 1024, num_seqs up to 65535. */
+pa_status pa_prefill_latent(void *out, const void *q, int64_t q_token_stride,
+                            int64_t q_head_stride, const void *k, int64_t k_token_stride,
+                            int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                            int64_t v_head_stride, const void *k_pe, int64_t k_pe_stride,
+                            const int32_t *q_starts, const int32_t *k_starts, int num_seqs,
+                            int total_q, int total_k, int max_q_len, int num_heads, float scale,
+                            int causal, pa_dtype dtype, void *stream);
+
 /* Partition size pa_decode uses for these shapes when partition_tokens = 0
  * (-1 means it will run single pass).  Needs the current CUDA device. */
 int pa_decode_auto_partition(int num_seqs, int num_kv_heads, int max_seq_len, int head_dim,

@@ -83,6 +83,16 @@ SIGNATURES = {
                                  _c_f, _vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _vp, _vp,
                                  _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_f, _c_f,
                                  _c_int, _vp]),
+    "pa_latent_norm_rope": (_c_int, [_vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _vp, _c_i64, _vp,
+                                     _c_f, _vp, _c_int, _c_int, _vp, _vp, _c_int, _vp, _vp, _c_int,
+                                     _c_int, _c_int, _c_int, _c_int, _vp]),
+    "pa_cache_read_latent": (_c_int, [_vp, _vp, _c_int, _vp, _c_int, _c_int, _c_int, _c_int, _vp]),
+    "pa_decode_latent": (_c_int, [_vp, _vp, _vp, _c_int, _vp, _c_int, _vp, _c_int, _c_int, _c_int,
+                                  _c_int, _c_int, _c_f, _vp, _c_sz, _c_int, _vp]),
+    "pa_decode_latent_workspace_size": (_c_sz, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int]),
+    "pa_prefill_latent": (_c_int, [_vp, _vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _vp, _c_i64,
+                                   _c_i64, _vp, _c_i64, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
+                                   _c_int, _c_f, _c_int, _c_int, _vp]),
     "pa_decode_auto_partition": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
                                           _c_int]),
     "pa_decode_fp8_auto_partition": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int,

@@ -574,6 +574,214 @@ def qk_norm_rope(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, positions, sl
            cos_sin=cos_sin, k_pool=k_pool, v_pool=v_pool)
 
 
+# Latent cache: one row of rank latent values and LATENT_ROPE shared key values a token.
+LATENT_ROPE = 64
+
+
+def _latent_pool(pool, dt):
+    """(blocks, block size, rank) of a pool of latent rows of type dt."""
+    shape = pool.shape
+    if len(shape) != 3 or shape[2] <= LATENT_ROPE:
+        raise ValueError(f"a latent pool must be [blocks, block size, rank + {LATENT_ROPE}]")
+    if pool.dtype is not dt:
+        raise TypeError("the pool must have the type of the other tensors")
+    return shape[0], shape[1], shape[2] - LATENT_ROPE
+
+
+def _steps(t, name):
+    """(token, head) steps in elements of t [T, heads, width]; a step that no
+    second token or head needs is given as that of a dense tensor."""
+    T, heads, width = t.shape
+    token, head, one = t.stride()
+    if heads <= 1:
+        head = width
+    if T <= 1:
+        token = max(head * heads, width)
+    if one != 1 and width > 1 and t.numel():
+        raise ValueError(f"{name}: the last dimension must be dense")
+    if token % 8 or head % 8:
+        raise ValueError(f"{name}: the steps of tokens and heads must be multiples of 8 elements")
+    if t.numel() and (token < width or head < width):
+        raise ValueError(f"{name}: tokens and heads must lie apart")
+    return token, head
+
+
+def latent_norm_rope(q_out, q, latent, weight, eps, cos_sin, positions, slot_mapping, pool,
+                     rows_out=None, interleaved=False, stream=None):
+    """RMS norm of each token's latent values, rotary positions of its shared key
+    values and of every query head's rotary part, and the write of its row into
+    the pool, in one pass (pa_latent_norm_rope).  q, q_out [T, H, 64] (tokens and
+    heads may be strided: the ends of wider heads; q_out may be q); latent
+    [T, rank + 64] (tokens may be strided); weight [rank]; cos_sin float32
+    [positions, 64] (cosines, sines); positions, slot_mapping int64 [T] (a slot
+    < 0: no cache write); pool [NB, B, rank + 64].  rows_out [T, rank + 64]
+    receives the rows too."""
+    qs, ls, dt = q.shape, latent.shape, q.dtype
+    if len(qs) != 3 or qs[2] != LATENT_ROPE or q_out.shape != qs:
+        raise ValueError(f"q and q_out must be [T, H, {LATENT_ROPE}]")
+    if not (latent.dtype is dt and q_out.dtype is dt and weight.dtype is dt):
+        raise TypeError("q, q_out, latent and weight must have one type")
+    T, heads = qs[0], qs[1]
+    nb, bs, rank = _latent_pool(pool, dt)
+    if len(ls) != 2 or ls != (T, rank + LATENT_ROPE):
+        raise ValueError(f"latent must be [T, {rank + LATENT_ROPE}]")
+    if weight.shape != (rank,) or positions.shape != (T,) or slot_mapping.shape != (T,):
+        raise ValueError("weight must be [rank], positions and slot_mapping [T]")
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != LATENT_ROPE:
+        raise ValueError(f"cos_sin must be [positions, {LATENT_ROPE}]")
+    if rows_out is not None and (rows_out.shape != ls or rows_out.dtype is not dt):
+        raise ValueError("rows_out must be like latent")
+    code = _dt(q)
+    dev = q.get_device()
+    if not (dev >= 0 and latent.get_device() == dev and q_out.get_device() == dev
+            and weight.get_device() == dev and cos_sin.get_device() == dev
+            and positions.get_device() == dev and slot_mapping.get_device() == dev
+            and pool.get_device() == dev and weight.is_contiguous() and cos_sin.is_contiguous()
+            and positions.is_contiguous() and slot_mapping.is_contiguous() and pool.is_contiguous()
+            and cos_sin.dtype is torch.float32 and positions.dtype is torch.int64
+            and slot_mapping.dtype is torch.int64
+            and (rows_out is None or (rows_out.get_device() == dev and rows_out.is_contiguous()))):
+        for name, t in (("q", q), ("latent", latent), ("q_out", q_out)):  # may be strided
+            if t.get_device() != dev or dev < 0:
+                raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
+        _explain(dev, weight=(weight, None), cos_sin=(cos_sin, torch.float32),
+                 positions=(positions, torch.int64), slot_mapping=(slot_mapping, torch.int64),
+                 pool=(pool, None), rows_out=(rows_out, None))
+    step, one = latent.stride()
+    if T <= 1:
+        step = rank + LATENT_ROPE
+    if one != 1 or step % 8 or step < rank + LATENT_ROPE:
+        raise ValueError("latent: each token's values must be dense, tokens a multiple of 8 apart")
+    rc = _run(dev, stream, _lib.load().pa_latent_norm_rope,
+              (q_out.data_ptr(), *_steps(q_out, "q_out"), q.data_ptr(), *_steps(q, "q"),
+               latent.data_ptr(), step, weight.data_ptr(), float(eps), cos_sin.data_ptr(),
+               cos_sin.shape[0], 1 if interleaved else 0, positions.data_ptr(),
+               slot_mapping.data_ptr(), T, None if rows_out is None else rows_out.data_ptr(),
+               pool.data_ptr(), nb, heads, rank, bs, code))
+    _check("pa_latent_norm_rope", rc, q_out=q_out, q=q, latent=latent, weight=weight,
+           cos_sin=cos_sin, pool=pool, rows_out=rows_out)
+
+
+def cache_read_latent(rows_out, slot_mapping, pool, stream=None):
+    """Cached tokens' rows out of a latent pool: rows_out [T, rank + 64] at
+    slot_mapping (int64 [T]; the row of a negative slot is left alone)."""
+    code = _dt(rows_out)
+    nb, bs, rank = _latent_pool(pool, rows_out.dtype)
+    T = rows_out.shape[0] if rows_out.dim() else 0
+    if rows_out.shape != (T, rank + LATENT_ROPE) or slot_mapping.shape != (T,):
+        raise ValueError(f"rows_out must be [T, {rank + LATENT_ROPE}], slot_mapping [T]")
+    dev = rows_out.get_device()
+    if not (dev >= 0 and rows_out.is_contiguous() and slot_mapping.is_contiguous()
+            and pool.is_contiguous() and slot_mapping.get_device() == dev
+            and pool.get_device() == dev and slot_mapping.dtype is torch.int64):
+        _explain(dev, rows_out=(rows_out, None), slot_mapping=(slot_mapping, torch.int64),
+                 pool=(pool, None))
+    rc = _run(dev, stream, _lib.load().pa_cache_read_latent,
+              (rows_out.data_ptr(), slot_mapping.data_ptr(), T, pool.data_ptr(), nb, rank, bs, code))
+    _check("pa_cache_read_latent", rc, rows_out=rows_out, pool=pool)
+
+
+def latent_workspace_size(num_seqs, num_heads, rank, block_size, max_seq_len, dtype):
+    return _lib.load().pa_decode_latent_workspace_size(num_seqs, num_heads, rank, block_size,
+                                                       max_seq_len, _DTYPES[dtype])
+
+
+def decode_latent(out, q, pool, block_tables, seq_lens, max_seq_len, scale, workspace=None,
+                  stream=None):
+    """Decode attention in the absorbed form over a latent pool
+    [NB, B, rank + 64]: q [S, H, rank + 64], out [S, H, rank].  workspace as for
+    decode (one allocated here is of latent_workspace_size bytes and tied to the
+    stream); returns the workspace used."""
+    qs, dt = q.shape, q.dtype
+    nb, bs, rank = _latent_pool(pool, dt)
+    if len(qs) != 3 or qs[2] != rank + LATENT_ROPE:
+        raise ValueError(f"q must be [S, H, {rank + LATENT_ROPE}]")
+    S, heads = qs[0], qs[1]
+    if out.shape != (S, heads, rank) or out.dtype is not dt:
+        raise ValueError(f"out must be [S, H, {rank}] of q's type")
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] != S or seq_lens.shape != (S,):
+        raise ValueError("block_tables must be [S, max_blocks], seq_lens [S]")
+    code = _dt(q)
+    dev = q.get_device()
+    if not (dev >= 0 and q.is_contiguous() and out.is_contiguous() and pool.is_contiguous()
+            and block_tables.is_contiguous() and seq_lens.is_contiguous()
+            and out.get_device() == dev and pool.get_device() == dev
+            and block_tables.get_device() == dev and seq_lens.get_device() == dev
+            and block_tables.dtype is torch.int32 and seq_lens.dtype is torch.int32):
+        _explain(dev, q=(q, None), out=(out, None), pool=(pool, None),
+                 block_tables=(block_tables, torch.int32), seq_lens=(seq_lens, torch.int32))
+    fn = _lib.load().pa_decode_latent
+    max_len = int(max_seq_len)
+    args = (out.data_ptr(), q.data_ptr(), pool.data_ptr(), nb, block_tables.data_ptr(), tables[1],
+            seq_lens.data_ptr(), max_len, S, heads, rank, bs, float(scale))
+
+    def run(ws):
+        if ws is None:
+            return _run(dev, stream, fn, args + (None, 0, code))
+        if ws.get_device() != dev or not ws.is_contiguous():
+            _explain(dev, workspace=(ws, None))
+        return _run(dev, stream, fn, args + (ws.data_ptr(), ws.nbytes, code))
+
+    rc = run(workspace)
+    if rc == _lib.PA_ERR_INVALID:  # perhaps for want of a workspace: nothing was launched
+        with torch.cuda.device(dev):
+            need = latent_workspace_size(S, heads, rank, bs, max_len, dt)
+        if need and (workspace is None or workspace.nbytes < need):
+            # from the stream's own memory: a block freed on another stream may
+            # still be in use there
+            with torch.cuda.stream(stream):
+                workspace = alloc_workspace(need, q.device)
+            rc = run(workspace)
+        elif need and workspace.data_ptr() % 256:
+            raise ValueError("workspace must start on a 256-byte boundary")
+    _check("pa_decode_latent", rc, out=out, q=q, pool=pool)
+    return workspace
+
+
+def prefill_latent(out, q, k, v, k_pe, q_starts, k_starts, max_q_len, scale, causal=True,
+                   stream=None):
+    """Attention of ragged prompts in the expanded form of latent attention
+    (pa_prefill_latent).  q [Tq, H, 192] (128 values of the head, 64 rotary);
+    k, v [Tk, H, 128]; k_pe [Tk, 64]; out [Tq, H, 128].  Tokens and heads of q,
+    k, v and tokens of k_pe may be strided (halves of one product; the ends of
+    cached rows).  q_starts, k_starts int32 [S + 1]: where each sequence's
+    queries and keys begin; with causal, a sequence's last query meets its last
+    key."""
+    qs, ks, dt = q.shape, k.shape, q.dtype
+    if len(qs) != 3 or qs[2] != 192 or len(ks) != 3 or ks[1:] != (qs[1], 128) or v.shape != ks:
+        raise ValueError("q must be [Tq, H, 192], k and v [Tk, H, 128]")
+    if k_pe.shape != (ks[0], LATENT_ROPE) or out.shape != (qs[0], qs[1], 128):
+        raise ValueError(f"k_pe must be [Tk, {LATENT_ROPE}], out [Tq, H, 128]")
+    if not (k.dtype is dt and v.dtype is dt and k_pe.dtype is dt and out.dtype is dt):
+        raise TypeError("q, k, v, k_pe and out must have one type")
+    if q_starts.dim() != 1 or q_starts.shape[0] < 1 or k_starts.shape != q_starts.shape:
+        raise ValueError("q_starts and k_starts must both be [S + 1]")
+    code = _dt(q)
+    dev = q.get_device()
+    if not (dev >= 0 and k.get_device() == dev and v.get_device() == dev
+            and k_pe.get_device() == dev and out.get_device() == dev and out.is_contiguous()
+            and q_starts.get_device() == dev and k_starts.get_device() == dev
+            and q_starts.is_contiguous() and k_starts.is_contiguous()
+            and q_starts.dtype is torch.int32 and k_starts.dtype is torch.int32):
+        for name, t in (("q", q), ("k", k), ("v", v), ("k_pe", k_pe)):  # may be strided
+            if t.get_device() != dev or dev < 0:
+                raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
+        _explain(dev, out=(out, None), q_starts=(q_starts, torch.int32),
+                 k_starts=(k_starts, torch.int32))
+    pe_step, one = k_pe.stride()
+    if ks[0] <= 1:
+        pe_step = LATENT_ROPE
+    if one != 1 or pe_step % 8 or pe_step < LATENT_ROPE:
+        raise ValueError("k_pe: each token's values must be dense, tokens a multiple of 8 apart")
+    rc = _run(dev, stream, _lib.load().pa_prefill_latent,
+              (out.data_ptr(), q.data_ptr(), *_steps(q, "q"), k.data_ptr(), *_steps(k, "k"),
+               v.data_ptr(), *_steps(v, "v"), k_pe.data_ptr(), pe_step, q_starts.data_ptr(),
+               k_starts.data_ptr(), q_starts.shape[0] - 1, qs[0], ks[0], int(max_q_len), qs[1],
+               float(scale), 1 if causal else 0, code))
+    _check("pa_prefill_latent", rc, out=out, q=q, k=k, v=v, k_pe=k_pe)
+
+
 def cascade_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                            max_seq_len, prefix_len, dtype):
     return _lib.load().pa_decode_cascade_workspace_size(num_seqs, num_q_heads, num_kv_heads,

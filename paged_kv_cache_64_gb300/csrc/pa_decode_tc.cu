@@ -61,6 +61,20 @@ bool pool_tensor_map_fp8(CUtensorMap *map, const void *pool, int64_t rows, int D
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool rows_tensor_map(CUtensorMap *map, const void *base, int rank, const int64_t *dims,
+                     const int64_t *steps, int box_rows, bool bf16) {
+    EncodeTiledFn enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t extent[3], stride[2];
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
+    for (int i = 0; i < rank; ++i) extent[i] = (cuuint64_t)dims[i];
+    for (int i = 0; i + 1 < rank; ++i) stride[i] = (cuuint64_t)steps[i] * 2;
+    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+               (cuuint32_t)rank, const_cast<void *>(base), extent, stride, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, bool SPAN, bool COMPACT>
 static TcKernel tc_variant(bool bf16) {
     return bf16 ? paged_decode_tc_kernel<true, D, SPAN, COMPACT, 0>

@@ -194,6 +194,18 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float *v) {
         "r"(__float_as_uint(v[30])), "r"(__float_as_uint(v[31]))
         : "memory");
 }
+__device__ __forceinline__ void tmem_store16(uint32_t taddr, const float (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+        "%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+        "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+        "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
+        "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+        "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
+        "r"(__float_as_uint(v[15]))
+        : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -235,5 +247,10 @@ bool pool_tensor_map(CUtensorMap *map, const void *pool, int64_t rows, int D, bo
 // (row-major) or with the swizzle of a K-major operand of d-byte rows
 // (128-byte swizzle for d = 128, 64-byte for d = 64).
 bool pool_tensor_map_fp8(CUtensorMap *map, const void *pool, int64_t rows, int D, bool swizzle);
+// A tensor of 16-bit elements with `rank` (2 or 3) dimensions, the first dense,
+// steps in elements of the others; boxes of 64 x box_rows (x 1) elements, 128-byte
+// swizzle; elements past the extents read as zero.
+bool rows_tensor_map(CUtensorMap *map, const void *base, int rank, const int64_t *dims,
+                     const int64_t *steps, int box_rows, bool bf16);
 
 }  // namespace pa

@@ -94,6 +94,19 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
     }
 }
 
+// mbar_wait that also ends, with false, once another role of the CTA gave up.
+__device__ __forceinline__ bool mbar_wait_or(uint64_t *bar, uint32_t parity,
+                                             volatile int *abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_timer_ns();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag || global_timer_ns() - t0 > kWaitLimitNs) return false;
+    }
+}
+
 // 1-D bulk copy global -> shared; completion is signalled as `bytes`
 // transaction bytes on `bar`.  Addresses 16-byte aligned, bytes % 16 == 0.
 __device__ __forceinline__ void bulk_copy_g2s(void *dst, const void *src, uint32_t bytes,

@@ -131,18 +131,6 @@ struct LatWalk {
     }
 };
 
-// Bounded wait that also ends when another role gave up.
-__device__ __forceinline__ bool lat_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = global_timer_ns();
-    for (;;) {
-#pragma unroll 1
-        for (int i = 0; i < 32; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag || global_timer_ns() - t0 > kWaitLimitNs) return false;
-    }
-}
-
 // Named barrier 1 over the 128 softmax threads, true on all if any passed true.
 __device__ __forceinline__ bool softmax_bar128_or(bool v) {
     int any;
@@ -279,7 +267,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                 const int nu = min(units - 4 * t, 4);
                 const int row = __shfl_sync(kFullMask, rows_cur, ((t & 7) * 4 + (lane & 3)) & 31);
                 if (rope_use > 0)
-                    ok = lat_wait(&bar[S::ROPE_EMPTY + rope], (rope_use - 1) & 1, abort_flag);
+                    ok = mbar_wait_or(&bar[S::ROPE_EMPTY + rope], (rope_use - 1) & 1, abort_flag);
                 ok = __all_sync(kFullMask, ok);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(&bar[S::ROPE_FULL + rope], nu * 2048);
@@ -291,7 +279,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
 #pragma unroll
                 for (int j = 0; j < S::PAIRS; ++j) {
                     if (ok && pair_use > 0)
-                        ok = lat_wait(&bar[S::PAIR_EMPTY + pair], (pair_use - 1) & 1, abort_flag);
+                        ok = mbar_wait_or(&bar[S::PAIR_EMPTY + pair], (pair_use - 1) & 1, abort_flag);
                     ok = __all_sync(kFullMask, ok);
                     if (!ok) break;
                     if (lane == 0) mbar_arrive_expect_tx(&bar[S::PAIR_FULL + pair], nu * 4096);
@@ -321,11 +309,11 @@ __global__ void __launch_bounds__(kLatThreads, 1)
             int pair = 0, pair_use = 0, rope = 0, rope_use = 0, g = 0, piece = 0;
             for (; ok && walk.next(); walk.advance()) {
                 if (walk.len == 0) continue;
-                ok = lat_wait(&bar[S::Q_FULL], piece & 1, abort_flag);
+                ok = mbar_wait_or(&bar[S::Q_FULL], piece & 1, abort_flag);
                 for (int t = 0; ok && t < walk.n; ++t, ++g) {
                     const int b = g & 1;
-                    if (g >= 2) ok = lat_wait(&bar[S::S_FREE + b], ((g >> 1) - 1) & 1, abort_flag);
-                    ok = ok && lat_wait(&bar[S::ROPE_FULL + rope], rope_use & 1, abort_flag);
+                    if (g >= 2) ok = mbar_wait_or(&bar[S::S_FREE + b], ((g >> 1) - 1) & 1, abort_flag);
+                    ok = ok && mbar_wait_or(&bar[S::ROPE_FULL + rope], rope_use & 1, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t d = tmem + S::S_COL + kLatTile * b;
@@ -339,7 +327,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                     if (++rope == S::ROPE_SLOTS) rope = 0, ++rope_use;
 #pragma unroll 1
                     for (int j = 0; j < S::PAIRS; ++j) {
-                        ok = lat_wait(&bar[S::PAIR_FULL + pair], pair_use & 1, abort_flag);
+                        ok = mbar_wait_or(&bar[S::PAIR_FULL + pair], pair_use & 1, abort_flag);
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t ka = base + S::OFF_PAIR + pair * 2 * S::SLAB;
@@ -368,14 +356,14 @@ __global__ void __launch_bounds__(kLatThreads, 1)
             int pair = 0, pair_use = 0, g = 0, piece = 0;
             for (; ok && walk.next(); walk.advance()) {
                 if (walk.len == 0) continue;
-                if (piece > 0) ok = lat_wait(&bar[S::O_FREE], (piece - 1) & 1, abort_flag);
+                if (piece > 0) ok = mbar_wait_or(&bar[S::O_FREE], (piece - 1) & 1, abort_flag);
                 for (int t = 0; ok && t < walk.n; ++t, ++g) {
                     const int pb = g % S::P_BUFS;
-                    ok = lat_wait(&bar[S::P_FULL + pb], (g / S::P_BUFS) & 1, abort_flag);
+                    ok = mbar_wait_or(&bar[S::P_FULL + pb], (g / S::P_BUFS) & 1, abort_flag);
                     const uint32_t pa = base + S::OFF_P + pb * S::P_BYTES;
 #pragma unroll 1
                     for (int j = 0; ok && j < S::PAIRS; ++j) {
-                        ok = lat_wait(&bar[S::PAIR_FULL + pair], pair_use & 1, abort_flag);
+                        ok = mbar_wait_or(&bar[S::PAIR_FULL + pair], pair_use & 1, abort_flag);
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t va = base + S::OFF_PAIR + pair * 2 * S::SLAB;
@@ -401,7 +389,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
             int piece = 0;
             for (; ok && walk.next(); walk.advance()) {
                 if (walk.len == 0) continue;
-                if (piece > 0) ok = lat_wait(&bar[S::Q_FREE], (piece - 1) & 1, abort_flag);
+                if (piece > 0) ok = mbar_wait_or(&bar[S::Q_FREE], (piece - 1) & 1, abort_flag);
                 if (!ok) break;
                 mbar_arrive_expect_tx(&bar[S::Q_FULL], S::SLABS * S::Q_SLAB);
                 // rows past the last sequence read as zero, other heads' rows as they are
@@ -429,7 +417,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         // phases are waited for in turn: a tile's is, at the latest, before P goes into
         // its buffer again.
         auto pv_done = [&](int k) -> bool {
-            return lat_wait(&bar[S::PV_DONE + k % S::P_BUFS], (k / S::P_BUFS) & 1, abort_flag);
+            return mbar_wait_or(&bar[S::PV_DONE + k % S::P_BUFS], (k / S::P_BUFS) & 1, abort_flag);
         };
         for (; ok && walk.next(); walk.advance()) {
             const int64_t out_row = (int64_t)walk.seq * p.num_heads + group * NH;
@@ -443,7 +431,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
             float m_run = -INFINITY, l_run = 0.f;
             for (int t = 0; t < walk.n; ++t, ++g) {
                 const int b = g & 1;
-                bool fine = lat_wait(&bar[S::S_FULL + b], (g >> 1) & 1, abort_flag);
+                bool fine = mbar_wait_or(&bar[S::S_FULL + b], (g >> 1) & 1, abort_flag);
                 fine = __all_sync(kFullMask, fine);
                 float s[kLatTile];
                 if (fine) {
@@ -489,7 +477,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                     // rows past the length: P is 0 there, and V must be finite
                     int pair = pair0;
                     for (int j = 0; j < S::PAIRS; ++j) {
-                        fine = fine && lat_wait(&bar[S::PAIR_FULL + pair],
+                        fine = fine && mbar_wait_or(&bar[S::PAIR_FULL + pair],
                                                 ((g * S::PAIRS + j) / S::PAIR_SLOTS) & 1, abort_flag);
                         uint8_t *slab = smem + S::OFF_PAIR + pair * 2 * S::SLAB;
                         for (int i = valid * 8 + quad * 32 + lane; i < kLatTile * 8; i += 128) {

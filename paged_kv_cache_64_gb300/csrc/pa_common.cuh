@@ -107,6 +107,49 @@ __device__ __forceinline__ bool mbar_wait_or(uint64_t *bar, uint32_t parity,
     }
 }
 
+// The same for a warp that issues tensor-core instructions: no result, so that the
+// control flow around it is the warp's own and their descriptors stay in uniform
+// registers (64 clocks an instruction otherwise, whatever its shape).  A wait that
+// ran out, or found that another role gave up, leaves the flag set; the warp runs on
+// over whatever is there, without waiting again.
+__device__ __forceinline__ void mbar_wait_flow(uint64_t *bar, uint32_t parity, int *abort_flag) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 f;\n\t.reg .b64 t0, t1;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
+        "@p bra DONE;\n\t"
+        "mov.u64 t0, %%globaltimer;\n\t"
+        "AGAIN:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
+        "@p bra DONE;\n\t"
+        "ld.volatile.shared.u32 f, [%2];\n\t"
+        "setp.ne.u32 p, f, 0;\n\t"
+        "@p bra DONE;\n\t"
+        "mov.u64 t1, %%globaltimer;\n\t"
+        "sub.u64 t1, t1, t0;\n\t"
+        "setp.lt.u64 p, t1, %3;\n\t"
+        "@p bra AGAIN;\n\t"
+        "st.volatile.shared.u32 [%2], 1;\n\t"
+        "DONE:\n\t}" ::"r"(smem_addr(bar)),
+        "r"(parity), "r"(smem_addr(abort_flag)), "l"(kWaitLimitNs)
+        : "memory");
+}
+
+// One lane of a converged warp, the same at every call.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
+// The warp's index, as a value that the compiler knows to be the same in its lanes.
+__device__ __forceinline__ int uniform_warp() {
+    return __shfl_sync(kFullMask, (int)(threadIdx.x >> 5), 0);
+}
+
 // 1-D bulk copy global -> shared; completion is signalled as `bytes`
 // transaction bytes on `bar`.  Addresses 16-byte aligned, bytes % 16 == 0.
 __device__ __forceinline__ void bulk_copy_g2s(void *dst, const void *src, uint32_t bytes,

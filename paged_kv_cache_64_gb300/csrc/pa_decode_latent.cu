@@ -157,11 +157,12 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + S::OFF_MISC);
     int *words = reinterpret_cast<int *>(smem + S::OFF_WORDS);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(words);
-    volatile int *abort_flag = words + 1;
+    int *flag = words + 1;
+    volatile int *abort_flag = flag;
     int *scan = words + 8;  // [8] warp sums, then start sequence and tile
     float *alphas = reinterpret_cast<float *>(smem + S::OFF_ALPHA);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int group = blockIdx.x % p.groups, range = blockIdx.x / p.groups;
     if (threadIdx.x == 0) {
         prefetch_tensormap(&map_rows);
@@ -303,85 +304,90 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------- q.K^T
-        if (lane == 0) {
-            constexpr uint32_t idesc = f16_idesc(BF16, false, false, 64, kLatTile);
-            const uint32_t base = smem_addr(smem);
-            int pair = 0, pair_use = 0, rope = 0, rope_use = 0, g = 0, piece = 0;
-            for (; ok && walk.next(); walk.advance()) {
-                if (walk.len == 0) continue;
-                ok = mbar_wait_or(&bar[S::Q_FULL], piece & 1, abort_flag);
-                for (int t = 0; ok && t < walk.n; ++t, ++g) {
-                    const int b = g & 1;
-                    if (g >= 2) ok = mbar_wait_or(&bar[S::S_FREE + b], ((g >> 1) - 1) & 1, abort_flag);
-                    ok = ok && mbar_wait_or(&bar[S::ROPE_FULL + rope], rope_use & 1, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t d = tmem + S::S_COL + kLatTile * b;
+        constexpr uint32_t idesc = f16_idesc(BF16, false, false, 64, kLatTile);
+        const uint32_t base = smem_addr(smem);
+        const uint64_t q_desc = sw128_desc(base + S::OFF_Q, 16, 1024);
+        const uint64_t pair_desc = sw128_desc(base + S::OFF_PAIR, 16, 1024);
+        const uint64_t rope_desc = sw128_desc(base + S::OFF_ROPE, 16, 1024);
+        int pair = 0, pair_use = 0, rope = 0, rope_use = 0, g = 0, piece = 0;
+        for (; walk.next(); walk.advance()) {
+            if (walk.len == 0) continue;
+            mbar_wait_flow(&bar[S::Q_FULL], piece & 1, flag);
+            for (int t = 0; t < walk.n; ++t, ++g) {
+                const int b = g & 1;
+                if (g >= 2) mbar_wait_flow(&bar[S::S_FREE + b], ((g >> 1) - 1) & 1, flag);
+                mbar_wait_flow(&bar[S::ROPE_FULL + rope], rope_use & 1, flag);
+                tc_fence_after();
+                const uint32_t d = tmem + S::S_COL + kLatTile * b;
+                if (elect_one()) {
+                    const uint64_t k = rope_desc + rope * (S::SLAB >> 4);
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        tc_mma(d,
-                               sw128_desc(base + S::OFF_Q + (S::SLABS - 1) * S::Q_SLAB + ks * 32, 16, 1024),
-                               sw128_desc(base + S::OFF_ROPE + rope * S::SLAB + ks * 32, 16, 1024), idesc,
-                               ks > 0);
+                        tc_mma(d, q_desc + (((S::SLABS - 1) * S::Q_SLAB + ks * 32) >> 4), k + ks * 2,
+                               idesc, ks > 0);
                     tc_commit(&bar[S::ROPE_EMPTY + rope]);
-                    if (++rope == S::ROPE_SLOTS) rope = 0, ++rope_use;
-#pragma unroll 1
-                    for (int j = 0; j < S::PAIRS; ++j) {
-                        ok = mbar_wait_or(&bar[S::PAIR_FULL + pair], pair_use & 1, abort_flag);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t ka = base + S::OFF_PAIR + pair * 2 * S::SLAB;
-                        const uint32_t qa = base + S::OFF_Q + 2 * j * S::Q_SLAB;
+                }
+                __syncwarp();
+                if (++rope == S::ROPE_SLOTS) rope = 0, ++rope_use;
+#pragma unroll
+                for (int j = 0; j < S::PAIRS; ++j) {
+                    mbar_wait_flow(&bar[S::PAIR_FULL + pair], pair_use & 1, flag);
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t k = pair_desc + pair * (2 * S::SLAB >> 4);
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
-                            tc_mma(d, sw128_desc(qa + (ks >> 2) * S::Q_SLAB + (ks & 3) * 32, 16, 1024),
-                                   sw128_desc(ka + (ks >> 2) * S::SLAB + (ks & 3) * 32, 16, 1024), idesc, 1);
-                        if (++pair == S::PAIR_SLOTS) pair = 0, ++pair_use;
+                            tc_mma(d,
+                                   q_desc + (((2 * j + (ks >> 2)) * S::Q_SLAB + (ks & 3) * 32) >> 4),
+                                   k + (((ks >> 2) * S::SLAB + (ks & 3) * 32) >> 4), idesc, 1);
+                        if (j + 1 == S::PAIRS) {
+                            if (t + 1 == walk.n) tc_commit(&bar[S::Q_FREE]);
+                            tc_commit(&bar[S::S_FULL + b]);
+                        }
                     }
-                    if (!ok) break;
-                    if (t + 1 == walk.n) tc_commit(&bar[S::Q_FREE]);
-                    tc_commit(&bar[S::S_FULL + b]);
+                    __syncwarp();
+                    if (++pair == S::PAIR_SLOTS) pair = 0, ++pair_use;
                 }
-                ++piece;
             }
-            tc_commit(&bar[S::DRAIN]);
-            (void)mbar_wait(&bar[S::DRAIN], 0);
+            ++piece;
         }
+        if (elect_one()) tc_commit(&bar[S::DRAIN]);
+        (void)mbar_wait(&bar[S::DRAIN], 0);
         __syncwarp();
     } else if (warp == 6) {
         // ---------------------------------------------------------- P.V
-        if (lane == 0) {
-            constexpr uint32_t idesc = f16_idesc(BF16, true, false, 128, NH);
-            const uint32_t base = smem_addr(smem);
-            int pair = 0, pair_use = 0, g = 0, piece = 0;
-            for (; ok && walk.next(); walk.advance()) {
-                if (walk.len == 0) continue;
-                if (piece > 0) ok = mbar_wait_or(&bar[S::O_FREE], (piece - 1) & 1, abort_flag);
-                for (int t = 0; ok && t < walk.n; ++t, ++g) {
-                    const int pb = g % S::P_BUFS;
-                    ok = mbar_wait_or(&bar[S::P_FULL + pb], (g / S::P_BUFS) & 1, abort_flag);
-                    const uint32_t pa = base + S::OFF_P + pb * S::P_BYTES;
-#pragma unroll 1
-                    for (int j = 0; ok && j < S::PAIRS; ++j) {
-                        ok = mbar_wait_or(&bar[S::PAIR_FULL + pair], pair_use & 1, abort_flag);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t va = base + S::OFF_PAIR + pair * 2 * S::SLAB;
+        constexpr uint32_t idesc = f16_idesc(BF16, true, false, 128, NH);
+        const uint32_t base = smem_addr(smem);
+        const uint64_t p_desc = sw128_desc(base + S::OFF_P, 16, 1024);
+        const uint64_t pair_desc = sw128_desc(base + S::OFF_PAIR, S::SLAB, 1024);
+        int pair = 0, pair_use = 0, g = 0, piece = 0;
+        for (; walk.next(); walk.advance()) {
+            if (walk.len == 0) continue;
+            if (piece > 0) mbar_wait_flow(&bar[S::O_FREE], (piece - 1) & 1, flag);
+            for (int t = 0; t < walk.n; ++t, ++g) {
+                const int pb = g % S::P_BUFS;
+                mbar_wait_flow(&bar[S::P_FULL + pb], (g / S::P_BUFS) & 1, flag);
+                const uint64_t w = p_desc + pb * (S::P_BYTES >> 4);
+#pragma unroll
+                for (int j = 0; j < S::PAIRS; ++j) {
+                    mbar_wait_flow(&bar[S::PAIR_FULL + pair], pair_use & 1, flag);
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t v = pair_desc + pair * (2 * S::SLAB >> 4);
 #pragma unroll
                         for (int ks = 0; ks < kLatTile / 16; ++ks)
-                            tc_mma(tmem + j * NH, sw128_desc(va + ks * 2048, S::SLAB, 1024),
-                                   sw128_desc(pa + ks * 32, 16, 1024), idesc, t > 0 || ks > 0);
+                            tc_mma(tmem + j * NH, v + ks * (2048 >> 4), w + ks * 2, idesc, t > 0 || ks > 0);
                         tc_commit(&bar[S::PAIR_EMPTY + pair]);
-                        if (++pair == S::PAIR_SLOTS) pair = 0, ++pair_use;
+                        if (j + 1 == S::PAIRS) tc_commit(&bar[S::PV_DONE + pb]);
                     }
-                    if (!ok) break;
-                    tc_commit(&bar[S::PV_DONE + pb]);
+                    __syncwarp();
+                    if (++pair == S::PAIR_SLOTS) pair = 0, ++pair_use;
                 }
-                ++piece;
             }
-            tc_commit(&bar[S::DRAIN + 1]);
-            (void)mbar_wait(&bar[S::DRAIN + 1], 0);
+            ++piece;
         }
+        if (elect_one()) tc_commit(&bar[S::DRAIN + 1]);
+        (void)mbar_wait(&bar[S::DRAIN + 1], 0);
         __syncwarp();
     } else if (warp == 7) {
         // ---------------------------------------------------------- Q
@@ -580,12 +586,10 @@ __global__ void __launch_bounds__(kLatThreads, 1)
             p.plan[range] = ok ? plan : make_int4(-1, 0, 0, 0);
         }
     }
-    if (!ok && lane == 0) {
-        record_error(p.err, PA_ERR_DEVICE_TIMEOUT);
-        *abort_flag = 1;
-    }
+    if (!ok) *abort_flag = 1;
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) record_error(p.err, PA_ERR_DEVICE_TIMEOUT);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);

@@ -67,12 +67,13 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kPreOffBar);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kPreOffBar + 384);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kPreOffBar + 392);
+    int *flag = reinterpret_cast<int *>(smem + kPreOffBar + 392);
+    volatile int *abort_flag = flag;
     static_assert(kPreBars * 8 <= 384, "barriers");
 
     // the longest tiles of a causal sequence first
     const int qt = gridDim.x - 1 - blockIdx.x, head = blockIdx.y, seq = blockIdx.z;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     pdl_wait();
     const int q0 = p.q_starts[seq], n_q = p.q_starts[seq + 1] - q0;
     const int k0 = p.k_starts[seq], n_k = p.k_starts[seq + 1] - k0;
@@ -92,8 +93,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         const int keys = p.causal ? min(reach + b - 1, n_k) : n_k;
         return keys > 0 ? (keys + kPreKeys - 1) / kPreKeys : 0;
     };
-    const int tiles[2] = {tiles_of(0), tiles_of(1)};
-    const int most = max(tiles[0], tiles[1]);
+    const int tiles0 = tiles_of(0), tiles1 = tiles_of(1), most = max(tiles0, tiles1);
 
     if (threadIdx.x == 0) {
         prefetch_tensormap(&map_q);
@@ -141,73 +141,79 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 return true;
             };
             int u = 0;
-            if (tiles[0] > 0) load_q(0);
+            if (tiles0 > 0) load_q(0);
             for (; u < 3; ++u) load(u);
-            if (tiles[1] > 0) load_q(1);
+            if (tiles1 > 0) load_q(1);
             for (; ok && u < 5 * most; u += ok) ok = load(u);
             // every copy has landed before shared memory goes (each slot's last use)
             for (int s = max(0, u - kPreSlots); s < u; ++s)
                 (void)mbar_wait(&bar[kPreFull + s % kPreSlots], (s / kPreSlots) & 1);
-            for (int x = 0; x < 2; ++x)
-                if (tiles[x] > 0) (void)mbar_wait(&bar[kPreQFull + x], 0);
+            if (tiles0 > 0) (void)mbar_wait(&bar[kPreQFull], 0);
+            if (tiles1 > 0) (void)mbar_wait(&bar[kPreQFull + 1], 0);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------- products
-        if (lane == 0 && most > 0) {
-            constexpr uint32_t idesc_qk = f16_idesc(BF16, false, false, kPreRows, kPreKeys);
-            constexpr uint32_t idesc_pv = f16_idesc(BF16, false, true, kPreRows, 64);
-            const uint32_t base = smem_addr(smem);
-            auto slab = [&](int u) -> uint32_t { return base + kPreOffRing + (u % kPreSlots) * kPreSlab; };
-            auto landed = [&](int u) -> bool {
-                return mbar_wait_or(&bar[kPreFull + u % kPreSlots], (u / kPreSlots) & 1, abort_flag);
-            };
-            // tile B uses a slab last where it reaches that far
-            auto last_user = [&](int x, int t) -> bool { return x == 1 || t >= tiles[1]; };
-            auto issue_qk = [&](int x, int t) -> bool {
-                if (t == 0 && !mbar_wait_or(&bar[kPreQFull + x], 0, abort_flag)) return false;
-                for (int i = 0; i < 3; ++i) {
-                    if (!landed(5 * t + i)) return false;
-                    tc_fence_after();
-                    const uint32_t qa = base + (3 * x + i) * kPreSlab, ka = slab(5 * t + i);
+        constexpr uint32_t idesc_qk = f16_idesc(BF16, false, false, kPreRows, kPreKeys);
+        constexpr uint32_t idesc_pv = f16_idesc(BF16, false, true, kPreRows, 64);
+        const uint32_t base = smem_addr(smem);
+        const uint64_t q_desc = sw128_desc(base, 16, 1024);
+        const uint64_t k_desc = sw128_desc(base + kPreOffRing, 16, 1024);
+        const uint64_t v_desc = sw128_desc(base + kPreOffRing, kPreSlab, 1024);
+        auto issue_qk = [&](int x, int t) {
+            if (t == 0) mbar_wait_flow(&bar[kPreQFull + x], 0, flag);
+            const bool last = x == 1 || t >= tiles1;  // tile B uses a slab last where it reaches it
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                const int u = 5 * t + i, slot = u % kPreSlots;
+                mbar_wait_flow(&bar[kPreFull + slot], (u / kPreSlots) & 1, flag);
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t q = q_desc + ((3 * x + i) * kPreSlab >> 4);
+                    const uint64_t k = k_desc + slot * (kPreSlab >> 4);
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        tc_mma(tmem + kPreColS + 128 * x, sw128_desc(qa + ks * 32, 16, 1024),
-                               sw128_desc(ka + ks * 32, 16, 1024), idesc_qk, i > 0 || ks > 0);
-                    if (last_user(x, t)) tc_commit(&bar[kPreEmpty + (5 * t + i) % kPreSlots]);
+                        tc_mma(tmem + kPreColS + 128 * x, q + ks * 2, k + ks * 2, idesc_qk, i > 0 || ks > 0);
+                    if (last) tc_commit(&bar[kPreEmpty + slot]);
+                    if (i == 2) tc_commit(&bar[kPreSFull + x]);
                 }
-                tc_commit(&bar[kPreSFull + x]);
-                return true;
-            };
-            auto issue_pv = [&](int x, int t) -> bool {
-                if (!mbar_wait_or(&bar[kPrePReady + x], t & 1, abort_flag)) return false;
-                for (int i = 0; i < 2; ++i) {
-                    if (!landed(5 * t + 3 + i)) return false;
-                    tc_fence_after();
-                    const uint32_t va = slab(5 * t + 3 + i);
+                __syncwarp();
+            }
+        };
+        auto issue_pv = [&](int x, int t) {
+            mbar_wait_flow(&bar[kPrePReady + x], t & 1, flag);
+            const bool last = x == 1 || t >= tiles1;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int u = 5 * t + 3 + i, slot = u % kPreSlots;
+                mbar_wait_flow(&bar[kPreFull + slot], (u / kPreSlots) & 1, flag);
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t v = v_desc + slot * (kPreSlab >> 4);
 #pragma unroll
                     for (int ks = 0; ks < kPreKeys / 16; ++ks)
                         tc_mma_ts(tmem + kPreColO + 128 * x + 64 * i, tmem + kPreColS + 128 * x + 8 * ks,
-                                  sw128_desc(va + ks * 2048, kPreSlab, 1024), idesc_pv, t > 0 || ks > 0);
-                    if (last_user(x, t)) tc_commit(&bar[kPreEmpty + (5 * t + 3 + i) % kPreSlots]);
+                                  v + ks * (2048 >> 4), idesc_pv, t > 0 || ks > 0);
+                    if (last) tc_commit(&bar[kPreEmpty + slot]);
+                    if (i == 1 && t + 1 == (x ? tiles1 : tiles0)) tc_commit(&bar[kPreODone + x]);
                 }
-                if (t + 1 == tiles[x]) tc_commit(&bar[kPreODone + x]);
-                return true;
-            };
-            for (int x = 0; x < 2; ++x)
-                if (ok && tiles[x] > 0) ok = issue_qk(x, 0);
-            for (int t = 0; ok && t < most; ++t)
-                for (int x = 0; x < 2; ++x) {
-                    if (ok && t < tiles[x]) ok = issue_pv(x, t);
-                    if (ok && t + 1 < tiles[x]) ok = issue_qk(x, t + 1);
-                }
-            tc_commit(&bar[kPreDrain]);
-            (void)mbar_wait(&bar[kPreDrain], 0);
+                __syncwarp();
+            }
+        };
+        if (tiles0 > 0) issue_qk(0, 0);
+        if (tiles1 > 0) issue_qk(1, 0);
+        for (int t = 0; t < most; ++t) {
+            if (t < tiles0) issue_pv(0, t);
+            if (t + 1 < tiles0) issue_qk(0, t + 1);
+            if (t < tiles1) issue_pv(1, t);
+            if (t + 1 < tiles1) issue_qk(1, t + 1);
         }
+        if (elect_one()) tc_commit(&bar[kPreDrain]);
+        (void)mbar_wait(&bar[kPreDrain], 0);
         __syncwarp();
     } else {
         // ---------------------------------------------------------- softmax / epilogue
-        const int x = (warp - 2) >> 2;
+        const int x = (warp - 2) >> 2, tiles = x ? tiles1 : tiles0;
         const int quad = warp & 3, r = quad * 32 + lane;  // TMEM lane = row of the tile
         const int row = first + x * kPreRows + r;         // query in the sequence
         const uint32_t s_at = tmem + ((uint32_t)(quad * 32) << 16) + kPreColS + 128 * x;
@@ -219,7 +225,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         // normal down to 2^-21 of the largest
         constexpr float kLift = BF16 ? 0.f : 7.f;
         float m_run = -INFINITY, l_run = 0.f;
-        for (int t = 0; ok && t < tiles[x]; ++t) {
+        for (int t = 0; ok && t < tiles; ++t) {
             ok = __all_sync(kFullMask, mbar_wait_or(&bar[kPreSFull + x], t & 1, abort_flag));
             if (!ok) break;
             tc_fence_after();
@@ -275,7 +281,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             }
             l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             tmem_wait_st();
-            if (here + kPreKeys > n_k && (x == 0 || t >= tiles[0])) {
+            if (here + kPreKeys > n_k && (x == 0 || t >= tiles0)) {
                 // rows past the sequence's keys: P is 0 there, and V must be finite.  Tile B's
                 // product follows A's, so the first tile to reach them clears them.
                 for (int i = 0; i < 2; ++i) {
@@ -291,7 +297,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[kPrePReady + x]);
         }
-        if (tiles[x] > 0 && ok)
+        if (tiles > 0 && ok)
             ok = __all_sync(kFullMask, mbar_wait_or(&bar[kPreODone + x], 0, abort_flag));
         if (ok) {
             tc_fence_after();
@@ -303,7 +309,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 float o[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[i] = 0.f;
-                if (tiles[x] > 0) tmem_load16(o_at + 16 * c, o);
+                if (tiles > 0) tmem_load16(o_at + 16 * c, o);
                 if (row < n_q) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[i] = l_run == 0.f ? 0.f : o[i] * inv;
@@ -315,12 +321,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             }
         }
     }
-    if (!ok && lane == 0) {
-        record_error(p.err, PA_ERR_DEVICE_TIMEOUT);
-        *abort_flag = 1;
-    }
+    if (!ok) *abort_flag = 1;
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) record_error(p.err, PA_ERR_DEVICE_TIMEOUT);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);

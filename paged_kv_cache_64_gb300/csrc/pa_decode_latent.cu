@@ -9,17 +9,24 @@
 //   S[heads x 64 pos]    = Q[heads x (RANK + 64)] . K_tile^T        (M=64, N=64)
 //   O^T[128 dims x heads] += V_tile^T[128 x 64 pos] . P^T, RANK/128 times (N=NH)
 //
-// S with the heads on the lanes: a thread owns a head's row, so maxima and sums
-// need no exchange.  O transposed: 128 dims fill the lanes whatever the number of
-// heads, RANK/128 * NH columns hold it, and the staged rows are its A operand as
-// they lie (MN-major).  Two S buffers and O are in TMEM; Q stays in shared memory,
-// the rows pass through rings of 64-column slabs (16 KiB pairs of the latent part,
-// freed after P.V; 8 KiB of the rotary part, freed after q.K).
+// S with the heads on the lanes: a thread owns a head's row.  O transposed: 128
+// dims fill the lanes whatever the number of heads, RANK/128 * NH columns hold it,
+// and the staged rows are its A operand as they lie (MN-major).  Two S buffers and O
+// are in TMEM; Q stays in shared memory, the rows pass through a ring of tiles.
 //
-// Roles (8 warps): 0 producer of rows (TMA boxes of 16 rows through the block
-// table); 1 issues q.K^T (and owns TMEM); 2-5 softmax and epilogue; 6 issues P.V;
-// 7 loads Q.  The running maximum moves only when a tile exceeds it by more than
-// kLazyRescale; then O's columns are rescaled in TMEM.
+// A unit of 16 rows is one TMA copy: the pool seen as [rows / 8][RANK / 64 + 1 slabs]
+// [8 rows][64 columns], a box of two 8-row groups with all their slabs (a copy a unit
+// and slab, 36 a tile, is bound by the issue of copies: 85 clocks each).  So a slab's
+// 8-row groups lie (RANK / 64 + 1) KiB apart, which is the operands' group stride.
+// P.V takes a unit at a time and frees it.
+//
+// Roles (12 warps): 0 producer of rows (TMA boxes of 16 rows through the block
+// table, and prefetches of whole units to L2 some tiles ahead); 1 issues q.K^T (and
+// owns TMEM); 2-9 softmax and epilogue, two warpgroups that share the heads: one
+// takes positions 0-31 of every tile and the first half of O's columns, the other
+// the rest; 10 issues P.V; 11 loads Q.  The running maximum moves only when a tile
+// exceeds it by more than kLazyRescale; then the halves exchange their maxima and
+// O's columns are rescaled in TMEM.
 //
 // The batch's tiles are shared out evenly: range b of the launch is tiles
 // [b per, (b + 1) per) of all sequences' tiles in a row, found from the lengths on
@@ -38,7 +45,9 @@ namespace pa {
 
 constexpr int kLatRope = 64;      // shared key values of a row
 constexpr int kLatTile = 64;      // positions of a tile
-constexpr int kLatWarps = 8;
+constexpr int kLatWarps = 12;
+constexpr int kLatSoftmax = 256;  // softmax threads: two warpgroups
+constexpr int kLatAhead = 4;      // tiles that are on their way to L2
 constexpr int kLatThreads = kLatWarps * 32;
 constexpr int kLatSmem = 232448;  // what a CTA may have
 constexpr int kLatMisc = 2048;    // barriers and exchange
@@ -47,6 +56,7 @@ constexpr int kLatWhole = 8;      // up to so many tiles a sequence is never cut
 
 struct DecodeLatentParams {
     uint16_t *out;
+    const uint16_t *pool;
     const int32_t *tables;
     const int32_t *lens;
     float *part_o;   // [ranges][groups][2][NH][RANK]
@@ -64,37 +74,36 @@ struct LatShape {
     static constexpr int SLABS = RANK / 64 + 1;    // the last one rotary
     static constexpr int PAIRS = RANK / 128;
     static constexpr int Q_SLAB = NH * 128;
-    static constexpr int SLAB = kLatTile * 128;
+    static constexpr int GROUP = SLABS * 1024;     // 8 rows of all slabs
+    static constexpr int UNIT = 2 * GROUP;         // 16 rows
+    static constexpr int TILE = 4 * UNIT;
     static constexpr int P_BYTES = NH * 128;
     static constexpr int P_BUFS = RANK == 512 && NH == 64 ? 1 : 2;
-    static constexpr int ROPE_SLOTS = RANK == 256 ? (NH == 64 ? 4 : 5) : (NH == 64 ? 2 : 3);
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_P = OFF_Q + SLABS * Q_SLAB;
-    static constexpr int OFF_ROPE = OFF_P + P_BUFS * P_BYTES;
-    static constexpr int OFF_PAIR = OFF_ROPE + ROPE_SLOTS * SLAB;
-    static constexpr int PAIR_SLOTS = (kLatSmem - 1024 - kLatMisc - OFF_PAIR) / (2 * SLAB);
-    static constexpr int OFF_MISC = OFF_PAIR + PAIR_SLOTS * 2 * SLAB;
+    static constexpr int OFF_RING = OFF_P + P_BUFS * P_BYTES;
+    static constexpr int STAGES = (kLatSmem - 1024 - kLatMisc - OFF_RING) / TILE;
+    static constexpr int OFF_MISC = OFF_RING + STAGES * TILE;
     static constexpr int SMEM_BYTES = OFF_MISC + kLatMisc + 1024;  // + slack to align the base
     static constexpr int S_COL = PAIRS * NH;       // TMEM: O first, then two S buffers
     // barriers
-    static constexpr int PAIR_FULL = 0, PAIR_EMPTY = PAIR_SLOTS, ROPE_FULL = 2 * PAIR_SLOTS,
-                         ROPE_EMPTY = ROPE_FULL + ROPE_SLOTS, Q_FULL = ROPE_EMPTY + ROPE_SLOTS,
-                         Q_FREE = Q_FULL + 1, S_FULL = Q_FREE + 1, S_FREE = S_FULL + 2,
-                         P_FULL = S_FREE + 2, PV_DONE = P_FULL + 2, O_FREE = PV_DONE + 2,
-                         DRAIN = O_FREE + 1, BARS = DRAIN + 2;
-    // behind the barriers: TMEM address, abort flag, scan scratch, then alphas / sums
+    static constexpr int FULL = 0, EMPTY = STAGES, Q_FULL = EMPTY + 4 * STAGES, Q_FREE = Q_FULL + 1,
+                         S_FULL = Q_FREE + 1, S_FREE = S_FULL + 2, P_FULL = S_FREE + 2,
+                         PV_DONE = P_FULL + 2, O_FREE = PV_DONE + 2, DRAIN = O_FREE + 1,
+                         BARS = DRAIN + 2;
+    // behind the barriers: TMEM address, abort flag, scan scratch, sums; then the heads'
+    // factors and two halves' maxima
     static constexpr int OFF_WORDS = OFF_MISC + 512, OFF_ALPHA = OFF_MISC + 1024;
-    static_assert(BARS * 8 <= 512 && NH * 4 <= 1024, "misc");
-    static_assert(PAIR_SLOTS >= 2 * PAIRS && S_COL + 2 * kLatTile <= 512, "rings, TMEM");
-    static_assert(OFF_P % 1024 == 0 && OFF_PAIR % 1024 == 0 && SMEM_BYTES <= kLatSmem, "layout");
+    static_assert(BARS * 8 <= 512 && 3 * NH * 4 <= 1024, "misc");
+    static_assert(STAGES >= 2 && S_COL + 2 * kLatTile <= 512, "rings, TMEM");
+    static_assert(OFF_P % 1024 == 0 && OFF_RING % 1024 == 0 && SMEM_BYTES <= kLatSmem, "layout");
     // q.K reads 64 rows of A whatever NH: past a slab's own rows it meets other
     // operands, whose products end in lanes that nothing reads
     static_assert(OFF_P - Q_SLAB + 64 * 128 <= OFF_MISC, "A rows in shared memory");
 };
 
 // Length of a sequence, clamped to what the launch and the table cover.
-__device__ __forceinline__ int latent_len(const DecodeLatentParams &p, int seq, bool report) {
-    int L = p.lens[seq];
+__device__ __forceinline__ int latent_len(const DecodeLatentParams &p, int L, bool report) {
     const int cover = p.max_blocks << p.log2_block;
     const int cap = cover < p.max_len ? cover : p.max_len;
     if (L < 0 || L > cap) {
@@ -108,17 +117,20 @@ __device__ __forceinline__ int latent_tiles(int len) {
     return len > 0 ? (len + kLatTile - 1) / kLatTile : 1;
 }
 
-// The pieces of a range, in order: every role walks them by itself.
+// The pieces of a range, in order: every role walks them by itself, the next
+// sequence's length on its way meanwhile.
 struct LatWalk {
     const DecodeLatentParams &p;
     int seq, tile, left;
     int len, n;    // of the current piece: the sequence's length, tiles
     bool more;     // the sequence goes on behind the range
+    int ahead;     // length of the sequence after the current piece's
     __device__ __forceinline__ LatWalk(const DecodeLatentParams &prm, int s, int t, int l)
-        : p(prm), seq(s), tile(t), left(l) {}
+        : p(prm), seq(s), tile(t), left(l), ahead(s < prm.num_seqs ? prm.lens[s] : 0) {}
     __device__ __forceinline__ bool next() {  // the current piece's data, false at the end
         if (left <= 0 || seq >= p.num_seqs) return false;
-        len = latent_len(p, seq, false);
+        len = latent_len(p, ahead, false);
+        if (seq + 1 < p.num_seqs) ahead = p.lens[seq + 1];
         n = latent_tiles(len) - tile;
         more = n > left;
         if (more) n = left;
@@ -131,16 +143,16 @@ struct LatWalk {
     }
 };
 
-// Named barrier 1 over the 128 softmax threads, true on all if any passed true.
-__device__ __forceinline__ bool softmax_bar128_or(bool v) {
+// Named barrier 1 over the softmax threads, true on all if any passed true.
+__device__ __forceinline__ bool latent_bar_or(bool v) {
     int any;
     asm volatile(
         "{\n\t.reg .pred pi, po;\n\t"
         "setp.ne.s32 pi, %1, 0;\n\t"
-        "bar.red.or.pred po, 1, 128, pi;\n\t"
+        "bar.red.or.pred po, 1, %2, pi;\n\t"
         "selp.s32 %0, 1, 0, po;\n\t}"
         : "=r"(any)
-        : "r"((int)v)
+        : "r"((int)v), "n"(kLatSoftmax)
         : "memory");
     return any != 0;
 }
@@ -159,7 +171,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(words);
     int *flag = words + 1;
     volatile int *abort_flag = flag;
-    int *scan = words + 8;  // [8] warp sums, then start sequence and tile
+    int *scan = words + 8;  // [kLatWarps] warp sums, then start sequence and tile
     float *alphas = reinterpret_cast<float *>(smem + S::OFF_ALPHA);
 
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
@@ -168,10 +180,11 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         prefetch_tensormap(&map_rows);
         prefetch_tensormap(&map_q);
         for (int b = 0; b < S::BARS; ++b)
-            mbar_init(&bar[b], (b >= S::S_FREE && b < S::PV_DONE) || b == S::O_FREE ? 4 : 1);
+            mbar_init(&bar[b], (b >= S::S_FREE && b < S::PV_DONE) || b == S::O_FREE
+                                      ? kLatSoftmax / 32 : 1);
         *abort_flag = 0;
-        scan[8] = p.num_seqs;
-        scan[9] = 0;
+        scan[kLatWarps] = p.num_seqs;
+        scan[kLatWarps + 1] = 0;
         mbar_init_fence();
     }
     if (warp == 1) {
@@ -183,13 +196,13 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     // ---------------------------------------------------------- this CTA's range
     int seq0 = range, tile0 = 0, left;
     if (p.whole) {
-        left = latent_tiles(latent_len(p, range, group == 0));
+        left = latent_tiles(latent_len(p, p.lens[range], group == 0));
         tc_fence_before();
         __syncthreads();
     } else {
         int sum = 0;
         for (int i = threadIdx.x; i < p.num_seqs; i += kLatThreads)
-            sum += latent_tiles(latent_len(p, i, blockIdx.x == 0));
+            sum += latent_tiles(latent_len(p, p.lens[i], blockIdx.x == 0));
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
         if (lane == 0) scan[warp] = sum;
@@ -206,7 +219,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         int before = 0;
         for (int base = 0; base < p.num_seqs && left > 0; base += kLatThreads) {
             const int i = base + (int)threadIdx.x;
-            const int mine = i < p.num_seqs ? latent_tiles(latent_len(p, i, false)) : 0;
+            const int mine = i < p.num_seqs ? latent_tiles(latent_len(p, p.lens[i], false)) : 0;
             int incl = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -224,15 +237,15 @@ __global__ void __launch_bounds__(kLatThreads, 1)
             }
             const int first = before + incl - mine;
             if (start >= first && start < first + mine) {
-                scan[8] = i;
-                scan[9] = start - first;
+                scan[kLatWarps] = i;
+                scan[kLatWarps + 1] = start - first;
             }
             before += all;
             if (before > start) break;  // the same for all threads
         }
         __syncthreads();
-        seq0 = scan[8];
-        tile0 = scan[9];
+        seq0 = scan[kLatWarps];
+        tile0 = scan[kLatWarps + 1];
     }
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
@@ -243,153 +256,149 @@ __global__ void __launch_bounds__(kLatThreads, 1)
 
     if (warp == 0) {
         // ---------------------------------------------------------- producer of rows
-        int pair = 0, pair_use = 0, rope = 0, rope_use = 0;
+        // The table's entries of 32 units (8 tiles) are a warp's load, one window ahead
+        // and the next sequence's first window with the current piece's; they are checked
+        // when they come into use.
+        const int log2_block = p.log2_block;
+        auto entry = [&](int seq, int first, int u) -> int {
+            const int64_t at = ((int64_t)first + u * kUnit) >> log2_block;
+            return seq < p.num_seqs && at < p.max_blocks ? p.tables[(int64_t)seq * p.max_blocks + at] : 0;
+        };
+        auto unit_row = [&](int phys, int first, int u, int units) -> int {
+            if (u >= units) return 0;
+            if ((unsigned)phys >= (unsigned)p.num_blocks) {
+                record_error(p.err, PA_ERR_BAD_INDEX);
+                phys = 0;
+            }
+            return (phys << log2_block) + ((first + u * kUnit) & ((1 << log2_block) - 1));
+        };
+        // a unit's rows lie together: one prefetch brings them to L2
+        auto prefetch = [&](int row) {
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                             p.pool + (int64_t)row * (RANK + kLatRope)),
+                         "r"(kUnit * (RANK + kLatRope) * 2)
+                         : "memory");
+        };
+        int st = 0, use = 0;
+        int raw_first = entry(seq0, tile0 * kLatTile, lane);
         for (; ok && walk.next(); walk.advance()) {
-            if (walk.len == 0) continue;
             const int first = walk.tile * kLatTile;
             const int units = (min(walk.len - first, walk.n * kLatTile) + kUnit - 1) / kUnit;
-            const int32_t *table = p.tables + (int64_t)walk.seq * p.max_blocks;
-            auto unit_row = [&](int u) -> int {  // first row of a unit in the pool
-                if (u >= units) return 0;
-                const int pos = first + u * kUnit;
-                int phys = table[pos >> p.log2_block];
-                if ((unsigned)phys >= (unsigned)p.num_blocks) {
-                    record_error(p.err, PA_ERR_BAD_INDEX);
-                    phys = 0;
-                }
-                return (phys << p.log2_block) + (pos & ((1 << p.log2_block) - 1));
-            };
-            int rows_cur = unit_row(lane), rows_next = unit_row(32 + lane);
+            int raw = raw_first;
+            int raw_next = units > 32 ? entry(walk.seq, first, 32 + lane) : 0;
+            raw_first = entry(walk.seq + 1, 0, lane);
+            if (walk.len == 0) continue;
+            int rows_cur = unit_row(raw, first, lane, units), rows_next = 0;
             for (int t = 0; ok && t < walk.n; ++t) {
-                if (t > 0 && (t & 7) == 0) {
-                    rows_cur = rows_next;
-                    rows_next = unit_row(32 * ((t >> 3) + 1) + lane);
+                if (t > 0 && (t & 7) == 0) rows_cur = rows_next;
+                if ((t & 7) == 2 && 4 * (t - 2) + 32 < units) {
+                    const int w = 4 * (t - 2) + 32;  // the next window's first unit
+                    rows_next = unit_row(raw_next, first, w + lane, units);
+                    raw_next = w + 32 < units ? entry(walk.seq, first, w + 32 + lane) : 0;
                 }
                 const int nu = min(units - 4 * t, 4);
-                const int row = __shfl_sync(kFullMask, rows_cur, ((t & 7) * 4 + (lane & 3)) & 31);
-                if (rope_use > 0)
-                    ok = mbar_wait_or(&bar[S::ROPE_EMPTY + rope], (rope_use - 1) & 1, abort_flag);
-                ok = __all_sync(kFullMask, ok);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&bar[S::ROPE_FULL + rope], nu * 2048);
-                __syncwarp();
-                if (lane < nu)
-                    tma_load_2d(smem + S::OFF_ROPE + rope * S::SLAB + lane * 2048, &map_rows, RANK, row,
-                                &bar[S::ROPE_FULL + rope]);
-                if (++rope == S::ROPE_SLOTS) rope = 0, ++rope_use;
+                uint64_t *full = &bar[S::FULL + st];
 #pragma unroll
-                for (int j = 0; j < S::PAIRS; ++j) {
-                    if (ok && pair_use > 0)
-                        ok = mbar_wait_or(&bar[S::PAIR_EMPTY + pair], (pair_use - 1) & 1, abort_flag);
+                for (int u = 0; u < 4; ++u) {
+                    const int row = __shfl_sync(kFullMask, rows_cur, (t & 7) * 4 + u);
+                    if (ok && use > 0)
+                        ok = mbar_wait_or(&bar[S::EMPTY + 4 * st + u], (use - 1) & 1, abort_flag);
                     ok = __all_sync(kFullMask, ok);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&bar[S::PAIR_FULL + pair], nu * 4096);
+                    if (ok && u < nu && elect_one()) {
+                        if (u == 0) mbar_arrive_expect_tx(full, nu * S::UNIT);
+                        tma_load_4d(smem + S::OFF_RING + st * S::TILE + u * S::UNIT, &map_rows, 0, 0, 0,
+                                    row >> 3, full);
+                    }
                     __syncwarp();
-                    if (lane < 8 && (lane & 3) < nu)
-                        tma_load_2d(smem + S::OFF_PAIR + pair * 2 * S::SLAB + (lane >> 2) * S::SLAB +
-                                        (lane & 3) * 2048,
-                                    &map_rows, 128 * j + 64 * (lane >> 2), row, &bar[S::PAIR_FULL + pair]);
-                    if (++pair == S::PAIR_SLOTS) pair = 0, ++pair_use;
                 }
+                if (!ok) break;
+                if (++st == S::STAGES) st = 0, ++use;
+                // tile t + kLatAhead's units; with the first tile also those before it
+                const int back = t == 0 ? kLatAhead - 2 : 0;
+                const int ahead = t + kLatAhead - back + (lane >> 2);  // lane's tile
+                const int u = 4 * ahead + (lane & 3);
+                const bool same = (ahead >> 3) == (t >> 3);
+                const int r_cur = __shfl_sync(kFullMask, rows_cur, (4 * ahead + (lane & 3)) & 31);
+                const int r_next = __shfl_sync(kFullMask, rows_next, (4 * ahead + (lane & 3)) & 31);
+                if ((lane >> 2) <= back && u < units) prefetch(same ? r_cur : r_next);
             }
         }
-        // every copy has landed before shared memory goes (a slot's last use)
-        for (int i = 0; i < S::PAIR_SLOTS; ++i) {
-            const int uses = pair_use + (i < pair);
-            if (uses > 0) (void)mbar_wait(&bar[S::PAIR_FULL + i], (uses - 1) & 1);
-        }
-        for (int i = 0; i < S::ROPE_SLOTS; ++i) {
-            const int uses = rope_use + (i < rope);
-            if (uses > 0) (void)mbar_wait(&bar[S::ROPE_FULL + i], (uses - 1) & 1);
+        // every copy has landed before shared memory goes (a stage's last use)
+        for (int i = 0; i < S::STAGES; ++i) {
+            const int uses = use + (i < st);
+            if (uses > 0) (void)mbar_wait(&bar[S::FULL + i], (uses - 1) & 1);
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------- q.K^T
         constexpr uint32_t idesc = f16_idesc(BF16, false, false, 64, kLatTile);
         const uint32_t base = smem_addr(smem);
         const uint64_t q_desc = sw128_desc(base + S::OFF_Q, 16, 1024);
-        const uint64_t pair_desc = sw128_desc(base + S::OFF_PAIR, 16, 1024);
-        const uint64_t rope_desc = sw128_desc(base + S::OFF_ROPE, 16, 1024);
-        int pair = 0, pair_use = 0, rope = 0, rope_use = 0, g = 0, piece = 0;
+        const uint64_t k_desc = sw128_desc(base + S::OFF_RING, 16, S::GROUP);
+        int st = 0, use = 0, g = 0, piece = 0;
         for (; walk.next(); walk.advance()) {
             if (walk.len == 0) continue;
             mbar_wait_flow(&bar[S::Q_FULL], piece & 1, flag);
             for (int t = 0; t < walk.n; ++t, ++g) {
                 const int b = g & 1;
                 if (g >= 2) mbar_wait_flow(&bar[S::S_FREE + b], ((g >> 1) - 1) & 1, flag);
-                mbar_wait_flow(&bar[S::ROPE_FULL + rope], rope_use & 1, flag);
+                mbar_wait_flow(&bar[S::FULL + st], use & 1, flag);
                 tc_fence_after();
-                const uint32_t d = tmem + S::S_COL + kLatTile * b;
                 if (elect_one()) {
-                    const uint64_t k = rope_desc + rope * (S::SLAB >> 4);
+                    const uint64_t k = k_desc + st * (S::TILE >> 4);
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        tc_mma(d, q_desc + (((S::SLABS - 1) * S::Q_SLAB + ks * 32) >> 4), k + ks * 2,
-                               idesc, ks > 0);
-                    tc_commit(&bar[S::ROPE_EMPTY + rope]);
+                    for (int i = 0; i < S::SLABS; ++i)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            tc_mma(tmem + S::S_COL + kLatTile * b, q_desc + ((i * S::Q_SLAB + ks * 32) >> 4),
+                                   k + ((i * 1024 + ks * 32) >> 4), idesc, i > 0 || ks > 0);
+                    if (t + 1 == walk.n) tc_commit(&bar[S::Q_FREE]);
+                    tc_commit(&bar[S::S_FULL + b]);
                 }
                 __syncwarp();
-                if (++rope == S::ROPE_SLOTS) rope = 0, ++rope_use;
-#pragma unroll
-                for (int j = 0; j < S::PAIRS; ++j) {
-                    mbar_wait_flow(&bar[S::PAIR_FULL + pair], pair_use & 1, flag);
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t k = pair_desc + pair * (2 * S::SLAB >> 4);
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            tc_mma(d,
-                                   q_desc + (((2 * j + (ks >> 2)) * S::Q_SLAB + (ks & 3) * 32) >> 4),
-                                   k + (((ks >> 2) * S::SLAB + (ks & 3) * 32) >> 4), idesc, 1);
-                        if (j + 1 == S::PAIRS) {
-                            if (t + 1 == walk.n) tc_commit(&bar[S::Q_FREE]);
-                            tc_commit(&bar[S::S_FULL + b]);
-                        }
-                    }
-                    __syncwarp();
-                    if (++pair == S::PAIR_SLOTS) pair = 0, ++pair_use;
-                }
+                if (++st == S::STAGES) st = 0, ++use;
             }
             ++piece;
         }
         if (elect_one()) tc_commit(&bar[S::DRAIN]);
         (void)mbar_wait(&bar[S::DRAIN], 0);
         __syncwarp();
-    } else if (warp == 6) {
+    } else if (warp == 10) {
         // ---------------------------------------------------------- P.V
         constexpr uint32_t idesc = f16_idesc(BF16, true, false, 128, NH);
         const uint32_t base = smem_addr(smem);
         const uint64_t p_desc = sw128_desc(base + S::OFF_P, 16, 1024);
-        const uint64_t pair_desc = sw128_desc(base + S::OFF_PAIR, S::SLAB, 1024);
-        int pair = 0, pair_use = 0, g = 0, piece = 0;
+        const uint64_t v_desc = sw128_desc(base + S::OFF_RING, 1024, S::GROUP);
+        int st = 0, use = 0, g = 0, piece = 0;
         for (; walk.next(); walk.advance()) {
             if (walk.len == 0) continue;
             if (piece > 0) mbar_wait_flow(&bar[S::O_FREE], (piece - 1) & 1, flag);
             for (int t = 0; t < walk.n; ++t, ++g) {
                 const int pb = g % S::P_BUFS;
                 mbar_wait_flow(&bar[S::P_FULL + pb], (g / S::P_BUFS) & 1, flag);
-                const uint64_t w = p_desc + pb * (S::P_BYTES >> 4);
+                mbar_wait_flow(&bar[S::FULL + st], use & 1, flag);
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t w = p_desc + pb * (S::P_BYTES >> 4);
+                    const uint64_t v = v_desc + st * (S::TILE >> 4);
 #pragma unroll
-                for (int j = 0; j < S::PAIRS; ++j) {
-                    mbar_wait_flow(&bar[S::PAIR_FULL + pair], pair_use & 1, flag);
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t v = pair_desc + pair * (2 * S::SLAB >> 4);
+                    for (int u = 0; u < 4; ++u) {
 #pragma unroll
-                        for (int ks = 0; ks < kLatTile / 16; ++ks)
-                            tc_mma(tmem + j * NH, v + ks * (2048 >> 4), w + ks * 2, idesc, t > 0 || ks > 0);
-                        tc_commit(&bar[S::PAIR_EMPTY + pair]);
-                        if (j + 1 == S::PAIRS) tc_commit(&bar[S::PV_DONE + pb]);
+                        for (int j = 0; j < S::PAIRS; ++j)
+                            tc_mma(tmem + j * NH, v + ((u * S::UNIT + j * 2048) >> 4), w + u * 2, idesc,
+                                   t > 0 || u > 0);
+                        tc_commit(&bar[S::EMPTY + 4 * st + u]);
                     }
-                    __syncwarp();
-                    if (++pair == S::PAIR_SLOTS) pair = 0, ++pair_use;
+                    tc_commit(&bar[S::PV_DONE + pb]);
                 }
+                __syncwarp();
+                if (++st == S::STAGES) st = 0, ++use;
             }
             ++piece;
         }
         if (elect_one()) tc_commit(&bar[S::DRAIN + 1]);
         (void)mbar_wait(&bar[S::DRAIN + 1], 0);
         __syncwarp();
-    } else if (warp == 7) {
+    } else if (warp == 11) {
         // ---------------------------------------------------------- Q
         if (lane == 0) {
             int piece = 0;
@@ -409,15 +418,21 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         __syncwarp();
     } else {
         // ---------------------------------------------------------- softmax / epilogue
+        const int half = (warp - 2) >> 2;
         const int quad = warp & 3;                 // TMEM lanes this warp may access
         const int row = quad * 16 + lane;          // head of lanes 0-15 (M = 64: 16 lanes a quadrant)
+        const int tid = threadIdx.x - 64;
         const int heads = min(NH, p.num_heads - group * NH);
         const bool mine = lane < 16 && row < heads;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        float *maxima = alphas + NH;               // [half][NH]
+        float *sums = reinterpret_cast<float *>(words + 64);  // the second half's, at a piece's end
+        constexpr int kPos = kLatTile / 2;         // positions of a half
+        constexpr int kCols = S::PAIRS * NH / 2;   // O columns of a half
         // f16 weights as 2^7 of themselves: at most 2^15 with the lag of the maximum, and
         // normal down to 2^-21 of the largest
         constexpr float kLift = BF16 ? 0.f : 7.f;
-        int g = 0, pair0 = 0;
+        int g = 0;
         int4 plan = make_int4(-1, 0, 0, 0);
         // P.V of tile k (counted over all pieces) is done.  One barrier a P buffer, whose
         // phases are waited for in turn: a tile's is, at the latest, before P goes into
@@ -429,7 +444,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
             const int64_t out_row = (int64_t)walk.seq * p.num_heads + group * NH;
             const int dim = quad * 32 + lane;
             if (walk.len == 0) {
-                for (int h = 0; h < heads; ++h)
+                for (int h = half; h < heads; h += 2)
 #pragma unroll
                     for (int j = 0; j < S::PAIRS; ++j) p.out[(out_row + h) * RANK + 128 * j + dim] = 0;
                 continue;
@@ -439,112 +454,114 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                 const int b = g & 1;
                 bool fine = mbar_wait_or(&bar[S::S_FULL + b], (g >> 1) & 1, abort_flag);
                 fine = __all_sync(kFullMask, fine);
-                float s[kLatTile];
-                if (fine) {
-                    tc_fence_after();
-                    tmem_ld32(tmem + lanes + S::S_COL + kLatTile * b, s);
-                    tmem_ld32(tmem + lanes + S::S_COL + kLatTile * b + 32, s + 32);
-                    tc_fence_before();
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kLatTile; ++j) s[j] = 0.f;
-                }
+                tc_fence_after();
+                float s[kPos];
+                tmem_ld32(tmem + lanes + S::S_COL + kLatTile * b + kPos * half, s);
+                tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[S::S_FREE + b]);
                 const int valid = min(walk.len - (walk.tile + t) * kLatTile, kLatTile);
-                float mx = -INFINITY;
+                if (valid == kLatTile) {
 #pragma unroll
-                for (int j = 0; j < kLatTile; ++j) {
-                    s[j] = j < valid ? s[j] * p.scale_log2 : -INFINITY;  // NaN-safe select
-                    mx = fmaxf(mx, s[j]);
-                }
-                float alpha = 1.f;
-                bool need = mx > m_run + kLazyRescale;
-                if (need) {
-                    alpha = fast_exp2(m_run - mx);  // 0 from an empty maximum
-                    m_run = mx;
-                    l_run *= alpha;
-                }
-                need = need && mine && t > 0;
-                if (mine) alphas[row] = alpha;
-                const float from = (m_run == -INFINITY ? 0.f : m_run) - kLift;
-                uint32_t w[kLatTile / 2];
+                    for (int j = 0; j < kPos; ++j) s[j] *= p.scale_log2;
+                } else {
 #pragma unroll
-                for (int j = 0; j < kLatTile / 2; ++j) {
-                    const float a = fast_exp2(s[2 * j] - from), c = fast_exp2(s[2 * j + 1] - from);
-                    l_run += a + c;
-                    w[j] = narrow2<BF16>(a, c);
+                    for (int j = 0; j < kPos; ++j)  // NaN-safe select
+                        s[j] = kPos * half + j < valid ? s[j] * p.scale_log2 : -INFINITY;
                 }
-                const bool any = softmax_bar128_or(need || !fine);
-                // P's buffer is free, and O at rest where it is rescaled
-                if (g >= S::P_BUFS) fine = fine && pv_done(g - S::P_BUFS);
-                if (any && g > 0) fine = fine && pv_done(g - 1);
-                if (valid < kLatTile) {
-                    // rows past the length: P is 0 there, and V must be finite
-                    int pair = pair0;
-                    for (int j = 0; j < S::PAIRS; ++j) {
-                        fine = fine && mbar_wait_or(&bar[S::PAIR_FULL + pair],
-                                                ((g * S::PAIRS + j) / S::PAIR_SLOTS) & 1, abort_flag);
-                        uint8_t *slab = smem + S::OFF_PAIR + pair * 2 * S::SLAB;
-                        for (int i = valid * 8 + quad * 32 + lane; i < kLatTile * 8; i += 128) {
-                            reinterpret_cast<uint4 *>(slab)[i] = make_uint4(0, 0, 0, 0);
-                            reinterpret_cast<uint4 *>(slab + S::SLAB)[i] = make_uint4(0, 0, 0, 0);
-                        }
-                        if (++pair == S::PAIR_SLOTS) pair = 0;
-                    }
-                }
-                fine = __all_sync(kFullMask, fine);
+                float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int j = 4; j < kPos; ++j) top[j & 3] = fmaxf(top[j & 3], s[j]);
+                float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                // the first tile sets the maximum; later ones move it where a half asks for it
+                bool any = true;
+                if (t > 0) any = latent_bar_or((mine && mx > m_run + kLazyRescale) || !fine);
                 if (any) {
-                    // rescale O, or end together
-                    if (softmax_bar128_or(!fine)) {
+                    if (mine) maxima[half * NH + row] = mx;
+                    if (latent_bar_or(!fine)) {  // all end together
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < S::PAIRS * NH; c += 16) {
-                        float o[16];
-                        tmem_load16(tmem + lanes + c, o);
-                        const float4 *a = reinterpret_cast<const float4 *>(alphas + c % NH);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float4 f = a[i];
-                            o[4 * i] *= f.x, o[4 * i + 1] *= f.y, o[4 * i + 2] *= f.z, o[4 * i + 3] *= f.w;
-                        }
-                        tmem_store16(tmem + lanes + c, o);
+                    if (mine) mx = fmaxf(mx, maxima[(1 - half) * NH + row]);
+                    float alpha = 1.f;
+                    if (mx > m_run + kLazyRescale) {
+                        alpha = fast_exp2(m_run - mx);  // 0 from an empty maximum
+                        m_run = mx;
+                        l_run *= alpha;
                     }
-                    tmem_wait_st();
-                    softmax_bar128_or(false);  // the alphas are free again
-                } else if (!fine) {
-                    *abort_flag = 1;
+                    if (t > 0) {
+                        if (mine && half == 0) alphas[row] = alpha;
+                        fine = pv_done(g - 1);  // O at rest
+                        if (latent_bar_or(!fine)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = kCols * half; c < kCols * (half + 1); c += 16) {
+                            float o[16];
+                            tmem_load16(tmem + lanes + c, o);
+                            const float4 *a = reinterpret_cast<const float4 *>(alphas + c % NH);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float4 f = a[i];
+                                o[4 * i] *= f.x, o[4 * i + 1] *= f.y;
+                                o[4 * i + 2] *= f.z, o[4 * i + 3] *= f.w;
+                            }
+                            tmem_store16(tmem + lanes + c, o);
+                        }
+                        tmem_wait_st();
+                    }
                 }
+                const float from = (m_run == -INFINITY ? 0.f : m_run) - kLift;
+                uint32_t w[kPos / 2];
+                float sum[4] = {};
+#pragma unroll
+                for (int j = 0; j < kPos / 2; ++j) {
+                    const float a = fast_exp2(s[2 * j] - from), c = fast_exp2(s[2 * j + 1] - from);
+                    sum[j & 3] += a + c;
+                    w[j] = narrow2<BF16>(a, c);
+                }
+                l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                if (g >= S::P_BUFS) fine = fine && pv_done(g - S::P_BUFS);  // P's buffer is free
+                if (valid < kLatTile) {
+                    // rows past the length: P is 0 there, and V must be finite
+                    fine = fine && mbar_wait_or(&bar[S::FULL + g % S::STAGES], (g / S::STAGES) & 1, abort_flag);
+                    uint8_t *tile = smem + S::OFF_RING + (g % S::STAGES) * S::TILE;
+                    for (int i = tid; i < (kLatTile - valid) * (RANK / 8); i += kLatSoftmax) {
+                        const int r = valid + i / (RANK / 8), c = i % (RANK / 8);
+                        *reinterpret_cast<uint4 *>(tile + (r >> 3) * S::GROUP + (c >> 3) * 1024 +
+                                                   (r & 7) * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                if (!fine) *abort_flag = 1;  // the next wait for S ends all
                 if (mine) {
                     uint8_t *to = smem + S::OFF_P + (g % S::P_BUFS) * S::P_BYTES + (row >> 3) * 1024 +
                                   (row & 7) * 128;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<uint4 *>(to + ((j ^ (row & 7)) << 4)) =
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<uint4 *>(to + (((4 * half + j) ^ (row & 7)) << 4)) =
                             make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
                 }
                 fence_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[S::P_FULL + g % S::P_BUFS]);
-                pair0 = (pair0 + S::PAIRS) % S::PAIR_SLOTS;
             }
             if (!ok) break;
-            const bool fine = pv_done(g - 1);
-            if (softmax_bar128_or(!fine)) {
+            if (mine && half == 1) sums[row] = l_run;
+            if (latent_bar_or(!pv_done(g - 1))) {
                 ok = false;
                 break;
             }
+            if (mine && half == 0) l_run += sums[row];
             tc_fence_after();
             const bool whole = walk.tile == 0 && !walk.more;
             if (whole) {
-                if (mine) alphas[row] = l_run > 0.f ? 1.f / l_run : l_run == 0.f ? 0.f : l_run;
-                softmax_bar128_or(false);
+                if (mine && half == 0) alphas[row] = l_run > 0.f ? 1.f / l_run : l_run == 0.f ? 0.f : l_run;
+                latent_bar_or(false);
 #pragma unroll 1
-                for (int c = 0; c < S::PAIRS * NH; c += 16) {
+                for (int c = kCols * half; c < kCols * (half + 1); c += 16) {
                     float o[16];
                     tmem_load16(tmem + lanes + c, o);
                     const int h0 = c % NH, j = c / NH;
@@ -560,13 +577,13 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                     const int rest = latent_tiles(walk.len) - walk.n;
                     plan = make_int4(walk.seq, cut, rest, 0);
                 }
-                if (mine) {
+                if (mine && half == 0) {
                     p.part_ml[(slot * NH + row) * 2] = m_run;
                     p.part_ml[(slot * NH + row) * 2 + 1] = l_run;
                 }
                 float *part = p.part_o + slot * NH * RANK + dim;
 #pragma unroll 1
-                for (int c = 0; c < S::PAIRS * NH; c += 16) {
+                for (int c = kCols * half; c < kCols * (half + 1); c += 16) {
                     float o[16];
                     tmem_load16(tmem + lanes + c, o);
                     const int h0 = c % NH, j = c / NH;
@@ -576,7 +593,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                 }
             }
             tc_fence_before();
-            softmax_bar128_or(false);  // O and the alphas have been read
+            latent_bar_or(false);  // O, the factors and the sums have been read
             if (lane == 0) mbar_arrive(&bar[S::O_FREE]);
         }
         if (!p.whole && group == 0 && threadIdx.x == 64) {
@@ -740,6 +757,7 @@ extern "C" pa_status pa_decode_latent(void *out, const void *q, const void *pool
     p.err = error_word();
     if (!p.err) return PA_ERR_CUDA;
     p.out = static_cast<uint16_t *>(out);
+    p.pool = static_cast<const uint16_t *>(pool);
     p.tables = block_tables;
     p.lens = seq_lens;
     if (!c.whole) {
@@ -763,10 +781,12 @@ extern "C" pa_status pa_decode_latent(void *out, const void *q, const void *pool
                                         : (bf16 ? latent_kernels<true, 256>(c.nh) : latent_kernels<false, 256>(c.nh));
     CUtensorMap map_rows, map_q;
     const int64_t row = rank + kLatRope;
-    const int64_t dims[2] = {row, (int64_t)num_blocks * block_size}, step[1] = {row};
-    const int64_t qdims[2] = {row, (int64_t)num_seqs * num_heads};
-    if (!rows_tensor_map(&map_rows, pool, 2, dims, step, kUnit, bf16) ||
-        !rows_tensor_map(&map_q, q, 2, qdims, step, c.nh, bf16) ||
+    const int64_t qdims[2] = {row, (int64_t)num_seqs * num_heads}, step[1] = {row};
+    const int64_t dims[4] = {64, 8, row / 64, (int64_t)num_blocks * block_size / 8};
+    const int64_t steps[3] = {row, 64, 8 * row};
+    const int box[4] = {64, 8, (int)(row / 64), kUnit / 8}, qbox[2] = {64, c.nh};
+    if (!boxed_tensor_map(&map_rows, pool, 4, dims, steps, box, bf16) ||
+        !boxed_tensor_map(&map_q, q, 2, qdims, step, qbox, bf16) ||
         !ensure_smem_attr(reinterpret_cast<const void *>(k.decode), k.smem))
         return PA_ERR_CUDA;
     if (launch_pdl(k.decode, dim3((unsigned)(c.ranges * c.groups)), dim3(kLatThreads), (size_t)k.smem,

@@ -61,16 +61,20 @@ bool pool_tensor_map_fp8(CUtensorMap *map, const void *pool, int64_t rows, int D
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool rows_tensor_map(CUtensorMap *map, const void *base, int rank, const int64_t *dims,
-                     const int64_t *steps, int box_rows, bool bf16) {
+bool boxed_tensor_map(CUtensorMap *map, const void *base, int rank, const int64_t *dims,
+                      const int64_t *steps, const int *box, bool bf16) {
     EncodeTiledFn enc = tensor_map_encoder();
-    if (!enc) return false;
-    cuuint64_t extent[3], stride[2];
-    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
-    for (int i = 0; i < rank; ++i) extent[i] = (cuuint64_t)dims[i];
+    if (!enc || rank < 2 || rank > 4) return false;
+    cuuint64_t extent[4], stride[3];
+    cuuint32_t boxes[4], estr[4];
+    for (int i = 0; i < rank; ++i) {
+        extent[i] = (cuuint64_t)dims[i];
+        boxes[i] = (cuuint32_t)box[i];
+        estr[i] = 1;
+    }
     for (int i = 0; i + 1 < rank; ++i) stride[i] = (cuuint64_t)steps[i] * 2;
     return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-               (cuuint32_t)rank, const_cast<void *>(base), extent, stride, box, estr,
+               (cuuint32_t)rank, const_cast<void *>(base), extent, stride, boxes, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

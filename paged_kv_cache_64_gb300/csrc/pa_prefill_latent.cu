@@ -370,9 +370,10 @@ extern "C" pa_status pa_prefill_latent(
     const bool bf16 = dtype == PA_BF16;
     // without keys no map of theirs is used: q stands in
     const bool keys = total_k > 0;
+    const int box[3] = {64, kPreKeys, 1};
     auto map3 = [&](CUtensorMap *map, const void *base, int width, int tokens, int64_t token, int64_t head) {
         const int64_t dims[3] = {width, tokens, num_heads}, step[2] = {token, head};
-        return rows_tensor_map(map, base, 3, dims, step, kPreKeys, bf16);
+        return boxed_tensor_map(map, base, 3, dims, step, box, bf16);
     };
     CUtensorMap map_q, map_k, map_v, map_pe;
     const int64_t pe_dims[2] = {kPreRope, keys ? total_k : total_q}, pe_step[1] = {keys ? k_pe_stride : q_token_stride};
@@ -381,7 +382,7 @@ extern "C" pa_status pa_prefill_latent(
                      map3(&map_v, v, kPreValue, total_k, v_token_stride, v_head_stride)
                : map3(&map_k, q, kPreNope, total_q, q_token_stride, q_head_stride) &&
                      map3(&map_v, q, kPreValue, total_q, q_token_stride, q_head_stride)) ||
-        !rows_tensor_map(&map_pe, keys ? k_pe : q, 2, pe_dims, pe_step, kPreKeys, bf16))
+        !boxed_tensor_map(&map_pe, keys ? k_pe : q, 2, pe_dims, pe_step, box, bf16))
         return PA_ERR_CUDA;
     auto kern = bf16 ? prefill_latent_kernel<true> : prefill_latent_kernel<false>;
     if (!ensure_smem_attr(reinterpret_cast<const void *>(kern), kPreSmem)) return PA_ERR_CUDA;

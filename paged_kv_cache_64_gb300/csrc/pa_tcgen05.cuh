@@ -104,6 +104,14 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
         : "memory");
 }
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int x, int y, int z,
+                                            int w, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+        : "memory");
+}
 // Bring a tensor-map descriptor (a __grid_constant__ kernel parameter) into
 // the TMA unit's cache before its first copy.
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap *map) {
@@ -265,10 +273,10 @@ bool pool_tensor_map(CUtensorMap *map, const void *pool, int64_t rows, int D, bo
 // (row-major) or with the swizzle of a K-major operand of d-byte rows
 // (128-byte swizzle for d = 128, 64-byte for d = 64).
 bool pool_tensor_map_fp8(CUtensorMap *map, const void *pool, int64_t rows, int D, bool swizzle);
-// A tensor of 16-bit elements with `rank` (2 or 3) dimensions, the first dense,
-// steps in elements of the others; boxes of 64 x box_rows (x 1) elements, 128-byte
-// swizzle; elements past the extents read as zero.
-bool rows_tensor_map(CUtensorMap *map, const void *base, int rank, const int64_t *dims,
-                     const int64_t *steps, int box_rows, bool bf16);
+// A tensor of 16-bit elements with `rank` (2 to 4) dimensions, the first dense,
+// steps in elements of the others; 128-byte swizzle (boxes 64 elements wide);
+// elements past the extents read as zero.
+bool boxed_tensor_map(CUtensorMap *map, const void *base, int rank, const int64_t *dims,
+                      const int64_t *steps, const int *box, bool bf16);
 
 }  // namespace pa

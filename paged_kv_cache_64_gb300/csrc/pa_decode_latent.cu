@@ -613,62 +613,116 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     }
 }
 
-// Joins the pieces of the sequences that ranges cut: block (range, head) the
-// sequence that begins in the range and goes on.
+// Joins the pieces of the sequences that ranges cut:
 //   M = max m_i;  out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i
-constexpr int kLatJoinThreads = 512;
+// A unit of work is a head of such a sequence, or a part of its values; a warp takes
+// whole units, or some warps of a block share one's pieces, as there are many units
+// or few: one wave of blocks, each of which lists the cut sequences for itself.
+// (A block a range and head instead, most of them with nothing to join, took longer
+// than the joining: 128 sequences of 513 to 8,192 positions and 128 heads 227 us a
+// call, 198 with this.)
+constexpr int kLatJoinWarps = 8, kLatJoinThreads = kLatJoinWarps * 32;
+constexpr int kLatMaxRanges = kLatJoinThreads;
 
 template <bool BF16, int RANK, int NH>
 __global__ void __launch_bounds__(kLatJoinThreads) latent_join_kernel(
     const __grid_constant__ DecodeLatentParams p) {
-    constexpr int D4 = RANK / 4, PARTS = kLatJoinThreads / D4;
-    __shared__ float weight[1024];
-    __shared__ float4 sums[PARTS][D4];
+    constexpr int CHUNKS = RANK / 128;  // float4 a lane for all of a head's values
+    __shared__ int4 plans[kLatMaxRanges];  // sequence, cut, further pieces, range
+    __shared__ int counts[kLatJoinWarps], most[kLatJoinWarps];
+    __shared__ float weights[kLatJoinWarps][kLatMaxRanges];
+    __shared__ float4 sums[kLatJoinWarps][CHUNKS][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
-    const int range = blockIdx.x, h = blockIdx.y, group = h / NH, row = h % NH;
-    const int4 plan = p.plan[range];
-    if (plan.x < 0) return;
-    const int n = plan.z + 1;
-    auto slot_of = [&](int i) -> int64_t {
-        return ((int64_t)(range + i) * p.groups + group) * 2 + (i == 0 ? plan.y : 0);
-    };
-    if (threadIdx.x < 32) {
-        float M = -INFINITY;
-        for (int i = threadIdx.x; i < n; i += 32)
-            M = fmaxf(M, p.part_ml[(slot_of(i) * NH + row) * 2]);
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
-        float total = 0.f;
-        for (int i = threadIdx.x; i < n; i += 32) {
-            const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + (slot_of(i) * NH + row) * 2);
-            const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
-            weight[i] = w;
-            total += w * ml.y;
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(kFullMask, total, o);
-        const float inv = total > 0.f ? 1.f / total : total == 0.f ? 0.f : total;
-        for (int i = threadIdx.x; i < n; i += 32) weight[i] *= inv;
+    int4 plan = make_int4(-1, 0, 0, 0);
+    if (threadIdx.x < p.ranges) plan = p.plan[threadIdx.x];
+    plan.w = threadIdx.x;
+    const unsigned live = __ballot_sync(kFullMask, plan.x >= 0);
+    const int deep = __reduce_max_sync(kFullMask, plan.x >= 0 ? plan.z + 1 : 0);
+    if (lane == 0) {
+        counts[warp] = __popc(live);
+        most[warp] = deep;
     }
     __syncthreads();
-    const int d = threadIdx.x % D4, part = threadIdx.x / D4;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    int at = 0, cut = 0, pieces = 0;
+#pragma unroll
+    for (int w = 0; w < kLatJoinWarps; ++w) {
+        if (w < warp) at += counts[w];
+        cut += counts[w];
+        pieces = max(pieces, most[w]);
+    }
+    if (plan.x >= 0) plans[at + __popc(live & ((1u << lane) - 1))] = plan;
+    __syncthreads();
+    const int items = cut * p.num_heads, warps = gridDim.x * kLatJoinWarps;
+    int split = 1, share = 1;  // parts of a head's values, warps a unit
+    while (split < CHUNKS && items * split * 2 <= warps) split *= 2;
+    while (share < kLatJoinWarps && share * 2 <= pieces && items * split * share * 2 <= warps) share *= 2;
+    const int own = CHUNKS / split, units = items * split, per = kLatJoinWarps / share;
+    const int part = warp % share;
+    for (int base = blockIdx.x * per; base < units; base += gridDim.x * per) {
+        const int unit = base + warp / share;
+        float4 acc[CHUNKS];
+#pragma unroll
+        for (int k = 0; k < CHUNKS; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int item = unit / split, first = (unit % split) * own;
+        const int h = item % p.num_heads, group = h / NH, row = h % NH;
+        if (unit < units) {
+            plan = plans[item / p.num_heads];
+            const int n = plan.z + 1;
+            auto slot_of = [&](int i) -> int64_t {
+                return ((int64_t)(plan.w + i) * p.groups + group) * 2 + (i == 0 ? plan.y : 0);
+            };
+            float M = -INFINITY, total = 0.f;
+            for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_ml[(slot_of(i) * NH + row) * 2]);
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
+            for (int i = lane; i < n; i += 32) {
+                const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + (slot_of(i) * NH + row) * 2);
+                const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
+                weights[warp][i] = w;
+                total += w * ml.y;
+            }
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(kFullMask, total, o);
+            const float inv = total > 0.f ? 1.f / total : total == 0.f ? 0.f : total;
+            __syncwarp();
 #pragma unroll 4
-    for (int i = part; i < n; i += PARTS) {
-        const float4 v = reinterpret_cast<const float4 *>(p.part_o + (slot_of(i) * NH + row) * RANK)[d];
-        const float w = weight[i];
-        acc.x += w * v.x, acc.y += w * v.y, acc.z += w * v.z, acc.w += w * v.w;
-    }
-    sums[part][d] = acc;
-    __syncthreads();
-    if (part == 0) {
+            for (int i = part; i < n; i += share) {
+                const float4 *from = reinterpret_cast<const float4 *>(p.part_o + (slot_of(i) * NH + row) * RANK) +
+                                     32 * first + lane;
+                const float w = weights[warp][i] * inv;
 #pragma unroll
-        for (int k = 1; k < PARTS; ++k) {
-            const float4 v = sums[k][d];
-            acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+                for (int k = 0; k < CHUNKS; ++k)
+                    if (k < own) {
+                        const float4 v = from[32 * k];
+                        acc[k].x += w * v.x, acc[k].y += w * v.y;
+                        acc[k].z += w * v.z, acc[k].w += w * v.w;
+                    }
+            }
         }
-        reinterpret_cast<uint2 *>(p.out + ((int64_t)plan.x * p.num_heads + h) * RANK)[d] =
-            make_uint2(narrow2<BF16>(acc.x, acc.y), narrow2<BF16>(acc.z, acc.w));
+        if (share > 1) {
+#pragma unroll
+            for (int k = 0; k < CHUNKS; ++k) sums[warp][k][lane] = acc[k];
+            __syncthreads();
+            if (part == 0) {
+                for (int w = 1; w < share; ++w)
+#pragma unroll
+                    for (int k = 0; k < CHUNKS; ++k) {
+                        const float4 v = sums[warp + w][k][lane];
+                        acc[k].x += v.x, acc[k].y += v.y, acc[k].z += v.z, acc[k].w += v.w;
+                    }
+            }
+            __syncthreads();
+        }
+        if (part == 0 && unit < units) {
+            uint2 *to = reinterpret_cast<uint2 *>(p.out + ((int64_t)plan.x * p.num_heads + h) * RANK) +
+                        32 * first + lane;
+#pragma unroll
+            for (int k = 0; k < CHUNKS; ++k)
+                if (k < own)
+                    to[32 * k] = make_uint2(narrow2<BF16>(acc[k].x, acc[k].y), narrow2<BF16>(acc[k].z, acc[k].w));
+        }
+        __syncwarp();
     }
 }
 
@@ -684,6 +738,7 @@ static LatentLaunch latent_launch(int num_seqs, int num_heads, int rank, int max
     c.nh = num_heads <= 16 ? 16 : num_heads <= 32 ? 32 : 64;
     c.groups = (num_heads + c.nh - 1) / c.nh;
     c.ranges = sms / c.groups > 0 ? sms / c.groups : 1;
+    if (c.ranges > kLatMaxRanges) c.ranges = kLatMaxRanges;
     const int tiles = (max_seq_len + kLatTile - 1) / kLatTile;
     c.whole = num_seqs <= c.ranges && tiles <= kLatWhole;
     if (c.whole) c.ranges = num_seqs;
@@ -793,7 +848,7 @@ extern "C" pa_status pa_decode_latent(void *out, const void *q, const void *pool
                    as_stream(stream), p, map_rows, map_q) != cudaSuccess)
         return PA_ERR_CUDA;
     if (!c.whole &&
-        launch_pdl(k.join, dim3((unsigned)c.ranges, (unsigned)num_heads), dim3(kLatJoinThreads), 0,
+        launch_pdl(k.join, dim3((unsigned)(2 * sms)), dim3(kLatJoinThreads), 0,
                    as_stream(stream), p) != cudaSuccess)
         return PA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;

@@ -169,6 +169,13 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+// Largest of three values, NaN left aside.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 // Widen two packed 16-bit values (low half first) to fp32.
 template <bool BF16>
 __device__ __forceinline__ float2 widen2(uint32_t w) {

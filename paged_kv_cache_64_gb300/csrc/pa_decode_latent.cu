@@ -47,7 +47,7 @@ constexpr int kLatRope = 64;      // shared key values of a row
 constexpr int kLatTile = 64;      // positions of a tile
 constexpr int kLatWarps = 12;
 constexpr int kLatSoftmax = 256;  // softmax threads: two warpgroups
-constexpr int kLatAhead = 4;      // tiles that are on their way to L2
+constexpr int kLatAhead = 2;      // tiles from a copy to the prefetch to L2 behind it
 constexpr int kLatThreads = kLatWarps * 32;
 constexpr int kLatSmem = 232448;  // what a CTA may have
 constexpr int kLatMisc = 2048;    // barriers and exchange
@@ -89,7 +89,8 @@ struct LatShape {
     // barriers
     static constexpr int FULL = 0, EMPTY = STAGES, Q_FULL = EMPTY + 4 * STAGES, Q_FREE = Q_FULL + 1,
                          S_FULL = Q_FREE + 1, S_FREE = S_FULL + 2, P_FULL = S_FREE + 2,
-                         PV_DONE = P_FULL + 2, O_FREE = PV_DONE + 2, DRAIN = O_FREE + 1,
+                         PV_DONE = P_FULL + 2, O_FREE = PV_DONE + 2, VOTE = O_FREE + 1,
+                         DRAIN = VOTE + 1,
                          BARS = DRAIN + 2;
     // behind the barriers: TMEM address, abort flag, scan scratch, sums; then the heads'
     // factors and two halves' maxima
@@ -157,6 +158,23 @@ __device__ __forceinline__ bool latent_bar_or(bool v) {
     return any != 0;
 }
 
+// Largest (MAX) or smallest of 32 values, NaN left aside.
+template <bool MAX>
+__device__ __forceinline__ float top32(const float (&s)[32]) {
+    float t[2] = {s[0], s[1]};
+#pragma unroll
+    for (int j = 2; j < 32; j += 2) {
+        if constexpr (MAX) {
+            if (j & 2) t[0] = max3(t[0], s[j], s[j + 1]);
+            else t[1] = max3(t[1], s[j], s[j + 1]);
+        } else {
+            t[0] = fminf(t[0], s[j]);
+            t[1] = fminf(t[1], s[j + 1]);
+        }
+    }
+    return MAX ? fmaxf(t[0], t[1]) : fminf(t[0], t[1]);
+}
+
 template <bool BF16, int RANK, int NH>
 __global__ void __launch_bounds__(kLatThreads, 1)
     decode_latent_kernel(const __grid_constant__ DecodeLatentParams p,
@@ -180,9 +198,10 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         prefetch_tensormap(&map_rows);
         prefetch_tensormap(&map_q);
         for (int b = 0; b < S::BARS; ++b)
-            mbar_init(&bar[b], (b >= S::S_FREE && b < S::PV_DONE) || b == S::O_FREE
+            mbar_init(&bar[b], (b >= S::S_FREE && b < S::PV_DONE) || b == S::O_FREE || b == S::VOTE
                                       ? kLatSoftmax / 32 : 1);
         *abort_flag = 0;
+        words[4] = words[5] = 0;
         scan[kLatWarps] = p.num_seqs;
         scan[kLatWarps + 1] = 0;
         mbar_init_fence();
@@ -313,14 +332,11 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                 }
                 if (!ok) break;
                 if (++st == S::STAGES) st = 0, ++use;
-                // tile t + kLatAhead's units; with the first tile also those before it
-                const int back = t == 0 ? kLatAhead - 2 : 0;
-                const int ahead = t + kLatAhead - back + (lane >> 2);  // lane's tile
-                const int u = 4 * ahead + (lane & 3);
-                const bool same = (ahead >> 3) == (t >> 3);
-                const int r_cur = __shfl_sync(kFullMask, rows_cur, (4 * ahead + (lane & 3)) & 31);
-                const int r_next = __shfl_sync(kFullMask, rows_next, (4 * ahead + (lane & 3)) & 31);
-                if ((lane >> 2) <= back && u < units) prefetch(same ? r_cur : r_next);
+                // tile t + kLatAhead's units
+                const int u = 4 * (t + kLatAhead) + (lane & 3);
+                const int r_cur = __shfl_sync(kFullMask, rows_cur, u & 31);
+                const int r_next = __shfl_sync(kFullMask, rows_next, u & 31);
+                if (lane < 4 && u < units) prefetch((u >> 5) == (t >> 3) ? r_cur : r_next);
             }
         }
         // every copy has landed before shared memory goes (a stage's last use)
@@ -374,8 +390,8 @@ __global__ void __launch_bounds__(kLatThreads, 1)
             if (piece > 0) mbar_wait_flow(&bar[S::O_FREE], (piece - 1) & 1, flag);
             for (int t = 0; t < walk.n; ++t, ++g) {
                 const int pb = g % S::P_BUFS;
+                mbar_wait_flow(&bar[S::FULL + st], use & 1, flag);  // long since, as S came of it
                 mbar_wait_flow(&bar[S::P_FULL + pb], (g / S::P_BUFS) & 1, flag);
-                mbar_wait_flow(&bar[S::FULL + st], use & 1, flag);
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t w = p_desc + pb * (S::P_BYTES >> 4);
@@ -432,7 +448,8 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         // f16 weights as 2^7 of themselves: at most 2^15 with the lag of the maximum, and
         // normal down to 2^-21 of the largest
         constexpr float kLift = BF16 ? 0.f : 7.f;
-        int g = 0;
+        int g = 0, votes = 0;
+        volatile int *asked = words + 4;           // by the parity of votes
         int4 plan = make_int4(-1, 0, 0, 0);
         // P.V of tile k (counted over all pieces) is done.  One barrier a P buffer, whose
         // phases are waited for in turn: a tile's is, at the latest, before P goes into
@@ -461,21 +478,44 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[S::S_FREE + b]);
                 const int valid = min(walk.len - (walk.tile + t) * kLatTile, kLatTile);
-                if (valid == kLatTile) {
-#pragma unroll
-                    for (int j = 0; j < kPos; ++j) s[j] *= p.scale_log2;
-                } else {
+                const float sc = p.scale_log2;
+                if (valid < kLatTile) {
 #pragma unroll
                     for (int j = 0; j < kPos; ++j)  // NaN-safe select
-                        s[j] = kPos * half + j < valid ? s[j] * p.scale_log2 : -INFINITY;
+                        s[j] = kPos * half + j < valid ? s[j] : sc > 0.f ? -INFINITY : INFINITY;
                 }
-                float top[4] = {s[0], s[1], s[2], s[3]};
+                float mx = (sc > 0.f ? top32<true>(s) : top32<false>(s)) * sc;
+                uint32_t w[kPos / 2];
+                auto weigh = [&]() -> float {  // the weights' sum
+                    const float from = (m_run == -INFINITY ? 0.f : m_run) - kLift;
+                    const float2 sc2 = make_float2(sc, sc), from2 = make_float2(-from, -from);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int j = 4; j < kPos; ++j) top[j & 3] = fmaxf(top[j & 3], s[j]);
-                float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                // the first tile sets the maximum; later ones move it where a half asks for it
+                    for (int j = 0; j < kPos / 2; ++j) {
+                        const float2 x = __ffma2_rn(make_float2(s[2 * j], s[2 * j + 1]), sc2, from2);
+                        const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                        sum[j & 1] = __fadd2_rn(sum[j & 1], e);
+                        w[j] = narrow2<BF16>(e.x, e.y);
+                    }
+                    return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                };
+                // The first tile sets the maximum; later ones move it where a half asks for
+                // it.  The weights by the old one are on their way while the warps vote.
                 bool any = true;
-                if (t > 0) any = latent_bar_or((mine && mx > m_run + kLazyRescale) || !fine);
+                float sum = 0.f;
+                if (t > 0) {
+                    const bool ask = __any_sync(kFullMask, (mine && mx > m_run + kLazyRescale) || !fine);
+                    if (lane == 0) {
+                        if (ask) asked[votes & 1] = 1;
+                        mbar_arrive(&bar[S::VOTE]);
+                    }
+                    sum = weigh();
+                    fine = mbar_wait_or(&bar[S::VOTE], votes & 1, abort_flag) && fine;
+                    fine = __all_sync(kFullMask, fine);
+                    any = asked[votes & 1] != 0;
+                    ++votes;
+                }
+                // (a vote that ran out is everyone's: the next wait for S ends all)
                 if (any) {
                     if (mine) maxima[half * NH + row] = mx;
                     if (latent_bar_or(!fine)) {  // all end together
@@ -491,6 +531,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                     }
                     if (t > 0) {
                         if (mine && half == 0) alphas[row] = alpha;
+                        if (tid == 0) asked[(votes - 1) & 1] = 0;  // everyone has read it
                         fine = pv_done(g - 1);  // O at rest
                         if (latent_bar_or(!fine)) {
                             ok = false;
@@ -513,16 +554,8 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                         tmem_wait_st();
                     }
                 }
-                const float from = (m_run == -INFINITY ? 0.f : m_run) - kLift;
-                uint32_t w[kPos / 2];
-                float sum[4] = {};
-#pragma unroll
-                for (int j = 0; j < kPos / 2; ++j) {
-                    const float a = fast_exp2(s[2 * j] - from), c = fast_exp2(s[2 * j + 1] - from);
-                    sum[j & 3] += a + c;
-                    w[j] = narrow2<BF16>(a, c);
-                }
-                l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                if (any) sum = weigh();
+                l_run += sum;
                 if (g >= S::P_BUFS) fine = fine && pv_done(g - S::P_BUFS);  // P's buffer is free
                 if (valid < kLatTile) {
                     // rows past the length: P is 0 there, and V must be finite
@@ -624,6 +657,66 @@ __global__ void __launch_bounds__(kLatThreads, 1)
 constexpr int kLatJoinWarps = 8, kLatJoinThreads = kLatJoinWarps * 32;
 constexpr int kLatMaxRanges = kLatJoinThreads;
 
+// A warp's share of one unit: OWN float4 a lane from chunk `first` on of the head's
+// values, of pieces part, part + share, ...  The first sixteen loads go out before the
+// weights are known.
+template <int OWN, int NH, int RANK, typename SlotOf>
+__device__ __forceinline__ void latent_join(const DecodeLatentParams &p, float4 (&acc)[RANK / 128],
+                                            float *weight, int n, int row, int first, int part,
+                                            int share, SlotOf slot_of) {
+    constexpr int BATCH = 16 / OWN;
+    const int lane = threadIdx.x & 31;
+    float4 v[BATCH][OWN];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const int i = i0 + b * share;
+#pragma unroll
+            for (int k = 0; k < OWN; ++k)
+                v[b][k] = i < n ? reinterpret_cast<const float4 *>(
+                                      p.part_o + (slot_of(i) * NH + row) * RANK)[32 * (first + k) + lane]
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    };
+    load(part);
+    float2 ml[kLatMaxRanges / 32];
+    float M = -INFINITY, total = 0.f;
+#pragma unroll
+    for (int j = 0; j < kLatMaxRanges / 32; ++j) {
+        const int i = lane + 32 * j;
+        ml[j] = i < n ? *reinterpret_cast<const float2 *>(p.part_ml + (slot_of(i) * NH + row) * 2)
+                      : make_float2(-INFINITY, 0.f);
+        M = fmaxf(M, ml[j].x);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
+#pragma unroll
+    for (int j = 0; j < kLatMaxRanges / 32; ++j) {
+        const float w = ml[j].x == -INFINITY ? 0.f : fast_exp2(ml[j].x - M);
+        weight[lane + 32 * j] = w;
+        total += w * ml[j].y;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(kFullMask, total, o);
+    const float inv = total > 0.f ? 1.f / total : total == 0.f ? 0.f : total;
+    __syncwarp();
+    for (int i0 = part; i0 < n; i0 += BATCH * share) {
+        if (i0 > part) load(i0);
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const int i = i0 + b * share;
+            if (i < n) {
+                const float w = weight[i] * inv;
+#pragma unroll
+                for (int k = 0; k < OWN; ++k) {
+                    acc[k].x += w * v[b][k].x, acc[k].y += w * v[b][k].y;
+                    acc[k].z += w * v[b][k].z, acc[k].w += w * v[b][k].w;
+                }
+            }
+        }
+    }
+}
+
 template <bool BF16, int RANK, int NH>
 __global__ void __launch_bounds__(kLatJoinThreads) latent_join_kernel(
     const __grid_constant__ DecodeLatentParams p) {
@@ -668,37 +761,16 @@ __global__ void __launch_bounds__(kLatJoinThreads) latent_join_kernel(
         const int h = item % p.num_heads, group = h / NH, row = h % NH;
         if (unit < units) {
             plan = plans[item / p.num_heads];
-            const int n = plan.z + 1;
             auto slot_of = [&](int i) -> int64_t {
                 return ((int64_t)(plan.w + i) * p.groups + group) * 2 + (i == 0 ? plan.y : 0);
             };
-            float M = -INFINITY, total = 0.f;
-            for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_ml[(slot_of(i) * NH + row) * 2]);
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
-            for (int i = lane; i < n; i += 32) {
-                const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + (slot_of(i) * NH + row) * 2);
-                const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
-                weights[warp][i] = w;
-                total += w * ml.y;
-            }
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(kFullMask, total, o);
-            const float inv = total > 0.f ? 1.f / total : total == 0.f ? 0.f : total;
-            __syncwarp();
-#pragma unroll 4
-            for (int i = part; i < n; i += share) {
-                const float4 *from = reinterpret_cast<const float4 *>(p.part_o + (slot_of(i) * NH + row) * RANK) +
-                                     32 * first + lane;
-                const float w = weights[warp][i] * inv;
-#pragma unroll
-                for (int k = 0; k < CHUNKS; ++k)
-                    if (k < own) {
-                        const float4 v = from[32 * k];
-                        acc[k].x += w * v.x, acc[k].y += w * v.y;
-                        acc[k].z += w * v.z, acc[k].w += w * v.w;
-                    }
-            }
+            if (own == 1)
+                latent_join<1, NH, RANK>(p, acc, weights[warp], plan.z + 1, row, first, part, share, slot_of);
+            else if (own == 2)
+                latent_join<2, NH, RANK>(p, acc, weights[warp], plan.z + 1, row, first, part, share, slot_of);
+            else
+                latent_join<CHUNKS, NH, RANK>(p, acc, weights[warp], plan.z + 1, row, first, part, share,
+                                              slot_of);
         }
         if (share > 1) {
 #pragma unroll
@@ -749,6 +821,7 @@ static LatentLaunch latent_launch(int num_seqs, int num_heads, int rank, int max
     c.plan_bytes = up((size_t)c.ranges * 16);
     return c;
 }
+
 
 struct LatentKernels {
     void (*decode)(const DecodeLatentParams, const CUtensorMap, const CUtensorMap);
@@ -830,7 +903,7 @@ extern "C" pa_status pa_decode_latent(void *out, const void *q, const void *pool
     p.ranges = c.ranges;
     p.groups = c.groups;
     p.whole = c.whole;
-    p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    p.scale_log2 = latent_scale(scale);
     const bool bf16 = dtype == PA_BF16;
     const LatentKernels k = rank == 512 ? (bf16 ? latent_kernels<true, 512>(c.nh) : latent_kernels<false, 512>(c.nh))
                                         : (bf16 ? latent_kernels<true, 256>(c.nh) : latent_kernels<false, 256>(c.nh));

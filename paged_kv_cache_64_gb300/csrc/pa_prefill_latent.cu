@@ -16,11 +16,18 @@
 // Shared memory: Q (96 KiB) and a ring of eight 16 KiB slabs (128 keys x 64
 // values) that K (three slabs a tile) and V (two) pass through in turn.
 //
-// Roles (10 warps): 0 producer (TMA); 1 issues every product (and owns TMEM);
+// Roles (11 warps): 0 producer (TMA); 1 issues every product (and owns TMEM);
 // 2-5 softmax and epilogue of tile A, 6-9 of tile B: thread r of four warps owns
-// row r (TMEM lane r), so maxima and sums need no exchange.  The products of a
-// tile are issued in the order q.K(t), P.V(t), q.K(t + 1): S(t + 1) may take P(t)'s
-// place, and once it is there, O is at rest for the lazy rescale.
+// row r (TMEM lane r), so maxima and sums need no exchange; 10 fetches the CTA's
+// next work.  The products of a tile are issued in the order q.K(t), P.V(t),
+// q.K(t + 1): S(t + 1) may take P(t)'s place, and once it is there, O is at rest for
+// the lazy rescale.
+//
+// The launch has a block for every (256 queries, head, sequence) up to the longest
+// sequence; a CTA that runs takes over blocks that have not been launched yet
+// (clusterlaunchcontrol), so the next work's queries and keys load, and its first
+// products run, while the softmax of the last ends.  Blocks past a sequence's end
+// cost the fetching warp a look at its lengths.
 #include <cmath>
 #include <cstdint>
 
@@ -35,17 +42,30 @@ constexpr int kPreRows = 128;   // query rows of a tile
 constexpr int kPreKeys = 128;   // keys of a tile
 constexpr int kPreSlab = kPreKeys * 128;
 constexpr int kPreSlots = 8;    // slabs of the ring
-constexpr int kPreWarps = 10;
+constexpr int kPreWarps = 11;
 constexpr int kPreThreads = kPreWarps * 32;
 constexpr int kPreOffRing = 2 * 3 * kPreSlab;
 constexpr int kPreOffBar = kPreOffRing + kPreSlots * kPreSlab;
-constexpr int kPreSmem = kPreOffBar + 512 + 1024;  // + slack to align the base to 1 KiB
+constexpr int kPreSmem = kPreOffBar + 1024 + 1024;  // + slack to align the base to 1 KiB
 constexpr int kPreColS = 0, kPreColO = 256;        // TMEM columns: S_A S_B O_A O_B
+constexpr int kPreQueue = 3;                       // work in hand: being done and fetched
 static_assert(kPreSmem <= 232448, "shared memory");
 
 enum PreBar { kPreFull = 0, kPreEmpty = kPreSlots, kPreQFull = 2 * kPreSlots,
-              kPreSFull = kPreQFull + 2, kPrePReady = kPreSFull + 2, kPreODone = kPrePReady + 2,
-              kPreDrain = kPreODone + 2, kPreBars };
+              kPreQFree = kPreQFull + 2, kPreSFull = kPreQFree + 2, kPrePReady = kPreSFull + 2,
+              kPreODone = kPrePReady + 2, kPreOFree = kPreODone + 2, kPreWorkFull = kPreOFree + 2,
+              kPreWorkFree = kPreWorkFull + kPreQueue, kPreClaim = kPreWorkFree + kPreQueue,
+              kPreDrain, kPreBars };
+constexpr int kPreOffWork = kPreOffBar + 512;      // the queue, then the claim's answer
+constexpr int kPreOffClaim = kPreOffWork + kPreQueue * 32;
+constexpr int kPreOffWords = kPreOffClaim + 16;    // TMEM address, abort flag
+static_assert(kPreBars * 8 <= 512 && kPreOffWords + 8 <= kPreOffBar + 1024, "barriers");
+
+// 256 queries of a head of a sequence.
+struct PreWork {
+    int q0, n_q, k0, n_k;  // the sequence's tokens; n_q < 0: no more work
+    int head, first;       // first query in the sequence
+};
 
 struct PrefillLatentParams {
     uint16_t *out;
@@ -54,6 +74,26 @@ struct PrefillLatentParams {
     float scale_log2;
     int *err;
 };
+
+// Keys that rows [first + 128 x, + 128) of a sequence meet, in tiles.
+__device__ __forceinline__ int prefill_tiles(const PreWork &w, int x, int causal) {
+    const int a = w.first + x * kPreRows, b = min(a + kPreRows, w.n_q);
+    if (a >= w.n_q) return 0;
+    const int keys = causal ? min(w.n_k - w.n_q + b, w.n_k) : w.n_k;
+    return keys > 0 ? (keys + kPreKeys - 1) / kPreKeys : 0;
+}
+
+// Largest (MAX) or smallest of 128 values, NaN left aside.
+template <bool MAX>
+__device__ __forceinline__ float top128(const float (&s)[kPreKeys]) {
+    float t[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+    for (int j = 4; j < kPreKeys; j += 2) {
+        float &m = t[(j >> 1) & 3];
+        m = MAX ? max3(m, s[j], s[j + 1]) : fminf(fminf(m, s[j]), s[j + 1]);
+    }
+    return MAX ? fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) : fminf(fminf(t[0], t[1]), fminf(t[2], t[3]));
+}
 
 template <bool BF16>
 __global__ void __launch_bounds__(kPreThreads, 1)
@@ -66,42 +106,22 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kPreOffBar);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kPreOffBar + 384);
-    int *flag = reinterpret_cast<int *>(smem + kPreOffBar + 392);
+    int4 *queue = reinterpret_cast<int4 *>(smem + kPreOffWork);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kPreOffWords);
+    int *flag = reinterpret_cast<int *>(smem + kPreOffWords + 4);
     volatile int *abort_flag = flag;
-    static_assert(kPreBars * 8 <= 384, "barriers");
 
-    // the longest tiles of a causal sequence first
-    const int qt = gridDim.x - 1 - blockIdx.x, head = blockIdx.y, seq = blockIdx.z;
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
-    pdl_wait();
-    const int q0 = p.q_starts[seq], n_q = p.q_starts[seq + 1] - q0;
-    const int k0 = p.k_starts[seq], n_k = p.k_starts[seq + 1] - k0;
-    if (q0 < 0 || n_q < 0 || n_q > p.max_q || n_q > p.total_q - q0 || k0 < 0 || n_k < 0 ||
-        n_k > p.total_k - k0) {
-        if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0)
-            record_error(p.err, PA_ERR_BAD_INDEX);
-        return;
-    }
-    const int first = qt * 2 * kPreRows;  // the CTA's first query in the sequence
-    if (first >= n_q) return;
-    // keys that a tile's rows meet: row i those below reach + i (causal) or n_k
-    const int reach = p.causal ? n_k - n_q + 1 : n_k;
-    auto tiles_of = [&](int x) -> int {
-        const int a = first + x * kPreRows, b = min(a + kPreRows, n_q);
-        if (a >= n_q) return 0;
-        const int keys = p.causal ? min(reach + b - 1, n_k) : n_k;
-        return keys > 0 ? (keys + kPreKeys - 1) / kPreKeys : 0;
-    };
-    const int tiles0 = tiles_of(0), tiles1 = tiles_of(1), most = max(tiles0, tiles1);
-
     if (threadIdx.x == 0) {
         prefetch_tensormap(&map_q);
         prefetch_tensormap(&map_k);
         prefetch_tensormap(&map_v);
         prefetch_tensormap(&map_pe);
-        for (int b = 0; b < kPreBars; ++b)
-            mbar_init(&bar[b], b >= kPrePReady && b < kPreODone ? 4 : 1);
+        for (int b = 0; b < kPreBars; ++b) {
+            const bool softmax = (b >= kPrePReady && b < kPreODone) || (b >= kPreOFree && b < kPreWorkFull);
+            const bool work = b >= kPreWorkFree && b < kPreClaim;
+            mbar_init(&bar[b], softmax ? 4 : work ? 10 : 1);  // ten warps end a turn
+        }
         *abort_flag = 0;
         mbar_init_fence();
     }
@@ -113,43 +133,132 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    pdl_wait();
     pdl_trigger();
     bool ok = true;
+    // The work of turn i, once it is there (roles take it in turns 0, 1, ...).
+    auto read_work = [&](int turn) -> PreWork {
+        const int4 a = queue[2 * (turn % kPreQueue)], b = queue[2 * (turn % kPreQueue) + 1];
+        return {a.x, a.y, a.z, a.w, b.x, b.y};
+    };
+    auto work_full = [&](int turn) -> uint64_t * { return &bar[kPreWorkFull + turn % kPreQueue]; };
+    auto work_free = [&](int turn) -> uint64_t * { return &bar[kPreWorkFree + turn % kPreQueue]; };
 
-    if (warp == 0) {
-        // ---------------------------------------------------------- producer
-        if (lane == 0 && most > 0) {
-            auto load_q = [&](int x) {
-                mbar_arrive_expect_tx(&bar[kPreQFull + x], 3 * kPreSlab);
-                for (int i = 0; i < 3; ++i)
-                    tma_load_3d(smem + (3 * x + i) * kPreSlab, &map_q, 64 * i, q0 + first + x * kPreRows,
-                                head, &bar[kPreQFull + x]);
-            };
-            // slab u: of tile u / 5 the keys' own values (two), the shared ones, V (two)
-            auto load = [&](int u) -> bool {
-                const int slot = u % kPreSlots, use = u / kPreSlots, t = u / 5, i = u % 5;
-                if (use > 0 && !mbar_wait_or(&bar[kPreEmpty + slot], (use - 1) & 1, abort_flag))
+    if (warp == 10) {
+        // ---------------------------------------------------------- next work
+        if (lane == 0) {
+            int x = blockIdx.x, y = blockIdx.y, z = blockIdx.z, claims = 0;
+            // a block that has not been launched yet becomes this CTA's; false: none is left
+            auto claim = [&]() -> bool {
+                const uint32_t answer = smem_addr(smem + kPreOffClaim);
+                fence_async_smem();  // the last answer has been read
+                mbar_arrive_expect_tx(&bar[kPreClaim], 16);
+                asm volatile(
+                    "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+                    "[%0], [%1];" ::"r"(answer), "r"(smem_addr(&bar[kPreClaim]))
+                    : "memory");
+                if (!mbar_wait(&bar[kPreClaim], claims & 1)) {
+                    ok = false;
                     return false;
-                uint8_t *to = smem + kPreOffRing + slot * kPreSlab;
-                uint64_t *full = &bar[kPreFull + slot];
-                mbar_arrive_expect_tx(full, kPreSlab);
-                const int key = k0 + t * kPreKeys;
-                if (i == 2)
-                    tma_load_2d(to, &map_pe, 0, key, full);
-                else
-                    tma_load_3d(to, i < 2 ? &map_k : &map_v, 64 * (i < 2 ? i : i - 3), key, head, full);
-                return true;
+                }
+                ++claims;
+                uint32_t got;
+                asm volatile(
+                    "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t"
+                    "ld.shared.b128 a, [%4];\n\t"
+                    "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+                    "selp.u32 %0, 1, 0, p;\n\t"
+                    "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+                    "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 "
+                    "{%1, %2, %3, _}, a;\n\t}"
+                    : "=&r"(got), "=&r"(x), "=&r"(y), "=&r"(z)
+                    : "r"(answer)
+                    : "memory");
+                return got != 0;
             };
-            int u = 0;
-            if (tiles0 > 0) load_q(0);
-            for (; u < 3; ++u) load(u);
-            if (tiles1 > 0) load_q(1);
-            for (; ok && u < 5 * most; u += ok) ok = load(u);
+            bool have = true;  // (x, y, z) is a block to look at
+            for (int turn = 0;; ++turn) {
+                if (turn >= kPreQueue &&
+                    !mbar_wait_or(work_free(turn), (turn / kPreQueue - 1) & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                PreWork w;
+                for (;;) {
+                    w = {0, -1, 0, 0, 0, 0};
+                    if (!have && !claim()) break;
+                    have = false;
+                    // the longest tiles of a causal sequence come first
+                    w.first = ((int)gridDim.x - 1 - x) * 2 * kPreRows;
+                    w.head = y;
+                    w.q0 = p.q_starts[z];
+                    w.k0 = p.k_starts[z];
+                    const int q1 = p.q_starts[z + 1], k1 = p.k_starts[z + 1];
+                    const bool good = w.q0 >= 0 && q1 >= w.q0 && q1 - w.q0 <= p.max_q && q1 <= p.total_q &&
+                                      w.k0 >= 0 && k1 >= w.k0 && k1 <= p.total_k;
+                    if (!good && x == 0 && y == 0) record_error(p.err, PA_ERR_BAD_INDEX);
+                    if (good && w.first < q1 - w.q0) {
+                        w.n_q = q1 - w.q0;
+                        w.n_k = k1 - w.k0;
+                        break;
+                    }
+                }
+                queue[2 * (turn % kPreQueue)] = make_int4(w.q0, w.n_q, w.k0, w.n_k);
+                queue[2 * (turn % kPreQueue) + 1] = make_int4(w.head, w.first, 0, 0);
+                mbar_arrive(work_full(turn));
+                if (w.n_q < 0) break;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 0) {
+        // ---------------------------------------------------------- producer
+        if (lane == 0) {
+            int u = 0, loaded[2] = {0, 0};  // slabs; queries of either tile
+            for (int turn = 0; ok; ++turn) {
+                ok = mbar_wait_or(work_full(turn), (turn / kPreQueue) & 1, abort_flag);
+                if (!ok) break;
+                const PreWork w = read_work(turn);
+                if (w.n_q < 0) break;
+                const int tiles0 = prefill_tiles(w, 0, p.causal), tiles1 = prefill_tiles(w, 1, p.causal);
+                const int end = u + 5 * max(tiles0, tiles1);
+                auto load_q = [&](int x, int &count) -> bool {
+                    if (count > 0 && !mbar_wait_or(&bar[kPreQFree + x], (count - 1) & 1, abort_flag))
+                        return false;
+                    ++count;
+                    mbar_arrive_expect_tx(&bar[kPreQFull + x], 3 * kPreSlab);
+                    for (int i = 0; i < 3; ++i)
+                        tma_load_3d(smem + (3 * x + i) * kPreSlab, &map_q, 64 * i,
+                                    w.q0 + w.first + x * kPreRows, w.head, &bar[kPreQFull + x]);
+                    return true;
+                };
+                // slab i of a tile: the keys' own values (two), the shared ones, V (two)
+                auto load = [&](int i, int key) -> bool {
+                    const int slot = u % kPreSlots, use = u / kPreSlots;
+                    if (use > 0 && !mbar_wait_or(&bar[kPreEmpty + slot], (use - 1) & 1, abort_flag))
+                        return false;
+                    uint8_t *to = smem + kPreOffRing + slot * kPreSlab;
+                    uint64_t *full = &bar[kPreFull + slot];
+                    mbar_arrive_expect_tx(full, kPreSlab);
+                    if (i == 2)
+                        tma_load_2d(to, &map_pe, 0, key, full);
+                    else
+                        tma_load_3d(to, i < 2 ? &map_k : &map_v, 64 * (i < 2 ? i : i - 3), key, w.head, full);
+                    ++u;
+                    return true;
+                };
+                if (tiles0 > 0) ok = load_q(0, loaded[0]);
+                for (int key = w.k0; ok && u < end; key += kPreKeys)
+                    for (int i = 0; ok && i < 5; ++i) {
+                        if (i == 3 && key == w.k0 && tiles1 > 0) ok = load_q(1, loaded[1]);
+                        ok = ok && load(i, key);
+                    }
+                mbar_arrive(work_free(turn));
+            }
             // every copy has landed before shared memory goes (each slot's last use)
             for (int s = max(0, u - kPreSlots); s < u; ++s)
                 (void)mbar_wait(&bar[kPreFull + s % kPreSlots], (s / kPreSlots) & 1);
-            if (tiles0 > 0) (void)mbar_wait(&bar[kPreQFull], 0);
-            if (tiles1 > 0) (void)mbar_wait(&bar[kPreQFull + 1], 0);
+            if (loaded[0] > 0) (void)mbar_wait(&bar[kPreQFull], (loaded[0] - 1) & 1);
+            if (loaded[1] > 0) (void)mbar_wait(&bar[kPreQFull + 1], (loaded[1] - 1) & 1);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -160,12 +269,16 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         const uint64_t q_desc = sw128_desc(base, 16, 1024);
         const uint64_t k_desc = sw128_desc(base + kPreOffRing, 16, 1024);
         const uint64_t v_desc = sw128_desc(base + kPreOffRing, kPreSlab, 1024);
-        auto issue_qk = [&](int x, int t) {
-            if (t == 0) mbar_wait_flow(&bar[kPreQFull + x], 0, flag);
-            const bool last = x == 1 || t >= tiles1;  // tile B uses a slab last where it reaches it
+        int at[2] = {0, 0}, works[2] = {0, 0};  // P.V steps and pieces of work of either tile
+        struct Turn {
+            int turn, tiles0, tiles1, most, slab;  // most 0: no more work
+        };
+        auto issue_qk = [&](int x, const Turn &w, int t) {
+            if (t == 0) mbar_wait_flow(&bar[kPreQFull + x], works[x] & 1, flag);
+            const bool last = x == 1 || t >= w.tiles1;  // tile B uses a slab last where it reaches it
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
-                const int u = 5 * t + i, slot = u % kPreSlots;
+                const int u = w.slab + 5 * t + i, slot = u % kPreSlots;
                 mbar_wait_flow(&bar[kPreFull + slot], (u / kPreSlots) & 1, flag);
                 tc_fence_after();
                 if (elect_one()) {
@@ -175,17 +288,24 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                     for (int ks = 0; ks < 4; ++ks)
                         tc_mma(tmem + kPreColS + 128 * x, q + ks * 2, k + ks * 2, idesc_qk, i > 0 || ks > 0);
                     if (last) tc_commit(&bar[kPreEmpty + slot]);
-                    if (i == 2) tc_commit(&bar[kPreSFull + x]);
+                    if (i == 2) {
+                        tc_commit(&bar[kPreSFull + x]);
+                        if (t + 1 == (x ? w.tiles1 : w.tiles0)) tc_commit(&bar[kPreQFree + x]);
+                    }
                 }
                 __syncwarp();
             }
         };
-        auto issue_pv = [&](int x, int t) {
-            mbar_wait_flow(&bar[kPrePReady + x], t & 1, flag);
-            const bool last = x == 1 || t >= tiles1;
+        auto issue_pv = [&](int x, const Turn &w, int t) {
+            // O has been read where it begins anew
+            if (t == 0 && works[x] > 0) mbar_wait_flow(&bar[kPreOFree + x], (works[x] - 1) & 1, flag);
+            mbar_wait_flow(&bar[kPrePReady + x], at[x] & 1, flag);
+            ++at[x];
+            const bool last = x == 1 || t >= w.tiles1;
+            const bool done = t + 1 == (x ? w.tiles1 : w.tiles0);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int u = 5 * t + 3 + i, slot = u % kPreSlots;
+                const int u = w.slab + 5 * t + 3 + i, slot = u % kPreSlots;
                 mbar_wait_flow(&bar[kPreFull + slot], (u / kPreSlots) & 1, flag);
                 tc_fence_after();
                 if (elect_one()) {
@@ -195,130 +315,174 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                         tc_mma_ts(tmem + kPreColO + 128 * x + 64 * i, tmem + kPreColS + 128 * x + 8 * ks,
                                   v + ks * (2048 >> 4), idesc_pv, t > 0 || ks > 0);
                     if (last) tc_commit(&bar[kPreEmpty + slot]);
-                    if (i == 1 && t + 1 == (x ? tiles1 : tiles0)) tc_commit(&bar[kPreODone + x]);
+                    if (i == 1 && done) tc_commit(&bar[kPreODone + x]);
                 }
                 __syncwarp();
             }
+            if (done) ++works[x];
         };
-        if (tiles0 > 0) issue_qk(0, 0);
-        if (tiles1 > 0) issue_qk(1, 0);
-        for (int t = 0; t < most; ++t) {
-            if (t < tiles0) issue_pv(0, t);
-            if (t + 1 < tiles0) issue_qk(0, t + 1);
-            if (t < tiles1) issue_pv(1, t);
-            if (t + 1 < tiles1) issue_qk(1, t + 1);
+        // the next work that has keys
+        auto next = [&](int turn, int slab) -> Turn {
+            for (;; ++turn) {
+                mbar_wait_flow(work_full(turn), (turn / kPreQueue) & 1, flag);
+                const PreWork w = read_work(turn);
+                if (__any_sync(kFullMask, *abort_flag || w.n_q < 0)) return {turn, 0, 0, 0, slab};
+                // by shuffles: values that the compiler knows to be the warp's
+                const int tiles0 = __shfl_sync(kFullMask, prefill_tiles(w, 0, p.causal), 0);
+                const int tiles1 = __shfl_sync(kFullMask, prefill_tiles(w, 1, p.causal), 0);
+                const int most = max(tiles0, tiles1);
+                if (most > 0) return {turn, tiles0, tiles1, most, slab};
+                if (elect_one()) mbar_arrive(work_free(turn));
+                __syncwarp();
+            }
+        };
+        Turn w = next(0, 0);
+        if (w.tiles0 > 0) issue_qk(0, w, 0);
+        if (w.tiles1 > 0) issue_qk(1, w, 0);
+        while (w.most > 0) {
+            for (int t = 0; t + 1 < w.most; ++t) {
+                if (t < w.tiles0) issue_pv(0, w, t);
+                if (t + 1 < w.tiles0) issue_qk(0, w, t + 1);
+                if (t < w.tiles1) issue_pv(1, w, t);
+                if (t + 1 < w.tiles1) issue_qk(1, w, t + 1);
+            }
+            // Every q.K of this work is issued: the next one's first may go before the other
+            // tile's last P.V, as they need no slab but the two of V beside their own three.
+            const int t = w.most - 1;
+            if (t < w.tiles0) issue_pv(0, w, t);
+            const Turn n = next(w.turn + 1, w.slab + 5 * w.most);
+            if (n.tiles0 > 0) issue_qk(0, n, 0);
+            if (t < w.tiles1) issue_pv(1, w, t);
+            if (n.tiles1 > 0) issue_qk(1, n, 0);
+            if (elect_one()) mbar_arrive(work_free(w.turn));
+            __syncwarp();
+            w = n;
         }
         if (elect_one()) tc_commit(&bar[kPreDrain]);
         (void)mbar_wait(&bar[kPreDrain], 0);
         __syncwarp();
     } else {
         // ---------------------------------------------------------- softmax / epilogue
-        const int x = (warp - 2) >> 2, tiles = x ? tiles1 : tiles0;
+        const int x = (warp - 2) >> 2;
         const int quad = warp & 3, r = quad * 32 + lane;  // TMEM lane = row of the tile
-        const int row = first + x * kPreRows + r;         // query in the sequence
         const uint32_t s_at = tmem + ((uint32_t)(quad * 32) << 16) + kPreColS + 128 * x;
         const uint32_t o_at = tmem + ((uint32_t)(quad * 32) << 16) + kPreColO + 128 * x;
-        const int limit = p.causal ? min(reach + row, n_k) : n_k;  // keys below it are met
-        // up to here no row of the tile has a masked key
-        const int clear = p.causal ? min(reach + first + x * kPreRows, n_k) : n_k;
         // f16 weights as 2^7 of themselves: at most 2^15 with the lag of the maximum, and
         // normal down to 2^-21 of the largest
         constexpr float kLift = BF16 ? 0.f : 7.f;
-        float m_run = -INFINITY, l_run = 0.f;
-        for (int t = 0; ok && t < tiles; ++t) {
-            ok = __all_sync(kFullMask, mbar_wait_or(&bar[kPreSFull + x], t & 1, abort_flag));
+        const float sc = p.scale_log2;
+        int steps = 0, works = 0, slab = 0;
+        for (int turn = 0; ok; ++turn) {
+            ok = __all_sync(kFullMask, mbar_wait_or(work_full(turn), (turn / kPreQueue) & 1, abort_flag));
             if (!ok) break;
-            tc_fence_after();
-            float s[kPreKeys];
+            const PreWork w = read_work(turn);
+            if (w.n_q < 0) break;
+            const int tiles0 = prefill_tiles(w, 0, p.causal), tiles1 = prefill_tiles(w, 1, p.causal);
+            const int tiles = x ? tiles1 : tiles0;
+            const int row = w.first + x * kPreRows + r;  // query in the sequence
+            // keys below the limit are met; below `clear` no row of the tile has a masked one
+            const int reach = w.n_k - w.n_q + 1;
+            const int limit = p.causal ? min(reach + row, w.n_k) : w.n_k;
+            const int clear = p.causal ? min(reach + w.first + x * kPreRows, w.n_k) : w.n_k;
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int t = 0; t < tiles; ++t, ++steps) {
+                ok = __all_sync(kFullMask, mbar_wait_or(&bar[kPreSFull + x], steps & 1, abort_flag));
+                if (!ok) break;
+                tc_fence_after();
+                float s[kPreKeys];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, s + 32 * c);
-            const int here = t * kPreKeys;
-            const float sc = p.scale_log2;
-            float mx = -INFINITY;
-            if (here + kPreKeys <= clear) {
+                for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, s + 32 * c);
+                const int here = t * kPreKeys;
+                if (here + kPreKeys > clear) {
+                    const float none = sc > 0.f ? -INFINITY : INFINITY;
 #pragma unroll
-                for (int j = 0; j < kPreKeys; ++j) {
-                    s[j] *= sc;
-                    mx = fmaxf(mx, s[j]);
+                    for (int j = 0; j < kPreKeys; ++j) s[j] = here + j < limit ? s[j] : none;  // NaN-safe
                 }
-            } else {
-#pragma unroll
-                for (int j = 0; j < kPreKeys; ++j) {
-                    s[j] = here + j < limit ? s[j] * sc : -INFINITY;  // NaN-safe select
-                    mx = fmaxf(mx, s[j]);
+                const float mx = (sc > 0.f ? top128<true>(s) : top128<false>(s)) * sc;
+                const bool need = mx > m_run + kLazyRescale;
+                float alpha = 1.f;
+                if (need) {
+                    alpha = fast_exp2(m_run - mx);  // 0 from an empty maximum
+                    m_run = mx;
+                    l_run *= alpha;
                 }
-            }
-            const bool need = mx > m_run + kLazyRescale;
-            float alpha = 1.f;
-            if (need) {
-                alpha = fast_exp2(m_run - mx);  // 0 from an empty maximum
-                m_run = mx;
-                l_run *= alpha;
-            }
-            if (t > 0 && __any_sync(kFullMask, need)) {
+                if (t > 0 && __any_sync(kFullMask, need)) {
 #pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
+                    for (int c = 0; c < 8; ++c) {
+                        float o[16];
+                        tmem_load16(o_at + 16 * c, o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] *= alpha;
+                        tmem_store16(o_at + 16 * c, o);
+                    }
+                }
+                const float from = (m_run == -INFINITY ? 0.f : m_run) - kLift;
+                const float2 sc2 = make_float2(sc, sc), from2 = make_float2(-from, -from);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
                     float o[16];
-                    tmem_load16(o_at + 16 * c, o);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] *= alpha;
-                    tmem_store16(o_at + 16 * c, o);
+                    for (int j = 0; j < 16; ++j) {
+                        const int k = 32 * c + 2 * j;
+                        const float2 y = __ffma2_rn(make_float2(s[k], s[k + 1]), sc2, from2);
+                        const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                        sum[j & 1] = __fadd2_rn(sum[j & 1], e);
+                        o[j] = __uint_as_float(narrow2<BF16>(e.x, e.y));
+                    }
+                    tmem_store16(s_at + 16 * c, o);
                 }
-            }
-            const float from = (m_run == -INFINITY ? 0.f : m_run) - kLift;
-            float sum[4] = {};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float w[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float a = fast_exp2(s[32 * c + 2 * j] - from);
-                    const float b = fast_exp2(s[32 * c + 2 * j + 1] - from);
-                    sum[j & 3] += a + b;
-                    w[j] = __uint_as_float(narrow2<BF16>(a, b));
+                l_run += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                tmem_wait_st();
+                if (here + kPreKeys > w.n_k && (x == 0 || t >= tiles0)) {
+                    // rows past the sequence's keys: P is 0 there, and V must be finite.  Tile
+                    // B's product follows A's, so the first tile to reach them clears them.
+                    for (int i = 0; i < 2; ++i) {
+                        const int u = slab + 5 * t + 3 + i;
+                        if (!mbar_wait_or(&bar[kPreFull + u % kPreSlots], (u / kPreSlots) & 1, abort_flag))
+                            *abort_flag = 1;  // the next wait for S ends all
+                        uint4 *z = reinterpret_cast<uint4 *>(smem + kPreOffRing + (u % kPreSlots) * kPreSlab);
+                        for (int k = (w.n_k - here) * 8 + r; k < kPreKeys * 8; k += 128)
+                            z[k] = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
                 }
-                tmem_store16(s_at + 16 * c, w);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[kPrePReady + x]);
             }
-            l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_wait_st();
-            if (here + kPreKeys > n_k && (x == 0 || t >= tiles0)) {
-                // rows past the sequence's keys: P is 0 there, and V must be finite.  Tile B's
-                // product follows A's, so the first tile to reach them clears them.
-                for (int i = 0; i < 2; ++i) {
-                    const int u = 5 * t + 3 + i;
-                    ok = ok && mbar_wait_or(&bar[kPreFull + u % kPreSlots], (u / kPreSlots) & 1, abort_flag);
-                    uint4 *z = reinterpret_cast<uint4 *>(smem + kPreOffRing + (u % kPreSlots) * kPreSlab);
-                    for (int k = (n_k - here) * 8 + r; k < kPreKeys * 8; k += 128)
-                        z[k] = make_uint4(0, 0, 0, 0);
-                }
-                fence_async_smem();
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[kPrePReady + x]);
-        }
-        if (tiles > 0 && ok)
-            ok = __all_sync(kFullMask, mbar_wait_or(&bar[kPreODone + x], 0, abort_flag));
-        if (ok) {
+            if (ok && tiles > 0)
+                ok = __all_sync(kFullMask, mbar_wait_or(&bar[kPreODone + x], works & 1, abort_flag));
+            if (!ok) break;
             tc_fence_after();
             const float inv = l_run > 0.f ? 1.f / l_run : l_run == 0.f ? 0.f : l_run;
             uint4 *to = reinterpret_cast<uint4 *>(
-                p.out + ((int64_t)(q0 + row) * p.num_heads + head) * kPreValue);
+                p.out + ((int64_t)(w.q0 + row) * p.num_heads + w.head) * kPreValue);
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-                float o[16];
+            for (int c = 0; c < 4; ++c) {
+                float o[32];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = 0.f;
-                if (tiles > 0) tmem_load16(o_at + 16 * c, o);
-                if (row < n_q) {
+                for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                if (tiles > 0) tmem_ld32(o_at + 32 * c, o);
+                if (row < w.n_q) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = l_run == 0.f ? 0.f : o[i] * inv;
-                    to[2 * c] = make_uint4(narrow2<BF16>(o[0], o[1]), narrow2<BF16>(o[2], o[3]),
-                                           narrow2<BF16>(o[4], o[5]), narrow2<BF16>(o[6], o[7]));
-                    to[2 * c + 1] = make_uint4(narrow2<BF16>(o[8], o[9]), narrow2<BF16>(o[10], o[11]),
-                                               narrow2<BF16>(o[12], o[13]), narrow2<BF16>(o[14], o[15]));
+                    for (int i = 0; i < 32; ++i) o[i] = l_run == 0.f ? 0.f : o[i] * inv;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        to[4 * c + i] = make_uint4(narrow2<BF16>(o[8 * i], o[8 * i + 1]),
+                                                   narrow2<BF16>(o[8 * i + 2], o[8 * i + 3]),
+                                                   narrow2<BF16>(o[8 * i + 4], o[8 * i + 5]),
+                                                   narrow2<BF16>(o[8 * i + 6], o[8 * i + 7]));
                 }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (tiles > 0) mbar_arrive(&bar[kPreOFree + x]);
+                mbar_arrive(work_free(turn));
+            }
+            works += tiles > 0;
+            slab += 5 * max(tiles0, tiles1);
         }
     }
     if (!ok) *abort_flag = 1;
@@ -366,7 +530,7 @@ extern "C" pa_status pa_prefill_latent(
     p.max_q = max_q_len;
     p.num_heads = num_heads;
     p.causal = causal != 0;
-    p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    p.scale_log2 = latent_scale(scale);
     const bool bf16 = dtype == PA_BF16;
     // without keys no map of theirs is used: q stands in
     const bool keys = total_k > 0;

@@ -51,7 +51,11 @@ constexpr int kPreColS = 0, kPreColO = 256;        // TMEM columns: S_A S_B O_A 
 constexpr int kPreQueue = 3;                       // work in hand: being done and fetched
 static_assert(kPreSmem <= 232448, "shared memory");
 
-enum PreBar { kPreFull = 0, kPreEmpty = kPreSlots, kPreQFull = 2 * kPreSlots,
+// K and V of a tile are awaited as a whole: group 2 t is K's slabs, 2 t + 1 V's.  At
+// most four groups lie in the ring.
+constexpr int kPreGroups = 4;
+
+enum PreBar { kPreFull = 0, kPreEmpty = kPreGroups, kPreQFull = kPreEmpty + kPreSlots,
               kPreQFree = kPreQFull + 2, kPreSFull = kPreQFree + 2, kPrePReady = kPreSFull + 2,
               kPreODone = kPrePReady + 2, kPreOFree = kPreODone + 2, kPreWorkFull = kPreOFree + 2,
               kPreWorkFree = kPreWorkFull + kPreQueue, kPreClaim = kPreWorkFree + kPreQueue,
@@ -71,6 +75,7 @@ struct PrefillLatentParams {
     uint16_t *out;
     const int32_t *q_starts, *k_starts;
     int total_q, total_k, max_q, num_heads, causal;
+    int wide;  // out lies on a 32-byte boundary
     float scale_log2;
     int *err;
 };
@@ -93,6 +98,19 @@ __device__ __forceinline__ float top128(const float (&s)[kPreKeys]) {
         m = MAX ? max3(m, s[j], s[j + 1]) : fminf(fminf(m, s[j]), s[j + 1]);
     }
     return MAX ? fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) : fminf(fminf(t[0], t[1]), fminf(t[2], t[3]));
+}
+
+// 32 bytes, in one store where the address allows it (a thread stores its own row, so
+// a store of a warp touches 32 lines however short it is).
+__device__ __forceinline__ void store32(uint16_t *to, const uint32_t *y, int wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(y[0]),
+                     "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(to)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+        reinterpret_cast<uint4 *>(to)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    }
 }
 
 template <bool BF16>
@@ -213,7 +231,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     } else if (warp == 0) {
         // ---------------------------------------------------------- producer
         if (lane == 0) {
-            int u = 0, loaded[2] = {0, 0};  // slabs; queries of either tile
+            int u = 0, group = 0, loaded[2] = {0, 0};  // slabs, groups of them; queries of either tile
+            uint64_t *full = nullptr;
             for (int turn = 0; ok; ++turn) {
                 ok = mbar_wait_or(work_full(turn), (turn / kPreQueue) & 1, abort_flag);
                 if (!ok) break;
@@ -231,14 +250,18 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                                     w.q0 + w.first + x * kPreRows, w.head, &bar[kPreQFull + x]);
                     return true;
                 };
-                // slab i of a tile: the keys' own values (two), the shared ones, V (two)
+                // Slab i of a tile: the keys' own values (two), the shared ones, V (two).  K's
+                // three and V's two are awaited as one, on the barrier of the first.
                 auto load = [&](int i, int key) -> bool {
                     const int slot = u % kPreSlots, use = u / kPreSlots;
                     if (use > 0 && !mbar_wait_or(&bar[kPreEmpty + slot], (use - 1) & 1, abort_flag))
                         return false;
                     uint8_t *to = smem + kPreOffRing + slot * kPreSlab;
-                    uint64_t *full = &bar[kPreFull + slot];
-                    mbar_arrive_expect_tx(full, kPreSlab);
+                    if (i == 0 || i == 3) {
+                        full = &bar[kPreFull + group % kPreGroups];
+                        ++group;
+                        mbar_arrive_expect_tx(full, (i == 0 ? 3 : 2) * kPreSlab);
+                    }
                     if (i == 2)
                         tma_load_2d(to, &map_pe, 0, key, full);
                     else
@@ -254,9 +277,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                     }
                 mbar_arrive(work_free(turn));
             }
-            // every copy has landed before shared memory goes (each slot's last use)
-            for (int s = max(0, u - kPreSlots); s < u; ++s)
-                (void)mbar_wait(&bar[kPreFull + s % kPreSlots], (s / kPreSlots) & 1);
+            // every copy has landed before shared memory goes (each barrier's last use)
+            for (int s = max(0, group - kPreGroups); s < group; ++s)
+                (void)mbar_wait(&bar[kPreFull + s % kPreGroups], (s / kPreGroups) & 1);
             if (loaded[0] > 0) (void)mbar_wait(&bar[kPreQFull], (loaded[0] - 1) & 1);
             if (loaded[1] > 0) (void)mbar_wait(&bar[kPreQFull + 1], (loaded[1] - 1) & 1);
         }
@@ -271,67 +294,72 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         const uint64_t v_desc = sw128_desc(base + kPreOffRing, kPreSlab, 1024);
         int at[2] = {0, 0}, works[2] = {0, 0};  // P.V steps and pieces of work of either tile
         struct Turn {
-            int turn, tiles0, tiles1, most, slab;  // most 0: no more work
+            int turn, tiles0, tiles1, most, tile;  // most 0: no more work; tile: counted over all work
         };
+        auto landed = [&](int group) {
+            mbar_wait_flow(&bar[kPreFull + group % kPreGroups], (group / kPreGroups) & 1, flag);
+        };
+        // (a slab's first user waits for it; tile B uses it last where it reaches that far)
         auto issue_qk = [&](int x, const Turn &w, int t) {
             if (t == 0) mbar_wait_flow(&bar[kPreQFull + x], works[x] & 1, flag);
-            const bool last = x == 1 || t >= w.tiles1;  // tile B uses a slab last where it reaches it
+            if (x == 0 || t >= w.tiles0) landed(2 * (w.tile + t));
+            const bool last = x == 1 || t >= w.tiles1;
+            const bool done = t + 1 == (x ? w.tiles1 : w.tiles0);
+            const int u = 5 * (w.tile + t);
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < 3; ++i) {
-                const int u = w.slab + 5 * t + i, slot = u % kPreSlots;
-                mbar_wait_flow(&bar[kPreFull + slot], (u / kPreSlots) & 1, flag);
-                tc_fence_after();
-                if (elect_one()) {
+                for (int i = 0; i < 3; ++i) {
+                    const int slot = (u + i) % kPreSlots;
                     const uint64_t q = q_desc + ((3 * x + i) * kPreSlab >> 4);
                     const uint64_t k = k_desc + slot * (kPreSlab >> 4);
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         tc_mma(tmem + kPreColS + 128 * x, q + ks * 2, k + ks * 2, idesc_qk, i > 0 || ks > 0);
                     if (last) tc_commit(&bar[kPreEmpty + slot]);
-                    if (i == 2) {
-                        tc_commit(&bar[kPreSFull + x]);
-                        if (t + 1 == (x ? w.tiles1 : w.tiles0)) tc_commit(&bar[kPreQFree + x]);
-                    }
                 }
-                __syncwarp();
+                tc_commit(&bar[kPreSFull + x]);
+                if (done) tc_commit(&bar[kPreQFree + x]);
             }
+            __syncwarp();
         };
         auto issue_pv = [&](int x, const Turn &w, int t) {
             // O has been read where it begins anew
             if (t == 0 && works[x] > 0) mbar_wait_flow(&bar[kPreOFree + x], (works[x] - 1) & 1, flag);
+            if (x == 0 || t >= w.tiles0) landed(2 * (w.tile + t) + 1);
             mbar_wait_flow(&bar[kPrePReady + x], at[x] & 1, flag);
             ++at[x];
             const bool last = x == 1 || t >= w.tiles1;
             const bool done = t + 1 == (x ? w.tiles1 : w.tiles0);
+            const int u = 5 * (w.tile + t) + 3;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int u = w.slab + 5 * t + 3 + i, slot = u % kPreSlots;
-                mbar_wait_flow(&bar[kPreFull + slot], (u / kPreSlots) & 1, flag);
-                tc_fence_after();
-                if (elect_one()) {
+                for (int i = 0; i < 2; ++i) {
+                    const int slot = (u + i) % kPreSlots;
                     const uint64_t v = v_desc + slot * (kPreSlab >> 4);
 #pragma unroll
                     for (int ks = 0; ks < kPreKeys / 16; ++ks)
                         tc_mma_ts(tmem + kPreColO + 128 * x + 64 * i, tmem + kPreColS + 128 * x + 8 * ks,
                                   v + ks * (2048 >> 4), idesc_pv, t > 0 || ks > 0);
                     if (last) tc_commit(&bar[kPreEmpty + slot]);
-                    if (i == 1 && done) tc_commit(&bar[kPreODone + x]);
                 }
-                __syncwarp();
+                if (done) tc_commit(&bar[kPreODone + x]);
             }
+            __syncwarp();
             if (done) ++works[x];
         };
         // the next work that has keys
-        auto next = [&](int turn, int slab) -> Turn {
+        auto next = [&](int turn, int tile) -> Turn {
             for (;; ++turn) {
                 mbar_wait_flow(work_full(turn), (turn / kPreQueue) & 1, flag);
                 const PreWork w = read_work(turn);
-                if (__any_sync(kFullMask, *abort_flag || w.n_q < 0)) return {turn, 0, 0, 0, slab};
+                if (__any_sync(kFullMask, *abort_flag || w.n_q < 0)) return {turn, 0, 0, 0, tile};
                 // by shuffles: values that the compiler knows to be the warp's
                 const int tiles0 = __shfl_sync(kFullMask, prefill_tiles(w, 0, p.causal), 0);
                 const int tiles1 = __shfl_sync(kFullMask, prefill_tiles(w, 1, p.causal), 0);
                 const int most = max(tiles0, tiles1);
-                if (most > 0) return {turn, tiles0, tiles1, most, slab};
+                if (most > 0) return {turn, tiles0, tiles1, most, tile};
                 if (elect_one()) mbar_arrive(work_free(turn));
                 __syncwarp();
             }
@@ -350,7 +378,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             // tile's last P.V, as they need no slab but the two of V beside their own three.
             const int t = w.most - 1;
             if (t < w.tiles0) issue_pv(0, w, t);
-            const Turn n = next(w.turn + 1, w.slab + 5 * w.most);
+            const Turn n = next(w.turn + 1, w.tile + w.most);
             if (n.tiles0 > 0) issue_qk(0, n, 0);
             if (t < w.tiles1) issue_pv(1, w, t);
             if (n.tiles1 > 0) issue_qk(1, n, 0);
@@ -371,7 +399,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         // normal down to 2^-21 of the largest
         constexpr float kLift = BF16 ? 0.f : 7.f;
         const float sc = p.scale_log2;
-        int steps = 0, works = 0, slab = 0;
+        int steps = 0, works = 0, tile = 0;
         for (int turn = 0; ok; ++turn) {
             ok = __all_sync(kFullMask, mbar_wait_or(work_full(turn), (turn / kPreQueue) & 1, abort_flag));
             if (!ok) break;
@@ -380,10 +408,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             const int tiles0 = prefill_tiles(w, 0, p.causal), tiles1 = prefill_tiles(w, 1, p.causal);
             const int tiles = x ? tiles1 : tiles0;
             const int row = w.first + x * kPreRows + r;  // query in the sequence
-            // keys below the limit are met; below `clear` no row of the tile has a masked one
-            const int reach = w.n_k - w.n_q + 1;
-            const int limit = p.causal ? min(reach + row, w.n_k) : w.n_k;
-            const int clear = p.causal ? min(reach + w.first + x * kPreRows, w.n_k) : w.n_k;
+            // keys below the limit are met; all of the warp's rows meet those below `clear`,
+            // none those from `reach` on
+            const int limit = p.causal ? min(w.n_k - w.n_q + 1 + row, w.n_k) : w.n_k;
+            const int clear = __shfl_sync(kFullMask, limit, 0), reach = __shfl_sync(kFullMask, limit, 31);
             float m_run = -INFINITY, l_run = 0.f;
             for (int t = 0; t < tiles; ++t, ++steps) {
                 ok = __all_sync(kFullMask, mbar_wait_or(&bar[kPreSFull + x], steps & 1, abort_flag));
@@ -396,7 +424,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 if (here + kPreKeys > clear) {
                     const float none = sc > 0.f ? -INFINITY : INFINITY;
 #pragma unroll
-                    for (int j = 0; j < kPreKeys; ++j) s[j] = here + j < limit ? s[j] : none;  // NaN-safe
+                    for (int c = 0; c < 4; ++c)
+                        if (here + 32 * c + 32 > clear) {
+#pragma unroll
+                            for (int j = 32 * c; j < 32 * c + 32; ++j)  // NaN-safe select
+                                s[j] = here + j < limit ? s[j] : none;
+                        }
                 }
                 const float mx = (sc > 0.f ? top128<true>(s) : top128<false>(s)) * sc;
                 const bool need = mx > m_run + kLazyRescale;
@@ -422,13 +455,18 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     float o[16];
+                    if (here + 32 * c < reach) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int k = 32 * c + 2 * j;
-                        const float2 y = __ffma2_rn(make_float2(s[k], s[k + 1]), sc2, from2);
-                        const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-                        sum[j & 1] = __fadd2_rn(sum[j & 1], e);
-                        o[j] = __uint_as_float(narrow2<BF16>(e.x, e.y));
+                        for (int j = 0; j < 16; ++j) {
+                            const int k = 32 * c + 2 * j;
+                            const float2 y = __ffma2_rn(make_float2(s[k], s[k + 1]), sc2, from2);
+                            const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                            sum[j & 1] = __fadd2_rn(sum[j & 1], e);
+                            o[j] = __uint_as_float(narrow2<BF16>(e.x, e.y));
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = 0.f;
                     }
                     tmem_store16(s_at + 16 * c, o);
                 }
@@ -437,11 +475,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 if (here + kPreKeys > w.n_k && (x == 0 || t >= tiles0)) {
                     // rows past the sequence's keys: P is 0 there, and V must be finite.  Tile
                     // B's product follows A's, so the first tile to reach them clears them.
+                    const int group = 2 * (tile + t) + 1;
+                    if (!mbar_wait_or(&bar[kPreFull + group % kPreGroups], (group / kPreGroups) & 1, abort_flag))
+                        *abort_flag = 1;  // the next wait for S ends all
                     for (int i = 0; i < 2; ++i) {
-                        const int u = slab + 5 * t + 3 + i;
-                        if (!mbar_wait_or(&bar[kPreFull + u % kPreSlots], (u / kPreSlots) & 1, abort_flag))
-                            *abort_flag = 1;  // the next wait for S ends all
-                        uint4 *z = reinterpret_cast<uint4 *>(smem + kPreOffRing + (u % kPreSlots) * kPreSlab);
+                        const int slot = (5 * (tile + t) + 3 + i) % kPreSlots;
+                        uint4 *z = reinterpret_cast<uint4 *>(smem + kPreOffRing + slot * kPreSlab);
                         for (int k = (w.n_k - here) * 8 + r; k < kPreKeys * 8; k += 128)
                             z[k] = make_uint4(0, 0, 0, 0);
                     }
@@ -456,24 +495,16 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const float inv = l_run > 0.f ? 1.f / l_run : l_run == 0.f ? 0.f : l_run;
-            uint4 *to = reinterpret_cast<uint4 *>(
-                p.out + ((int64_t)(w.q0 + row) * p.num_heads + w.head) * kPreValue);
-#pragma unroll 1
+            uint16_t *to = p.out + ((int64_t)(w.q0 + row) * p.num_heads + w.head) * kPreValue;
+            // O into registers first: the next work's products may take its place
+            uint32_t y[kPreValue / 2];
+#pragma unroll
             for (int c = 0; c < 4; ++c) {
                 float o[32];
+                tmem_ld32(o_at + 32 * c, o);  // (nothing of use where no key was met)
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = 0.f;
-                if (tiles > 0) tmem_ld32(o_at + 32 * c, o);
-                if (row < w.n_q) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = l_run == 0.f ? 0.f : o[i] * inv;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        to[4 * c + i] = make_uint4(narrow2<BF16>(o[8 * i], o[8 * i + 1]),
-                                                   narrow2<BF16>(o[8 * i + 2], o[8 * i + 3]),
-                                                   narrow2<BF16>(o[8 * i + 4], o[8 * i + 5]),
-                                                   narrow2<BF16>(o[8 * i + 6], o[8 * i + 7]));
-                }
+                for (int i = 0; i < 16; ++i)
+                    y[16 * c + i] = l_run == 0.f ? 0u : narrow2<BF16>(o[2 * i] * inv, o[2 * i + 1] * inv);
             }
             tc_fence_before();
             __syncwarp();
@@ -481,8 +512,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 if (tiles > 0) mbar_arrive(&bar[kPreOFree + x]);
                 mbar_arrive(work_free(turn));
             }
+            if (row < w.n_q) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) store32(to + 16 * c, y + 8 * c, p.wide);
+            }
             works += tiles > 0;
-            slab += 5 * max(tiles0, tiles1);
+            tile += max(tiles0, tiles1);
         }
     }
     if (!ok) *abort_flag = 1;
@@ -530,6 +565,7 @@ extern "C" pa_status pa_prefill_latent(
     p.max_q = max_q_len;
     p.num_heads = num_heads;
     p.causal = causal != 0;
+    p.wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
     p.scale_log2 = latent_scale(scale);
     const bool bf16 = dtype == PA_BF16;
     // without keys no map of theirs is used: q stands in

@@ -119,7 +119,7 @@ __device__ __forceinline__ int latent_tiles(int len) {
 }
 
 // The pieces of a range, in order: every role walks them by itself, the next
-// sequence's length on its way meanwhile.
+// sequence's length on its way meanwhile; by whole warps.
 struct LatWalk {
     const DecodeLatentParams &p;
     int seq, tile, left;
@@ -130,7 +130,9 @@ struct LatWalk {
         : p(prm), seq(s), tile(t), left(l), ahead(s < prm.num_seqs ? prm.lens[s] : 0) {}
     __device__ __forceinline__ bool next() {  // the current piece's data, false at the end
         if (left <= 0 || seq >= p.num_seqs) return false;
-        len = latent_len(p, ahead, false);
+        // (a shuffle's result is known to be the warp's: what follows from it stays in
+        // uniform registers)
+        len = __shfl_sync(kFullMask, latent_len(p, ahead, false), 0);
         if (seq + 1 < p.num_seqs) ahead = p.lens[seq + 1];
         n = latent_tiles(len) - tile;
         more = n > left;
@@ -270,7 +272,9 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     const uint32_t tmem = *tmem_slot;
     pdl_trigger();  // the joining launch waits for this one's end by itself
 
-    LatWalk walk(p, seq0, tile0, left);
+    seq0 = __shfl_sync(kFullMask, seq0, 0);
+    tile0 = __shfl_sync(kFullMask, tile0, 0);
+    LatWalk walk(p, seq0, tile0, __shfl_sync(kFullMask, left, 0));
     bool ok = true;
 
     if (warp == 0) {
@@ -416,21 +420,23 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         __syncwarp();
     } else if (warp == 11) {
         // ---------------------------------------------------------- Q
-        if (lane == 0) {
-            int piece = 0;
-            for (; ok && walk.next(); walk.advance()) {
-                if (walk.len == 0) continue;
-                if (piece > 0) ok = mbar_wait_or(&bar[S::Q_FREE], (piece - 1) & 1, abort_flag);
-                if (!ok) break;
+        int piece = 0;
+        for (; ok && walk.next(); walk.advance()) {
+            if (walk.len == 0) continue;
+            if (piece > 0) ok = mbar_wait_or(&bar[S::Q_FREE], (piece - 1) & 1, abort_flag);
+            ok = __all_sync(kFullMask, ok);
+            if (!ok) break;
+            if (elect_one()) {
                 mbar_arrive_expect_tx(&bar[S::Q_FULL], S::SLABS * S::Q_SLAB);
                 // rows past the last sequence read as zero, other heads' rows as they are
                 for (int i = 0; i < S::SLABS; ++i)
                     tma_load_2d(smem + S::OFF_Q + i * S::Q_SLAB, &map_q, 64 * i,
                                 walk.seq * p.num_heads + group * NH, &bar[S::Q_FULL]);
-                ++piece;
             }
-            if (piece > 0) (void)mbar_wait(&bar[S::Q_FULL], (piece - 1) & 1);
+            __syncwarp();
+            ++piece;
         }
+        if (piece > 0) (void)mbar_wait(&bar[S::Q_FULL], (piece - 1) & 1);
         __syncwarp();
     } else {
         // ---------------------------------------------------------- softmax / epilogue

@@ -593,6 +593,8 @@ def _steps(t, name):
     second token or head needs is given as that of a dense tensor."""
     T, heads, width = t.shape
     token, head, one = t.stride()
+    if one == 1 and T > 1 and heads > 1 and token >= width and head >= width and not (token | head) & 7:
+        return token, head
     if heads <= 1:
         head = width
     if T <= 1:
@@ -627,7 +629,8 @@ def latent_norm_rope(q_out, q, latent, weight, eps, cos_sin, positions, slot_map
         raise ValueError(f"latent must be [T, {rank + LATENT_ROPE}]")
     if weight.shape != (rank,) or positions.shape != (T,) or slot_mapping.shape != (T,):
         raise ValueError("weight must be [rank], positions and slot_mapping [T]")
-    if cos_sin.dim() != 2 or cos_sin.shape[1] != LATENT_ROPE:
+    table = cos_sin.shape
+    if len(table) != 2 or table[1] != LATENT_ROPE:
         raise ValueError(f"cos_sin must be [positions, {LATENT_ROPE}]")
     if rows_out is not None and (rows_out.shape != ls or rows_out.dtype is not dt):
         raise ValueError("rows_out must be like latent")
@@ -655,7 +658,7 @@ def latent_norm_rope(q_out, q, latent, weight, eps, cos_sin, positions, slot_map
     rc = _run(dev, stream, _lib.load().pa_latent_norm_rope,
               (q_out.data_ptr(), *_steps(q_out, "q_out"), q.data_ptr(), *_steps(q, "q"),
                latent.data_ptr(), step, weight.data_ptr(), float(eps), cos_sin.data_ptr(),
-               cos_sin.shape[0], 1 if interleaved else 0, positions.data_ptr(),
+               table[0], 1 if interleaved else 0, positions.data_ptr(),
                slot_mapping.data_ptr(), T, None if rows_out is None else rows_out.data_ptr(),
                pool.data_ptr(), nb, heads, rank, bs, code))
     _check("pa_latent_norm_rope", rc, q_out=q_out, q=q, latent=latent, weight=weight,

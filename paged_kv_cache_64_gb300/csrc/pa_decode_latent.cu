@@ -52,6 +52,7 @@ constexpr int kLatThreads = kLatWarps * 32;
 constexpr int kLatSmem = 232448;  // what a CTA may have
 constexpr int kLatMisc = 2048;    // barriers and exchange
 constexpr int kLatMinTiles = 4;   // tiles of a range, at least
+constexpr int kLatMaxLen = 1 << 24;
 constexpr int kLatWhole = 8;      // up to so many tiles a sequence is never cut
 
 struct DecodeLatentParams {
@@ -875,6 +876,10 @@ extern "C" pa_status pa_decode_latent(void *out, const void *q, const void *pool
     if ((int64_t)num_blocks * block_size >= 1ll << 31 ||
         (int64_t)max_blocks_per_seq * block_size >= 1ll << 31 ||
         ((int64_t)max_seq_len / kLatTile + 1) * num_seqs >= 1ll << 31)
+        return PA_ERR_INVALID;
+    // a CTA may have a whole sequence, and its next queries wait for the end of it: well
+    // within the limit of a wait (64 positions take about 1.7 us)
+    if (max_seq_len > kLatMaxLen && (int64_t)max_blocks_per_seq * block_size > kLatMaxLen)
         return PA_ERR_INVALID;
     if (num_seqs == 0) return PA_OK;
     const void *ptrs[] = {out, q, pool};

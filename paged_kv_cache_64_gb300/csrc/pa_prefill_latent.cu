@@ -53,6 +53,9 @@ constexpr int kPreColS = 0, kPreColO = 256;        // TMEM columns: S_A S_B O_A 
 // 16 heads of 16,600 tokens 122 us the first way, 132 the other; 32 heads of 6,000
 // tokens behind 24,000 1,049 and 911.
 constexpr int kPreByLength = 400000;
+// 256 queries meet 2^24 keys in about 0.3 s; the fetching warp waits for three such
+// pieces of work at most, which a wait's limit has to cover.
+constexpr int kPreMaxKeys = 1 << 24;
 constexpr int kPreQueue = 3;                       // work in hand: being done and fetched
 static_assert(kPreSmem <= 232448, "shared memory");
 
@@ -549,7 +552,7 @@ extern "C" pa_status pa_prefill_latent(
     const int32_t *k_starts, int num_seqs, int total_q, int total_k, int max_q_len, int num_heads,
     float scale, int causal, pa_dtype dtype, void *stream) {
     if (num_seqs < 0 || total_q < 0 || total_k < 0 || max_q_len < 0 || num_heads <= 0 ||
-        num_heads > 1024 || num_seqs > 65535 || !std::isfinite(scale) ||
+        num_heads > 1024 || num_seqs > 65535 || total_k > kPreMaxKeys || !std::isfinite(scale) ||
         (dtype != PA_F16 && dtype != PA_BF16))
         return PA_ERR_INVALID;
     const int64_t steps[] = {q_token_stride, q_head_stride, k_token_stride, k_head_stride,

@@ -238,6 +238,70 @@ def test_decode_minus_infinite_key():
     check(out, ref, bound)
 
 
+@BOTH
+@pytest.mark.parametrize("scale", [0.0, -0.1, 1e-20])
+def test_attention_of_unusual_scales(dtype, scale):
+    """No scale (the mean of the values) and negative ones, masked positions among the tiles."""
+    case = Decode(np.random.default_rng(19), dtype, [77, 200, 64], 20, 256, 16)
+    case.scale = scale
+    run_decode(case)
+    case = Prefill(np.random.default_rng(20), dtype, [150, 7], [200, 7], 2, True)
+    case.scale = scale
+    run_prefill(case)
+
+
+def test_decode_more_heads_than_two_groups():
+    run_decode(Decode(np.random.default_rng(21), "bf16", [300, 5, 0, 64], 300, 256, 32))
+
+
+def test_decode_rows_far_into_a_large_pool():
+    """Rows whose elements lie past 2^32 (written, read back and attended)."""
+    rng = np.random.default_rng(22)
+    case = Decode(rng, "bf16", [150, 40], 3, 512, 64, poison=False, spare=0)
+    blocks = (1 << 32) // (64 * 576) + 20
+    pool = torch.empty(blocks, 64, 576, dtype=torch.bfloat16, device="cuda")
+    far = blocks - len(case.pool)
+    pool[far:] = dev(case.pool, "bf16")
+    g = case.gpu()
+    g["block_tables"] = g["block_tables"] + far
+    ref, bound = case.reference()
+    out = case.empty()
+    api.decode_latent(out, **{**g, "pool": pool})
+    api.check_error()
+    check(out, ref, bound)
+    slots = torch.tensor([blocks * 64 - 1, 5, far * 64 + 3], device="cuda")
+    rows = torch.empty(3, 576, dtype=torch.bfloat16, device="cuda")
+    r = Rows(rng, "bf16", 3, 2, 512, 64).gpu()
+    api.latent_norm_rope(torch.empty(3, 2, 64, dtype=torch.bfloat16, device="cuda"),
+                         **{**r, "pool": pool, "slot_mapping": slots}, rows_out=rows)
+    again = torch.empty_like(rows)
+    api.cache_read_latent(again, slots, pool)
+    api.check_error()
+    assert torch.equal(rows, again)
+
+
+def test_decode_a_head_of_nan_stays_alone():
+    """A query head of NaN spoils its own outputs only."""
+    case = Decode(np.random.default_rng(23), "bf16", [500, 70], 9, 256, 16)
+    ref, bound = case.reference()
+    g, out = case.gpu(), case.empty()
+    g["q"][0, 4] = float("nan")
+    api.decode_latent(out, **g)
+    api.check_error()
+    assert torch.isnan(out[0, 4]).all()
+    rest = [h for h in range(9) if h != 4]
+    check(out[0, rest], ref[0, rest], bound[0, rest])
+    check(out[1], ref[1], bound[1])
+
+
+def test_decode_shared_and_repeated_blocks():
+    """Sequences that share blocks, and one that names a block twice."""
+    case = Decode(np.random.default_rng(24), "f16", [160, 96, 64], 6, 512, 32, poison=False)
+    case.tables[1, :2] = case.tables[0, :2]
+    case.tables[2, 1] = case.tables[2, 0]
+    run_decode(case)
+
+
 def test_decode_empty_batches():
     g = Decode(np.random.default_rng(15), "bf16", [3, 5], 8, 256, 16).gpu()
     out = torch.full((2, 8, 256), 5.0, device="cuda", dtype=torch.bfloat16)
@@ -410,6 +474,57 @@ def test_prefill_bad_starts():
         api.check_error()
     assert (out[int(s[2]):] == 7.0).all()
     check(out[int(s[0]):int(s[2])], ref[s[0]:s[2]], bound[s[0]:s[2]])
+
+
+def test_prefill_many_short_prompts():
+    rng = np.random.default_rng(10)
+    n_q = rng.integers(0, 4, 3000)
+    run_prefill(Prefill(rng, "bf16", n_q, n_q + rng.integers(0, 3, 3000), 2, True))
+
+
+def test_prefill_output_off_a_32_byte_boundary():
+    case = Prefill(np.random.default_rng(11), "bf16", [300], [300], 3, True)
+    n = case.empty().numel()
+    out = torch.full((n + 8,), 7.0, dtype=torch.bfloat16, device="cuda")[8:].view(-1, 3, 128)
+    assert out.data_ptr() % 32 == 16
+    api.prefill_latent(out, **case.gpu())
+    api.check_error()
+    case.check(out)
+
+
+@pytest.mark.parametrize("heads,n_q,n_k", [(70, 300, 6100), (1, 9000, 9000)])
+def test_prefill_orders_of_work(heads, n_q, n_k):
+    """More (key, head) pairs than the order by length takes; more queries than one wave."""
+    rng = np.random.default_rng(heads)
+    case = Prefill(rng, "bf16", [n_q], [n_k], heads, True)
+    out = case.empty()
+    api.prefill_latent(out, **case.gpu())
+    api.check_error()
+    pick = np.unique(np.concatenate([rng.integers(0, n_q, 40), [0, n_q - 1]]))
+    for h in (0, heads - 1):  # some rows of two heads
+        for i in pick:
+            last = n_k - n_q + i + 1
+            a, b = int(case.q_starts[0] + i), int(case.k_starts[0])
+            ref, size, terms = latent.prefill(
+                case.q[a:a + 1, h:h + 1], case.kv[b:b + last, h:h + 1, :128],
+                case.kv[b:b + last, h:h + 1, 128:], case.rows[b:b + last, 256:], np.array([0, 1]),
+                np.array([0, last]), case.scale, True, "bf16")
+            check(out[a:a + 1, h:h + 1], ref, attention_bound(ref, size, terms, "bf16", last, 192, 0.0))
+
+
+def test_prefill_on_two_streams_at_once():
+    cases = [Prefill(np.random.default_rng(12 + i), "f16", [500, 40 + i], [700, 90], 4, True)
+             for i in range(2)]
+    gs, outs = [c.gpu() for c in cases], [c.empty() for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(5):
+        for g, out, stream in zip(gs, outs, streams):
+            api.prefill_latent(out, **g, stream=stream)
+    torch.cuda.synchronize()
+    api.check_error()
+    for c, out in zip(cases, outs):
+        c.check(out)
 
 
 def test_prefill_in_a_graph():

@@ -67,7 +67,8 @@ def test_decode_refusals(lib):
     for kw in (dict(S=-1), dict(S=65536), dict(nb=0), dict(mb=0), dict(max_len=-1), dict(heads=0),
                dict(heads=1025), dict(scale=float("inf")), dict(dt=2), dict(out=NULL), dict(q=ODD),
                dict(pool=ODD), dict(tables=NULL), dict(lens=NULL), dict(nb=1 << 27),
-               dict(mb=1 << 27)):
+               dict(mb=1 << 27), dict(mb=1 << 21, max_len=(1 << 24) + 1),
+               dict(S=65535, max_len=1 << 24, mb=1 << 20)):
         assert decode(lib, **kw) == INVALID, kw
     for kw in (dict(rank=128), dict(bs=8)):
         assert decode(lib, **kw) == UNSUPPORTED, kw
@@ -78,7 +79,8 @@ def test_prefill_refusals(lib):
     for kw in (dict(S=-1), dict(S=65536), dict(tq=-1), dict(tk=-1), dict(mq=-1), dict(heads=0),
                dict(heads=1025), dict(scale=float("nan")), dict(dt=3), dict(qt=184), dict(qh=190),
                dict(kt=120), dict(kh=129), dict(vh=64), dict(pt=32), dict(vt=1 << 39), dict(out=NULL),
-               dict(q=ODD), dict(k=NULL), dict(v=ODD), dict(pe=ODD), dict(qs=NULL), dict(ks=NULL)):
+               dict(q=ODD), dict(k=NULL), dict(v=ODD), dict(pe=ODD), dict(qs=NULL), dict(ks=NULL),
+               dict(tk=(1 << 24) + 1)):
         assert prefill(lib, **kw) == INVALID, kw
     for kw in (dict(S=0), dict(tq=0), dict(mq=0)):
         assert prefill(lib, **kw) == 0, kw

@@ -30,7 +30,7 @@
 //
 // The batch's tiles are shared out evenly: range b of the launch is tiles
 // [b per, (b + 1) per) of all sequences' tiles in a row, found from the lengths on
-// the device.  A CTA goes through its range's pieces of sequences; Q and the rows
+// the device, or sequence b where they are about even.  A CTA goes through its range's pieces of sequences; Q and the rows
 // of the next piece are on their way while one ends.  A piece that is a whole
 // sequence is written out; the others leave (m, l, O) and a second launch joins
 // them.
@@ -51,9 +51,14 @@ constexpr int kLatAhead = 2;      // tiles from a copy to the prefetch to L2 beh
 constexpr int kLatThreads = kLatWarps * 32;
 constexpr int kLatSmem = 232448;  // what a CTA may have
 constexpr int kLatMisc = 2048;    // barriers and exchange
-constexpr int kLatMinTiles = 4;   // tiles of a range, at least
 constexpr int kLatMaxLen = 1 << 24;
-constexpr int kLatWhole = 8;      // up to so many tiles a sequence is never cut
+// Sequences are not cut where each has a range of its own and the longest is at most
+// this many tiles above an even share: cutting costs a range the write of its partial
+// results and all the joining launch.  Cut against whole, in us, of sequences of 8
+// tiles: 4 of 64 heads (a share of 1 tile) 13.4 and 17.3, 20 (2) 16.3 and 17.4, 70 (4)
+// 27.8 and 19.4, 64 of 128 heads (7) 33.7 and 21.8; of 12 tiles: 60 of 16 heads (5)
+// 21.5 and 22.3, 140 (12) 33.2 and 27.3.
+constexpr int kLatWhole = 5;
 
 struct DecodeLatentParams {
     uint16_t *out;
@@ -65,7 +70,7 @@ struct DecodeLatentParams {
     int4 *plan;      // [ranges]: sequence whose pieces begin in the range and go on, or -1
     int num_blocks, max_blocks, max_len, num_seqs, num_heads, log2_block;
     int ranges, groups;
-    int whole;       // range b is sequence b
+    int whole;       // range b is sequence b, whatever the lengths
     float scale_log2;
     int *err;
 };
@@ -217,26 +222,36 @@ __global__ void __launch_bounds__(kLatThreads, 1)
 
     // ---------------------------------------------------------- this CTA's range
     int seq0 = range, tile0 = 0, left;
-    if (p.whole) {
+    if (p.whole) {  // no sequence can be long enough to be cut
         left = latent_tiles(latent_len(p, p.lens[range], group == 0));
         tc_fence_before();
         __syncthreads();
     } else {
-        int sum = 0;
-        for (int i = threadIdx.x; i < p.num_seqs; i += kLatThreads)
-            sum += latent_tiles(latent_len(p, p.lens[i], blockIdx.x == 0));
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
-        if (lane == 0) scan[warp] = sum;
+        int sum = 0, longest = 0, *longest_of = words + 32;
+        for (int i = threadIdx.x; i < p.num_seqs; i += kLatThreads) {
+            const int n = latent_tiles(latent_len(p, p.lens[i], blockIdx.x == 0));
+            sum += n;
+            longest = max(longest, n);
+        }
+        sum = __reduce_add_sync(kFullMask, sum);
+        longest = __reduce_max_sync(kFullMask, longest);
+        if (lane == 0) {
+            scan[warp] = sum;
+            longest_of[warp] = longest;
+        }
         tc_fence_before();
         __syncthreads();
         int total = 0;
+        longest = 0;
 #pragma unroll
-        for (int w = 0; w < kLatWarps; ++w) total += scan[w];
-        int per = (total + p.ranges - 1) / p.ranges;
-        if (per < kLatMinTiles) per = kLatMinTiles;
+        for (int w = 0; w < kLatWarps; ++w) {
+            total += scan[w];
+            longest = max(longest, longest_of[w]);
+        }
+        const int per = (total + p.ranges - 1) / p.ranges;
+        const bool whole = p.num_seqs <= p.ranges && longest <= per + kLatWhole;
         const int start = (int)min((int64_t)range * per, (int64_t)total);
-        left = min(per, total - start);
+        left = whole ? 0 : min(per, total - start);
         // the sequence and tile that the range begins with
         int before = 0;
         for (int base = 0; base < p.num_seqs && left > 0; base += kLatThreads) {
@@ -268,6 +283,10 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         __syncthreads();
         seq0 = scan[kLatWarps];
         tile0 = scan[kLatWarps + 1];
+        if (whole && range < p.num_seqs) {
+            seq0 = range;
+            left = latent_tiles(latent_len(p, p.lens[range], false));
+        }
     }
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
@@ -819,7 +838,7 @@ static LatentLaunch latent_launch(int num_seqs, int num_heads, int rank, int max
     c.ranges = sms / c.groups > 0 ? sms / c.groups : 1;
     if (c.ranges > kLatMaxRanges) c.ranges = kLatMaxRanges;
     const int tiles = (max_seq_len + kLatTile - 1) / kLatTile;
-    c.whole = num_seqs <= c.ranges && tiles <= kLatWhole;
+    c.whole = num_seqs <= c.ranges && tiles <= kLatWhole + 1;  // an even share is a tile at least
     if (c.whole) c.ranges = num_seqs;
     const size_t pieces = (size_t)c.ranges * c.groups * 2 * c.nh;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };

@@ -27,9 +27,13 @@
 // sequence; a CTA that runs takes over blocks that have not been launched yet
 // (clusterlaunchcontrol), so the next work's queries and keys load, and its first
 // products run, while the softmax of the last ends.  Blocks past a sequence's end
-// cost the fetching warp a look at its lengths.
+// cost the fetching warp a look at its lengths.  Where there are few blocks and many
+// keys, a cluster shares a block's keys instead and joins its sums through distributed
+// shared memory.
 #include <cmath>
 #include <cstdint>
+#include <map>
+#include <mutex>
 
 #include "pa_decode.cuh"
 #include "pa_internal.h"
@@ -56,6 +60,12 @@ constexpr int kPreByLength = 400000;
 // 256 queries meet 2^24 keys in about 0.3 s; the fetching warp waits for three such
 // pieces of work at most, which a wait's limit has to cover.
 constexpr int kPreMaxKeys = 1 << 24;
+// A work's keys are shared out over up to eight CTAs, at least kPreSplitTiles tiles
+// each, as far as one wave holds them (1 query behind 8,000 keys, 4 heads: 89 us whole,
+// 23 with eight; 300 behind 6,000 twice, 8 heads: 72 and 31 with four), and over two
+// where there is about a wave of work and sequences are long enough to even it out
+// (16,000 tokens, 2 heads: 214 and 118; 4,096 tokens, 8 heads: 61 and 70).
+constexpr int kPreMaxSplit = 8, kPreSplitTiles = 4, kPreSplitLong = 64;
 constexpr int kPreQueue = 3;                       // work in hand: being done and fetched
 static_assert(kPreSmem <= 232448, "shared memory");
 
@@ -77,6 +87,7 @@ static_assert(kPreBars * 8 <= 512 && kPreOffWords + 8 <= kPreOffBar + 1024, "bar
 struct PreWork {
     int q0, n_q, k0, n_k;  // the sequence's tokens; n_q < 0: no more work
     int head, first;       // first query in the sequence
+    int from, upto;        // key tiles
 };
 
 struct PrefillLatentParams {
@@ -84,17 +95,19 @@ struct PrefillLatentParams {
     const int32_t *q_starts, *k_starts;
     int total_q, total_k, max_q, num_heads, causal;
     int wide;       // out lies on a 32-byte boundary
+    int split;      // CTAs of a cluster that share a work's keys
     int by_length;  // grid (heads, sequences, tiles) instead of (tiles, heads, sequences)
     float scale_log2;
     int *err;
 };
 
-// Keys that rows [first + 128 x, + 128) of a sequence meet, in tiles.
+// Keys that rows [first + 128 x, + 128) of a sequence meet, in tiles of the work's.
 __device__ __forceinline__ int prefill_tiles(const PreWork &w, int x, int causal) {
     const int a = w.first + x * kPreRows, b = min(a + kPreRows, w.n_q);
     if (a >= w.n_q) return 0;
     const int keys = causal ? min(w.n_k - w.n_q + b, w.n_k) : w.n_k;
-    return keys > 0 ? (keys + kPreKeys - 1) / kPreKeys : 0;
+    const int end = keys > 0 ? (keys + kPreKeys - 1) / kPreKeys : 0;
+    return max(min(end, w.upto) - w.from, 0);
 }
 
 // Largest (MAX) or smallest of 128 values, NaN left aside.
@@ -122,7 +135,79 @@ __device__ __forceinline__ void store32(uint16_t *to, const uint32_t *y, int wid
     }
 }
 
+// The CTAs of a cluster have had shares of one work's keys: their sums meet through
+// distributed shared memory.  M = max m_c, out = sum 2^(m_c - M) O_c / sum 2^(m_c - M) l_c.
+// Each CTA weighs its O rows and sends them to the CTA that owns the row, which adds
+// them up.  Every product and copy has ended, so the shared memory is free: the rows'
+// slots lie first in it, [tile][sender][owned row][128 + 4].
 template <bool BF16>
+__device__ __forceinline__ void prefill_join(const PrefillLatentParams &p, const PreWork &w, uint8_t *smem,
+                                          uint32_t tmem, int warp, int lane, float m_run, float l_run) {
+    constexpr int kStep = kPreValue + 4;
+    constexpr int kSlots = 2 * kPreRows;  // C senders of 128 / C rows of either tile
+    static_assert(kSlots * (kStep + 1) * 4 + 2 * kPreRows * 8 <= kPreOffBar, "shared memory");
+    float *slots = reinterpret_cast<float *>(smem);
+    float2 *ml = reinterpret_cast<float2 *>(slots + kSlots * kStep);  // [tile][row]
+    float *weights = reinterpret_cast<float *>(ml + 2 * kPreRows);          // [tile][owned row][sender]
+    const int C = p.split, R = kPreRows / C, rank = (int)cluster_ctarank();
+    const bool softmax = warp >= 2 && warp < 10;
+    const int x = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane;
+    if (softmax) ml[x * kPreRows + r] = make_float2(l_run == 0.f ? -INFINITY : m_run, l_run);
+    __syncwarp();
+    cluster_sync();
+    if (softmax) {
+        float M = -INFINITY, L = 0.f, own = 0.f;
+        const uint32_t at = smem_addr(ml + x * kPreRows + r);
+        for (int c = 0; c < C; ++c) M = fmaxf(M, ld_cluster_f32(map_cluster(at, c)));
+        auto factor = [&](int c) -> float {
+            const float m = ld_cluster_f32(map_cluster(at, c));
+            return m == -INFINITY ? 0.f : fast_exp2(m - M);
+        };
+        for (int c = 0; c < C; ++c) L += factor(c) * ld_cluster_f32(map_cluster(at + 4, c));
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const int owner = r / R, slot = r % R;
+        for (int c = 0; c < C; ++c) {
+            const float f = factor(c) * inv;
+            if (c == rank) own = f;
+            if (owner == rank) weights[(x * R + slot) * C + c] = f;
+        }
+        const uint32_t to = map_cluster(smem_addr(slots + ((x * C + rank) * R + slot) * kStep), owner);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+            float o[32];
+            tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + kPreColO + 128 * x + 32 * c, o);
+            if (own != 0.f) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    st_cluster_f4(to + (32 * c + 4 * i) * 4,
+                                  make_float4(o[4 * i] * own, o[4 * i + 1] * own, o[4 * i + 2] * own,
+                                              o[4 * i + 3] * own));
+            }
+        }
+    }
+    __syncwarp();
+    cluster_sync();
+    if (softmax) {
+        for (int i = r; i < R * (kPreValue / 8); i += kPreRows) {
+            const int slot = i / (kPreValue / 8), d = i % (kPreValue / 8) * 8;
+            const int row = w.first + x * kPreRows + rank * R + slot;
+            if (row >= w.n_q) continue;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+            for (int c = 0; c < C; ++c) {
+                if (weights[(x * R + slot) * C + c] == 0.f) continue;  // nothing was sent
+                const float4 *v = reinterpret_cast<const float4 *>(slots + ((x * C + c) * R + slot) * kStep + d);
+                a.x += v[0].x, a.y += v[0].y, a.z += v[0].z, a.w += v[0].w;
+                b.x += v[1].x, b.y += v[1].y, b.z += v[1].z, b.w += v[1].w;
+            }
+            *reinterpret_cast<uint4 *>(p.out + ((int64_t)(w.q0 + row) * p.num_heads + w.head) * kPreValue + d) =
+                make_uint4(narrow2<BF16>(a.x, a.y), narrow2<BF16>(a.z, a.w), narrow2<BF16>(b.x, b.y),
+                           narrow2<BF16>(b.z, b.w));
+        }
+    }
+}
+
+// SPLIT: the CTAs of a cluster share one block's keys, and take over no others.
+template <bool BF16, bool SPLIT>
 __global__ void __launch_bounds__(kPreThreads, 1)
     prefill_latent_kernel(const __grid_constant__ PrefillLatentParams p,
                           const __grid_constant__ CUtensorMap map_q,
@@ -139,6 +224,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     volatile int *abort_flag = flag;
 
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
+    const int split = SPLIT ? p.split : 1;
     if (threadIdx.x == 0) {
         prefetch_tensormap(&map_q);
         prefetch_tensormap(&map_k);
@@ -163,10 +249,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     pdl_wait();
     pdl_trigger();
     bool ok = true;
+    float m_of = -INFINITY, l_of = 0.f;  // a softmax thread's row, for the cluster
     // The work of turn i, once it is there (roles take it in turns 0, 1, ...).
     auto read_work = [&](int turn) -> PreWork {
         const int4 a = queue[2 * (turn % kPreQueue)], b = queue[2 * (turn % kPreQueue) + 1];
-        return {a.x, a.y, a.z, a.w, b.x, b.y};
+        return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     };
     auto work_full = [&](int turn) -> uint64_t * { return &bar[kPreWorkFull + turn % kPreQueue]; };
     auto work_free = [&](int turn) -> uint64_t * { return &bar[kPreWorkFree + turn % kPreQueue]; };
@@ -174,7 +261,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     if (warp == 10) {
         // ---------------------------------------------------------- next work
         if (lane == 0) {
-            int x = blockIdx.x, y = blockIdx.y, z = blockIdx.z, claims = 0;
+            int x = blockIdx.x / split, y = blockIdx.y, z = blockIdx.z, claims = 0;
             // a block that has not been launched yet becomes this CTA's; false: none is left
             auto claim = [&]() -> bool {
                 const uint32_t answer = smem_addr(smem + kPreOffClaim);
@@ -212,12 +299,13 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 }
                 PreWork w;
                 for (;;) {
-                    w = {0, -1, 0, 0, 0, 0};
-                    if (!have && !claim()) break;
+                    w = {0, -1, 0, 0, 0, 0, 0, 0x7fffffff};
+                    if (!have && (SPLIT || !claim())) break;
                     have = false;
                     // the longest tiles of causal sequences come first: of each head in turn,
                     // or of all
-                    const int seq = p.by_length ? y : z, last = (p.by_length ? gridDim.z : gridDim.x) - 1;
+                    const int seq = p.by_length ? y : z;
+                    const int last = (p.by_length ? gridDim.z : gridDim.x / split) - 1;
                     w.first = (last - (p.by_length ? z : x)) * 2 * kPreRows;
                     w.head = p.by_length ? x : y;
                     w.q0 = p.q_starts[seq];
@@ -229,11 +317,17 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                     if (good && w.first < q1 - w.q0) {
                         w.n_q = q1 - w.q0;
                         w.n_k = k1 - w.k0;
+                        if constexpr (SPLIT) {  // this CTA's share of the keys
+                            const int all = max(prefill_tiles(w, 0, p.causal), prefill_tiles(w, 1, p.causal));
+                            const int per = (all + split - 1) / split;
+                            w.from = per * (int)cluster_ctarank();
+                            w.upto = w.from + per;
+                        }
                         break;
                     }
                 }
                 queue[2 * (turn % kPreQueue)] = make_int4(w.q0, w.n_q, w.k0, w.n_k);
-                queue[2 * (turn % kPreQueue) + 1] = make_int4(w.head, w.first, 0, 0);
+                queue[2 * (turn % kPreQueue) + 1] = make_int4(w.head, w.first, w.from, w.upto);
                 mbar_arrive(work_full(turn));
                 if (w.n_q < 0) break;
             }
@@ -281,9 +375,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                     return true;
                 };
                 if (tiles0 > 0) ok = load_q(0, loaded[0]);
-                for (int key = w.k0; ok && u < end; key += kPreKeys)
+                const int key0 = w.k0 + w.from * kPreKeys;
+                for (int key = key0; ok && u < end; key += kPreKeys)
                     for (int i = 0; ok && i < 5; ++i) {
-                        if (i == 3 && key == w.k0 && tiles1 > 0) ok = load_q(1, loaded[1]);
+                        if (i == 3 && key == key0 && tiles1 > 0) ok = load_q(1, loaded[1]);
                         ok = ok && load(i, key);
                     }
                 mbar_arrive(work_free(turn));
@@ -431,7 +526,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 float s[kPreKeys];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, s + 32 * c);
-                const int here = t * kPreKeys;
+                const int here = (w.from + t) * kPreKeys;
                 if (here + kPreKeys > clear) {
                     const float none = sc > 0.f ? -INFINITY : INFINITY;
 #pragma unroll
@@ -505,6 +600,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 ok = __all_sync(kFullMask, mbar_wait_or(&bar[kPreODone + x], works & 1, abort_flag));
             if (!ok) break;
             tc_fence_after();
+            if constexpr (SPLIT) {  // one piece of work, joined below
+                m_of = m_run;
+                l_of = l_run;
+                break;
+            }
             const float inv = l_run > 0.f ? 1.f / l_run : l_run == 0.f ? 0.f : l_run;
             uint16_t *to = p.out + ((int64_t)(w.q0 + row) * p.num_heads + w.head) * kPreValue;
             // O into registers first: the next work's products may take its place
@@ -535,10 +635,48 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *abort_flag) record_error(p.err, PA_ERR_DEVICE_TIMEOUT);
+    if constexpr (SPLIT) {
+        tc_fence_after();
+        const PreWork w = read_work(0);
+        if (w.n_q >= 0)  // the same for the cluster
+            prefill_join<BF16>(p, w, smem, tmem, warp, lane, m_of, l_of);
+        tc_fence_before();
+        __syncthreads();
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+}
+
+// Clusters of c CTAs that the current device holds at once (0 if the query fails),
+// kept by type, size and device.
+static int prefill_clusters(bool bf16, int c) {
+    static std::mutex mu;
+    static std::map<int, int> known;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    const int key = (dev * 16 + c) * 2 + bf16;
+    const auto it = known.find(key);
+    if (it != known.end()) return it->second;
+    const void *kern = bf16 ? reinterpret_cast<const void *>(prefill_latent_kernel<true, true>)
+                            : reinterpret_cast<const void *>(prefill_latent_kernel<false, true>);
+    if (!ensure_smem_attr(kern, kPreSmem)) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)c);
+    cfg.blockDim = dim3(kPreThreads);
+    cfg.dynamicSmemBytes = kPreSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
+    known[key] = n;
+    return n;
 }
 
 }  // namespace pa
@@ -595,14 +733,34 @@ extern "C" pa_status pa_prefill_latent(
                      map3(&map_v, q, kPreValue, total_q, q_token_stride, q_head_stride)) ||
         !boxed_tensor_map(&map_pe, keys ? k_pe : q, 2, pe_dims, pe_step, box, bf16))
         return PA_ERR_CUDA;
-    auto kern = bf16 ? prefill_latent_kernel<true> : prefill_latent_kernel<false>;
-    if (!ensure_smem_attr(reinterpret_cast<const void *>(kern), kPreSmem)) return PA_ERR_CUDA;
     const unsigned tiles = (unsigned)(((int64_t)max_q_len + 2 * kPreRows - 1) / (2 * kPreRows));
-    p.by_length = tiles <= 65535 && (int64_t)total_k * num_heads <= kPreByLength;
-    const dim3 grid = p.by_length ? dim3((unsigned)num_heads, (unsigned)num_seqs, tiles)
-                                  : dim3(tiles, (unsigned)num_heads, (unsigned)num_seqs);
-    if (launch_pdl(kern, grid, dim3(kPreThreads), kPreSmem, as_stream(stream), p, map_q, map_k, map_v,
-                   map_pe) != cudaSuccess)
+    // few pieces of work with many keys each: clusters that share the keys of one
+    const int64_t works = (int64_t)tiles * num_heads * num_seqs;
+    const int64_t key_tiles = ((int64_t)total_k / num_seqs + kPreKeys - 1) / kPreKeys;
+    p.split = 1;
+    for (int c = kPreMaxSplit; c > 1 && p.split == 1; c /= 2)
+        if (key_tiles >= c * kPreSplitTiles && works <= sm_count() / c && works <= prefill_clusters(bf16, c))
+            p.split = c;
+    if (p.split == 1 && works <= 2 * sm_count() && key_tiles >= kPreSplitLong) p.split = 2;
+    p.by_length = p.split == 1 && tiles <= 65535 && (int64_t)total_k * num_heads <= kPreByLength;
+    auto kern = p.split > 1 ? (bf16 ? prefill_latent_kernel<true, true> : prefill_latent_kernel<false, true>)
+                            : (bf16 ? prefill_latent_kernel<true, false> : prefill_latent_kernel<false, false>);
+    if (!ensure_smem_attr(reinterpret_cast<const void *>(kern), kPreSmem)) return PA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = p.by_length ? dim3((unsigned)num_heads, (unsigned)num_seqs, tiles)
+                              : dim3(tiles * (unsigned)p.split, (unsigned)num_heads, (unsigned)num_seqs);
+    cfg.blockDim = dim3(kPreThreads);
+    cfg.dynamicSmemBytes = kPreSmem;
+    cfg.stream = as_stream(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.split > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kern, p, map_q, map_k, map_v, map_pe) != cudaSuccess)
         return PA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

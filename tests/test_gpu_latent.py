@@ -476,6 +476,29 @@ def test_prefill_bad_starts():
     check(out[int(s[0]):int(s[2])], ref[s[0]:s[2]], bound[s[0]:s[2]])
 
 
+@BOTH
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n_q,n_k,heads", [
+    ([1], [3000], 3), ([200, 0, 37], [2500, 2600, 2700], 5), ([300, 129], [1100, 1500], 20),
+    ([600], [400], 4), ([1, 1, 1], [5000, 0, 130], 2), ([700], [1200], 30)])
+def test_prefill_keys_shared_out(dtype, causal, n_q, n_k, heads):
+    """Few pieces of work with many keys: two to eight CTAs share the keys of one, some with none."""
+    run_prefill(Prefill(np.random.default_rng(heads), dtype, n_q, n_k, heads, causal))
+
+
+def test_prefill_keys_shared_out_of_bad_starts():
+    case = Prefill(np.random.default_rng(13), "bf16", [40, 50], [3000, 2000], 2, True)
+    ref, bound = case.reference()
+    g, out = case.gpu(), case.empty()
+    g["k_starts"][0] = 1 << 20
+    api.prefill_latent(out, **g)
+    with pytest.raises(_lib.PagedAttentionError):
+        api.check_error()
+    a, b = int(case.q_starts[1]), int(case.q_starts[2])
+    assert (out[:a] == 7.0).all()
+    check(out[a:b], ref[a:b], bound[a:b])
+
+
 def test_prefill_many_short_prompts():
     rng = np.random.default_rng(10)
     n_q = rng.integers(0, 4, 3000)

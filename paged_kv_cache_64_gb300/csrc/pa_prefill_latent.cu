@@ -62,10 +62,12 @@ constexpr int kPreByLength = 400000;
 constexpr int kPreMaxKeys = 1 << 24;
 // A work's keys are shared out over up to eight CTAs, at least kPreSplitTiles tiles
 // each, as far as one wave holds them (1 query behind 8,000 keys, 4 heads: 89 us whole,
-// 23 with eight; 300 behind 6,000 twice, 8 heads: 72 and 31 with four), and over two
-// where there is about a wave of work and sequences are long enough to even it out
-// (16,000 tokens, 2 heads: 214 and 118; 4,096 tokens, 8 heads: 61 and 70).
-constexpr int kPreMaxSplit = 8, kPreSplitTiles = 4, kPreSplitLong = 64;
+// 22 with eight; 300 behind 6,000 twice, 8 heads: 72 and 31 with four), and over two
+// where there is about a wave of work, up to a fifth more, and sequences are long
+// enough to even it out (in pieces of work and tiles of keys: 126 of 125 214 us whole,
+// 118 in two; 160 of 63 180 and 157; 128 of 63 111 and 95; but 128 of 32 61 and 70, 224
+// of 47 130 and 148, 240 of 47 115 and 128).
+constexpr int kPreMaxSplit = 8, kPreSplitTiles = 4, kPreSplitLong = 40;
 constexpr int kPreQueue = 3;                       // work in hand: being done and fetched
 static_assert(kPreSmem <= 232448, "shared memory");
 
@@ -741,7 +743,7 @@ extern "C" pa_status pa_prefill_latent(
     for (int c = kPreMaxSplit; c > 1 && p.split == 1; c /= 2)
         if (key_tiles >= c * kPreSplitTiles && works <= sm_count() / c && works <= prefill_clusters(bf16, c))
             p.split = c;
-    if (p.split == 1 && works <= 2 * sm_count() && key_tiles >= kPreSplitLong) p.split = 2;
+    if (p.split == 1 && 5 * works <= 6 * sm_count() && key_tiles >= kPreSplitLong) p.split = 2;
     p.by_length = p.split == 1 && tiles <= 65535 && (int64_t)total_k * num_heads <= kPreByLength;
     auto kern = p.split > 1 ? (bf16 ? prefill_latent_kernel<true, true> : prefill_latent_kernel<false, true>)
                             : (bf16 ? prefill_latent_kernel<true, false> : prefill_latent_kernel<false, false>);

@@ -36,6 +36,7 @@
 // them.
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "pa_decode.cuh"
 #include "pa_internal.h"
@@ -47,7 +48,6 @@ constexpr int kLatRope = 64;      // shared key values of a row
 constexpr int kLatTile = 64;      // positions of a tile
 constexpr int kLatWarps = 12;
 constexpr int kLatSoftmax = 256;  // softmax threads: two warpgroups
-constexpr int kLatAhead = 2;      // tiles from a copy to the prefetch to L2 behind it
 constexpr int kLatThreads = kLatWarps * 32;
 constexpr int kLatSmem = 232448;  // what a CTA may have
 constexpr int kLatMisc = 2048;    // barriers and exchange
@@ -315,7 +315,12 @@ __global__ void __launch_bounds__(kLatThreads, 1)
             }
             return (phys << log2_block) + ((first + u * kUnit) & ((1 << log2_block) - 1));
         };
-        // a unit's rows lie together: one prefetch brings them to L2
+        // A unit's rows lie together: one prefetch brings them to L2, a tile before its
+        // copy can go, or two where two CTAs read the same rows and wait for one another's.
+        // (Farther ahead it only keeps the copies waiting: 16 sequences of 16-32k positions
+        // 94 us without, 88, 90, 94 and 105 with one to four tiles; 128 heads of 513-8192
+        // positions 219 without, 202, 188, 187 and 206.)
+        const int far = p.groups > 1 ? 2 : 1;
         auto prefetch = [&](int row) {
             asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
                              p.pool + (int64_t)row * (RANK + kLatRope)),
@@ -356,8 +361,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                 }
                 if (!ok) break;
                 if (++st == S::STAGES) st = 0, ++use;
-                // tile t + kLatAhead's units
-                const int u = 4 * (t + kLatAhead) + (lane & 3);
+                const int u = 4 * (t + far) + (lane & 3);
                 const int r_cur = __shfl_sync(kFullMask, rows_cur, u & 31);
                 const int r_next = __shfl_sync(kFullMask, rows_next, u & 31);
                 if (lane < 4 && u < units) prefetch((u >> 5) == (t >> 3) ? r_cur : r_next);
@@ -619,16 +623,28 @@ __global__ void __launch_bounds__(kLatThreads, 1)
             if (whole) {
                 if (mine && half == 0) alphas[row] = l_run > 0.f ? 1.f / l_run : l_run == 0.f ? 0.f : l_run;
                 latent_bar_or(false);
+                auto put = [&](auto all) {  // all: every head of the group is there
 #pragma unroll 1
-                for (int c = kCols * half; c < kCols * (half + 1); c += 16) {
-                    float o[16];
-                    tmem_load16(tmem + lanes + c, o);
-                    const int h0 = c % NH, j = c / NH;
-                    uint16_t *to = p.out + (out_row + h0) * RANK + 128 * j + dim;
+                    for (int c = kCols * half; c < kCols * (half + 1); c += 16) {
+                        float o[16];
+                        tmem_load16(tmem + lanes + c, o);
+                        const int h0 = c % NH, j = c / NH;
+                        uint16_t *to = p.out + (out_row + h0) * RANK + 128 * j + dim;
+                        const float4 *a = reinterpret_cast<const float4 *>(alphas + h0);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (h0 + i < heads) to[i * RANK] = narrow1<BF16>(o[i] * alphas[h0 + i]);
-                }
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 f = a[i / 4];
+                            if (all.value || h0 + i < heads) to[i * RANK] = narrow1<BF16>(o[i] * f.x);
+                            if (all.value || h0 + i + 1 < heads) to[(i + 1) * RANK] = narrow1<BF16>(o[i + 1] * f.y);
+                            if (all.value || h0 + i + 2 < heads) to[(i + 2) * RANK] = narrow1<BF16>(o[i + 2] * f.z);
+                            if (all.value || h0 + i + 3 < heads) to[(i + 3) * RANK] = narrow1<BF16>(o[i + 3] * f.w);
+                        }
+                    }
+                };
+                if (heads == NH)
+                    put(std::true_type());
+                else
+                    put(std::false_type());
             } else {
                 const int cut = walk.seq == seq0 && walk.tile == tile0 ? 0 : 1;
                 const int64_t slot = ((int64_t)range * p.groups + group) * 2 + cut;
@@ -647,8 +663,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                     tmem_load16(tmem + lanes + c, o);
                     const int h0 = c % NH, j = c / NH;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (h0 + i < heads) part[(h0 + i) * RANK + 128 * j] = o[i];
+                    for (int i = 0; i < 16; ++i) part[(h0 + i) * RANK + 128 * j] = o[i];  // heads that are not there too
                 }
             }
             tc_fence_before();

@@ -2,7 +2,7 @@
 
 Every translation unit under csrc/ is compiled in parallel (nvcc for the .cu
 files: decode, tensor-core decode, E4M3 and 4-bit decode, cascade, norm and
-rotation, cache writes and block copy; g++ for the .cpp files: the block allocator and the prefix-caching
+rotation, latent attention, cache writes and block copy; g++ for the .cpp files: the block allocator and the prefix-caching
 pool) and linked by nvcc into paged_kv_cache_64_gb300/_build/libpa.so.  The CUDA runtime is linked
 statically, so the library only needs the driver at run time.
 """

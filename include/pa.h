@@ -492,7 +492,10 @@ pa_status pa_cache_read_latent(void *rows_out, const int64_t *slot_mapping, int 
  * the GPU from the lengths on the device, and the pieces of sequences that this
  * cuts merged by a second launch; the result does not depend on the order in
  * which they run.  The weights are rounded to dtype before they meet the
- * values; their sum is not. */
+ * values; their sum is not.  Scores and sums are formed in fp32, the sums before
+ * their division (scores in fp32's range and |c| L_i below 2^119 are safe).  A
+ * live row that holds a NaN or an infinity may make the outputs of its sequence
+ * NaN.  out overlaps no other argument. */
 pa_status pa_decode_latent(void *out, const void *q, const void *pool, int num_blocks,
                            const int32_t *block_tables, int max_blocks_per_seq,
                            const int32_t *seq_lens, int max_seq_len, int num_seqs, int num_heads,
@@ -523,7 +526,9 @@ size_t pa_decode_latent_workspace_size(int num_seqs, int num_heads, int rank, in
  * leave [0, total], or with n_q > max_q_len, is a bad index (its rows left as
  * they were).  num_heads in 1 .. 1024, num_seqs up to 65535, total_k at most
  * 2^24.  The weights are rounded to dtype before they meet the values; their
- * sum is not. */
+ * sum is not.  Scores and sums are formed in fp32, the sums before their division
+ * (scores in fp32's range and |v| n_k below 2^119 are safe).  out overlaps no
+ * other argument. */
 pa_status pa_prefill_latent(void *out, const void *q, int64_t q_token_stride,
                             int64_t q_head_stride, const void *k, int64_t k_token_stride,
                             int64_t k_head_stride, const void *v, int64_t v_token_stride,

@@ -294,6 +294,31 @@ def test_decode_a_head_of_nan_stays_alone():
     check(out[1], ref[1], bound[1])
 
 
+def test_decode_thousands_of_sequences():
+    rng = np.random.default_rng(25)
+    lens = rng.integers(0, 3, 5000)
+    lens[[0, 17, 4999]] = [700, 300, 129]
+    run_decode(Decode(rng, "bf16", lens, 2, 256, 16))
+
+
+def test_attention_of_large_values():
+    """Values near the largest whose sums fp32 is said to hold (2^119 over the keys)."""
+    case = Decode(np.random.default_rng(26), "bf16", [500, 60], 5, 256, 16, poison=False)
+    size = 2.0 ** (119 - 9 - 2)
+    wide = int4.widen(case.pool, "bf16")
+    wide[..., :256] *= size
+    case.pool = int4.narrow(wide, "bf16")
+    wide = int4.widen(case.q, "bf16")
+    wide[..., :256] /= size
+    case.q = int4.narrow(wide, "bf16")
+    run_decode(case)
+    case = Prefill(np.random.default_rng(27), "bf16", [300], [500], 2, True)
+    wide = int4.widen(case.kv, "bf16")
+    wide[..., 128:] *= size
+    case.kv = int4.narrow(wide, "bf16")
+    run_prefill(case)
+
+
 def test_decode_shared_and_repeated_blocks():
     """Sequences that share blocks, and one that names a block twice."""
     case = Decode(np.random.default_rng(24), "f16", [160, 96, 64], 6, 512, 32, poison=False)

@@ -410,6 +410,54 @@ def test_decode_on_streams_and_in_graphs():
         check(ob, ref, bound)
 
 
+def test_two_graphs_share_a_workspace():
+    """Graphs of batches that are cut and that are not, replayed in turn over one workspace."""
+    rng = np.random.default_rng(28)
+    cases = [Decode(rng, "bf16", [2500, 300], 33, 256, 16), Decode(rng, "bf16", [400, 390], 33, 256, 16)]
+    gs, outs = [c.gpu() for c in cases], [c.empty() for c in cases]
+    ws = api.alloc_workspace(max(api.latent_workspace_size(2, 33, 256, 16, c.max_len, torch.bfloat16)
+                                 for c in cases), "cuda")
+    graphs = []
+    for g, out in zip(gs, outs):
+        api.decode_latent(out, **g, workspace=ws)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            api.decode_latent(out, **g, workspace=ws)
+    for _ in range(3):
+        for out in outs:
+            out.fill_(float("nan"))
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        api.check_error()
+        for c, out in zip(cases, outs):
+            ref, bound = c.reference()
+            check(out, ref, bound)
+
+
+def test_a_step_on_another_stream():
+    """Rows written, read back and attended on a stream that is not the current one, in order."""
+    rng = np.random.default_rng(29)
+    case = Decode(rng, "f16", [200, 65], 10, 512, 32, poison=False)
+    g, out, side = case.gpu(), case.empty(), torch.cuda.Stream()
+    r = Rows(rng, "f16", 2, 10, 512, 32)
+    last = [int(case.tables[i, (n - 1) // 32]) * 32 + (n - 1) % 32 for i, n in enumerate(case.lens.tolist())]
+    rows, back_rows = (torch.zeros(2, 576, dtype=torch.float16, device="cuda") for _ in range(2))
+    slots, args = torch.tensor(last, device="cuda"), r.gpu()
+    torch.cuda.synchronize()
+    api.latent_norm_rope(g["q"][..., 512:], **{**args, "pool": g["pool"], "slot_mapping": slots},
+                         rows_out=rows, stream=side)
+    api.cache_read_latent(back_rows, slots, g["pool"], stream=side)
+    api.decode_latent(out, **g, stream=side)
+    side.synchronize()
+    api.check_error(side)
+    assert torch.equal(rows, back_rows)
+    case.pool, case.q = back(g["pool"]), back(g["q"])
+    ref, bound = case.reference()
+    check(out, ref, bound)
+
+
 # ------------------------------------------------------------------ prompts
 def run_prefill(case, what=""):
     out = case.empty()

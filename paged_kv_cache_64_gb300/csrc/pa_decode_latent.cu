@@ -30,10 +30,10 @@
 //
 // The batch's tiles are shared out evenly: range b of the launch is tiles
 // [b per, (b + 1) per) of all sequences' tiles in a row, found from the lengths on
-// the device, or sequence b where they are about even.  A CTA goes through its range's pieces of sequences; Q and the rows
-// of the next piece are on their way while one ends.  A piece that is a whole
-// sequence is written out; the others leave (m, l, O) and a second launch joins
-// them.
+// the device, or sequence b where they are about even.  A CTA goes through its range's
+// pieces of sequences; Q and the rows of the next piece are on their way while one
+// ends.  A piece that is a whole sequence is written out; the others leave (m, l, O)
+// and a second launch joins them.
 //
 // What bounds it (rank 512).  A tile's products are 36 instructions of 32 clocks for
 // q.K^T (M = N = 64: their operands' 4 KiB from shared memory) and 16 of 48 for P.V,
@@ -45,7 +45,7 @@
 // 513-8192 positions, 128 heads, 178-190 us (0.83 PFLOP/s); 16 of 16-32k, 64 heads, 87 us
 // (5.2 TB/s); one of 200,003, 32 heads, 51 us (6.1 TB/s from the first tile to the last).
 // Issued from code that the compiler does not know to be a warp's, every instruction
-// took 64 clocks (286 us for 316 of the first).
+// takes 64 clocks (the first of these 316 us then, 286 with that mended alone).
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -63,7 +63,7 @@ constexpr int kLatSoftmax = 256;  // softmax threads: two warpgroups
 constexpr int kLatThreads = kLatWarps * 32;
 constexpr int kLatSmem = 232448;  // what a CTA may have
 constexpr int kLatMisc = 2048;    // barriers and exchange
-constexpr int kLatMaxLen = 1 << 24;
+constexpr int kLatMaxLen = 1 << 24;  // positions (a CTA's whole sequence is a wait, below)
 // Sequences are not cut where each has a range of its own and the longest is at most
 // this many tiles above an even share: cutting costs a range the write of its partial
 // results and all the joining launch.  Cut against whole, in us, of sequences of 8
@@ -108,8 +108,7 @@ struct LatShape {
     static constexpr int FULL = 0, EMPTY = STAGES, Q_FULL = EMPTY + 4 * STAGES, Q_FREE = Q_FULL + 1,
                          S_FULL = Q_FREE + 1, S_FREE = S_FULL + 2, P_FULL = S_FREE + 2,
                          PV_DONE = P_FULL + 2, O_FREE = PV_DONE + 2, VOTE = O_FREE + 1,
-                         DRAIN = VOTE + 1,
-                         BARS = DRAIN + 2;
+                         DRAIN = VOTE + 1, BARS = DRAIN + 2;
     // behind the barriers: TMEM address, abort flag, scan scratch, sums; then the heads'
     // factors and two halves' maxima
     static constexpr int OFF_WORDS = OFF_MISC + 512, OFF_ALPHA = OFF_MISC + 1024;

@@ -65,8 +65,8 @@ constexpr int kPreColS = 0, kPreColO = 256;        // TMEM columns: S_A S_B O_A 
 // 16 heads of 16,600 tokens 122 us the first way, 132 the other; 32 heads of 6,000
 // tokens behind 24,000 1,049 and 911.
 constexpr int kPreByLength = 400000;
-// 256 queries meet 2^24 keys in about 0.3 s; the fetching warp waits for three such
-// pieces of work at most, which a wait's limit has to cover.
+// 256 queries meet 2^24 keys in about 0.3 s; the next work's queries and the fetching
+// warp wait for the end of one such piece, which a wait's limit has to cover.
 constexpr int kPreMaxKeys = 1 << 24;
 // A work's keys are shared out over up to eight CTAs, at least kPreSplitTiles tiles
 // each, as far as one wave holds them (1 query behind 8,000 keys, 4 heads: 89 us whole,

@@ -625,7 +625,7 @@ def latent_norm_rope(q_out, q, latent, weight, eps, cos_sin, positions, slot_map
         raise TypeError("q, q_out, latent and weight must have one type")
     T, heads = qs[0], qs[1]
     nb, bs, rank = _latent_pool(pool, dt)
-    if len(ls) != 2 or ls != (T, rank + LATENT_ROPE):
+    if ls != (T, rank + LATENT_ROPE):
         raise ValueError(f"latent must be [T, {rank + LATENT_ROPE}]")
     if weight.shape != (rank,) or positions.shape != (T,) or slot_mapping.shape != (T,):
         raise ValueError("weight must be [rank], positions and slot_mapping [T]")
@@ -661,8 +661,9 @@ def latent_norm_rope(q_out, q, latent, weight, eps, cos_sin, positions, slot_map
                table[0], 1 if interleaved else 0, positions.data_ptr(),
                slot_mapping.data_ptr(), T, None if rows_out is None else rows_out.data_ptr(),
                pool.data_ptr(), nb, heads, rank, bs, code))
-    _check("pa_latent_norm_rope", rc, q_out=q_out, q=q, latent=latent, weight=weight,
-           cos_sin=cos_sin, pool=pool, rows_out=rows_out)
+    if rc:
+        _check("pa_latent_norm_rope", rc, q_out=q_out, q=q, latent=latent, weight=weight,
+               cos_sin=cos_sin, pool=pool, rows_out=rows_out)
 
 
 def cache_read_latent(rows_out, slot_mapping, pool, stream=None):
@@ -681,7 +682,8 @@ def cache_read_latent(rows_out, slot_mapping, pool, stream=None):
                  pool=(pool, None))
     rc = _run(dev, stream, _lib.load().pa_cache_read_latent,
               (rows_out.data_ptr(), slot_mapping.data_ptr(), T, pool.data_ptr(), nb, rank, bs, code))
-    _check("pa_cache_read_latent", rc, rows_out=rows_out, pool=pool)
+    if rc:
+        _check("pa_cache_read_latent", rc, rows_out=rows_out, pool=pool)
 
 
 def latent_workspace_size(num_seqs, num_heads, rank, block_size, max_seq_len, dtype):
@@ -719,14 +721,12 @@ def decode_latent(out, q, pool, block_tables, seq_lens, max_seq_len, scale, work
     args = (out.data_ptr(), q.data_ptr(), pool.data_ptr(), nb, block_tables.data_ptr(), tables[1],
             seq_lens.data_ptr(), max_len, S, heads, rank, bs, float(scale))
 
-    def run(ws):
-        if ws is None:
-            return _run(dev, stream, fn, args + (None, 0, code))
-        if ws.get_device() != dev or not ws.is_contiguous():
-            _explain(dev, workspace=(ws, None))
-        return _run(dev, stream, fn, args + (ws.data_ptr(), ws.nbytes, code))
-
-    rc = run(workspace)
+    if workspace is None:
+        rc = _run(dev, stream, fn, args + (None, 0, code))
+    else:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            _explain(dev, workspace=(workspace, None))
+        rc = _run(dev, stream, fn, args + (workspace.data_ptr(), workspace.nbytes, code))
     if rc == _lib.PA_ERR_INVALID:  # perhaps for want of a workspace: nothing was launched
         with torch.cuda.device(dev):
             need = latent_workspace_size(S, heads, rank, bs, max_len, dt)
@@ -735,10 +735,11 @@ def decode_latent(out, q, pool, block_tables, seq_lens, max_seq_len, scale, work
             # still be in use there
             with torch.cuda.stream(stream):
                 workspace = alloc_workspace(need, q.device)
-            rc = run(workspace)
+            rc = _run(dev, stream, fn, args + (workspace.data_ptr(), workspace.nbytes, code))
         elif need and workspace.data_ptr() % 256:
             raise ValueError("workspace must start on a 256-byte boundary")
-    _check("pa_decode_latent", rc, out=out, q=q, pool=pool)
+    if rc:
+        _check("pa_decode_latent", rc, out=out, q=q, pool=pool)
     return workspace
 
 
@@ -782,7 +783,8 @@ def prefill_latent(out, q, k, v, k_pe, q_starts, k_starts, max_q_len, scale, cau
                v.data_ptr(), *_steps(v, "v"), k_pe.data_ptr(), pe_step, q_starts.data_ptr(),
                k_starts.data_ptr(), q_starts.shape[0] - 1, qs[0], ks[0], int(max_q_len), qs[1],
                float(scale), 1 if causal else 0, code))
-    _check("pa_prefill_latent", rc, out=out, q=q, k=k, v=v, k_pe=k_pe)
+    if rc:
+        _check("pa_prefill_latent", rc, out=out, q=q, k=k, v=v, k_pe=k_pe)
 
 
 def cascade_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,

@@ -36,7 +36,7 @@ def decode(lib, out=P, q=P, pool=P, nb=4, tables=P, mb=2, lens=P, max_len=30, S=
                                 ws, wb, dt, NULL)
 
 
-def prefill(lib, out=P, q=P, qt=3072 + 192, qh=192, k=P, kt=4096, kh=256, v=P, vt=4096, vh=256, pe=P,
+def prefill(lib, out=P, q=P, qt=3264, qh=192, k=P, kt=4096, kh=256, v=P, vt=4096, vh=256, pe=P,
             pt=576, qs=P, ks=P, S=2, tq=10, tk=12, mq=5, heads=16, scale=0.1, causal=1, dt=1):
     return lib.pa_prefill_latent(out, q, qt, qh, k, kt, kh, v, vt, vh, pe, pt, qs, ks, S, tq, tk, mq,
                                  heads, scale, causal, dt, NULL)

@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         const uint64_t v_desc = sw128_desc(base + kPreOffRing, kPreSlab, 1024);
         int at[2] = {0, 0}, works[2] = {0, 0};  // P.V steps and pieces of work of either tile
         struct Turn {
-            int turn, tiles0, tiles1, most, tile;  // most 0: no more work; tile: counted over all work
+            int turn, tiles0, tiles1, most, tile;  // most -1: no more work; tile: counted over all work
         };
         auto landed = [&](int group) {
             mbar_wait_flow(&bar[kPreFull + group % kPreGroups], (group / kPreGroups) & 1, flag);
@@ -465,24 +465,33 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             __syncwarp();
             if (done) ++works[x];
         };
-        // the next work that has keys
-        auto next = [&](int turn, int tile) -> Turn {
+        // The work of a turn, and the first one from there on that has keys (or the end).
+        auto look = [&](int turn, int tile) -> Turn {
+            mbar_wait_flow(work_full(turn), (turn / kPreQueue) & 1, flag);
+            const PreWork w = read_work(turn);
+            if (__any_sync(kFullMask, *abort_flag || w.n_q < 0)) return {turn, 0, 0, -1, tile};
+            // by shuffles: values that the compiler knows to be the warp's
+            const int tiles0 = __shfl_sync(kFullMask, prefill_tiles(w, 0, p.causal), 0);
+            const int tiles1 = __shfl_sync(kFullMask, prefill_tiles(w, 1, p.causal), 0);
+            return {turn, tiles0, tiles1, max(tiles0, tiles1), tile};
+        };
+        auto release = [&](int turn) {
+            if (elect_one()) mbar_arrive(work_free(turn));
+            __syncwarp();
+        };
+        auto keyed = [&](int turn, int tile) -> Turn {
             for (;; ++turn) {
-                mbar_wait_flow(work_full(turn), (turn / kPreQueue) & 1, flag);
-                const PreWork w = read_work(turn);
-                if (__any_sync(kFullMask, *abort_flag || w.n_q < 0)) return {turn, 0, 0, 0, tile};
-                // by shuffles: values that the compiler knows to be the warp's
-                const int tiles0 = __shfl_sync(kFullMask, prefill_tiles(w, 0, p.causal), 0);
-                const int tiles1 = __shfl_sync(kFullMask, prefill_tiles(w, 1, p.causal), 0);
-                const int most = max(tiles0, tiles1);
-                if (most > 0) return {turn, tiles0, tiles1, most, tile};
-                if (elect_one()) mbar_arrive(work_free(turn));
-                __syncwarp();
+                const Turn w = look(turn, tile);
+                if (w.most != 0) return w;
+                release(turn);
             }
         };
-        Turn w = next(0, 0);
-        if (w.tiles0 > 0) issue_qk(0, w, 0);
-        if (w.tiles1 > 0) issue_qk(1, w, 0);
+        auto start = [&](const Turn &w) {
+            if (w.tiles0 > 0) issue_qk(0, w, 0);
+            if (w.tiles1 > 0) issue_qk(1, w, 0);
+        };
+        Turn w = keyed(0, 0);
+        start(w);
         while (w.most > 0) {
             for (int t = 0; t + 1 < w.most; ++t) {
                 if (t < w.tiles0) issue_pv(0, w, t);
@@ -492,15 +501,21 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             }
             // Every q.K of this work is issued: the next one's first may go before the other
             // tile's last P.V, as they need no slab but the two of V beside their own three.
+            // No work past the next is looked at while this one's turn is held: the queue's
+            // fourth turn waits for the release of its first.
             const int t = w.most - 1;
             if (t < w.tiles0) issue_pv(0, w, t);
-            const Turn n = next(w.turn + 1, w.tile + w.most);
+            const Turn n = look(w.turn + 1, w.tile + w.most);
             if (n.tiles0 > 0) issue_qk(0, n, 0);
             if (t < w.tiles1) issue_pv(1, w, t);
             if (n.tiles1 > 0) issue_qk(1, n, 0);
-            if (elect_one()) mbar_arrive(work_free(w.turn));
-            __syncwarp();
+            release(w.turn);
             w = n;
+            if (w.most == 0) {  // without keys, and no turn held
+                release(w.turn);
+                w = keyed(w.turn + 1, w.tile);
+                start(w);
+            }
         }
         if (elect_one()) tc_commit(&bar[kPreDrain]);
         (void)mbar_wait(&bar[kPreDrain], 0);

@@ -24,10 +24,11 @@
 // the lazy rescale.
 //
 // The launch has a block for every (256 queries, head, sequence) up to the longest
-// sequence; a CTA that runs takes over blocks that have not been launched yet
+// sequence; or, where most of these would have no queries, for every piece of work that
+// the numbers of tokens and sequences allow, which the fetching warp finds from the
+// sequences' starts.  A CTA that runs takes over blocks that have not been launched yet
 // (clusterlaunchcontrol), so the next work's queries and keys load, and its first
-// products run, while the softmax of the last ends.  Blocks past a sequence's end
-// cost the fetching warp a look at its lengths.  Where there are few blocks and many
+// products run, while the softmax of the last ends.  Where there are few blocks and many
 // keys, a cluster shares a block's keys instead and joins its sums through distributed
 // shared memory.
 //
@@ -42,6 +43,7 @@
 #include <cstdint>
 #include <map>
 #include <mutex>
+#include <type_traits>
 
 #include "pa_decode.cuh"
 #include "pa_internal.h"
@@ -77,6 +79,18 @@ constexpr int kPreMaxKeys = 1 << 24;
 // of 47 130 and 148, 240 of 47 115 and 128).
 constexpr int kPreMaxSplit = 8, kPreSplitTiles = 4, kPreSplitLong = 40;
 constexpr int kPreQueue = 3;                       // work in hand: being done and fetched
+// Blocks of a launch at most; past them a block stands for several pieces of work in a
+// row.  It bounds the blocks without work that a CTA takes over in a row (6,900 of 152)
+// while its other roles wait.
+constexpr int kPreBlocks = 1 << 20;
+// A block for every (256 queries, head, sequence) while these are up to so many times
+// the pieces of work that there can be: a piece is found faster so, but a block without
+// queries costs its CTA about a microsecond.  16 heads, so and found from the starts:
+// 255 sequences of 30-70 tokens 100 us and 105, one of 8,192 241 and 254, 16 of 31-2,048
+// (1.6 times as many) 119 and 121, but 157 and 121 with a bound on lengths eight times
+// as large; 255 of 30-70 and one of 8,192 (25 times) 496 and 315.
+constexpr int kPreSparse = 2;
+constexpr int kPreChunk = 256;                     // sequences that the fetching warp holds
 static_assert(kPreSmem <= 232448, "shared memory");
 
 // K and V of a tile are awaited as a whole: group 2 t is K's slabs, 2 t + 1 V's.  At
@@ -105,8 +119,10 @@ struct PrefillLatentParams {
     const int32_t *q_starts, *k_starts;
     int total_q, total_k, max_q, num_heads, causal;
     int wide;       // out lies on a 32-byte boundary
+    int num_seqs;
+    int per;        // pieces of work a block; 0: a block is (256 queries, head, sequence)
     int split;      // CTAs of a cluster that share a work's keys
-    int by_length;  // grid (heads, sequences, tiles) instead of (tiles, heads, sequences)
+    int by_length;  // order of work: grid (heads, sequences, tiles) instead of (tiles, heads, sequences)
     float scale_log2;
     int *err;
 };
@@ -119,6 +135,134 @@ __device__ __forceinline__ int prefill_tiles(const PreWork &w, int x, int causal
     const int end = keys > 0 ? (keys + kPreKeys - 1) / kPreKeys : 0;
     return max(min(end, w.upto) - w.from, 0);
 }
+
+// A sequence's tokens; false: it has none, or its starts are bad.
+__device__ __forceinline__ bool prefill_sequence(const PrefillLatentParams &p, int seq, PreWork &w, bool report) {
+    const int q0 = p.q_starts[seq], q1 = p.q_starts[seq + 1], k0 = p.k_starts[seq], k1 = p.k_starts[seq + 1];
+    const bool good = q0 >= 0 && q1 >= q0 && q1 - q0 <= p.max_q && q1 <= p.total_q && k0 >= 0 && k1 >= k0 &&
+                      k1 <= p.total_k;
+    if (!good && report) record_error(p.err, PA_ERR_BAD_INDEX);
+    w.q0 = q0, w.n_q = q1 - q0, w.k0 = k0, w.n_k = k1 - k0;
+    return good && q1 > q0;
+}
+
+// Where most blocks of (256 queries, head, sequence) would be empty: the pieces of work
+// in their order, walked by a whole warp that holds the tiles of a chunk of sequences
+// (32 k + lane in tiles[k]).  A chunk's follow the last one's.  Within a chunk the order
+// is that of the blocks: by length, the longest sequences' last tiles of all heads first
+// (tiles down, then sequences, then heads); or sequence by sequence, of each head in
+// turn, the last tile first.
+struct PreList {
+    static constexpr int ROWS = kPreChunk / 32;
+    const PrefillLatentParams &p;
+    const int lane;
+    int base;                   // the chunk's first sequence
+    int tiles[ROWS];            // of 256 queries
+    unsigned marks[ROWS];       // by length: lanes that reach `level`; else the row's tiles up to a lane
+    int total, top;             // tiles of the chunk; of its longest sequence
+    int level, above, there;    // by length: tiles past `level`, and on it
+    int64_t before;             // pieces of work in earlier chunks
+
+    __device__ __forceinline__ PreList(const PrefillLatentParams &prm, int l) : p(prm), lane(l) {}
+
+    __device__ __forceinline__ void restart() {
+        before = 0;
+        load(0);
+    }
+
+    __device__ __forceinline__ void set_level(int l, int past) {
+        level = l;
+        above = past;
+        there = 0;
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            marks[k] = __ballot_sync(kFullMask, tiles[k] > level);
+            there += __popc(marks[k]);
+        }
+    }
+
+    // Sequences [first, first + kPreChunk).  A bad one has no work.
+    __device__ __forceinline__ void load(int first) {
+        base = first;
+        int sum = 0, longest = 0;
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            const int s = first + 32 * k + lane;
+            PreWork w;
+            tiles[k] = 0;
+            if (s < p.num_seqs && prefill_sequence(p, s, w, true))
+                tiles[k] = (int)(((unsigned)w.n_q + 2 * kPreRows - 1) / (2 * kPreRows));
+            sum += tiles[k];
+            longest = max(longest, tiles[k]);
+        }
+        total = __reduce_add_sync(kFullMask, sum);
+        top = __reduce_max_sync(kFullMask, longest);
+        if (p.by_length) {
+            set_level(top - 1, 0);
+        } else {
+#pragma unroll
+            for (int k = 0; k < ROWS; ++k) {
+                int upto = tiles[k];
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(kFullMask, upto, o);
+                    if (lane >= o) upto += v;
+                }
+                marks[k] = upto;
+            }
+        }
+    }
+
+    // Piece of work `item`; false: there are not so many.
+    __device__ __forceinline__ bool find(int64_t item, PreWork &w) {
+        const unsigned heads = p.num_heads;
+        if (item < before) restart();
+        while (item >= before + (int64_t)total * heads) {
+            if (base + kPreChunk >= p.num_seqs) return false;
+            before += (int64_t)total * heads;
+            load(base + kPreChunk);
+        }
+        // (a chunk's pieces are fewer than 2^31: their outputs lie in memory)
+        unsigned r = (unsigned)(item - before);
+        int row = 0, mine, tile;
+        if (p.by_length) {
+            w.head = (int)(r % heads);
+            r /= heads;
+            if ((int)r < above) set_level(top - 1, 0);
+            while ((int)r >= above + there) set_level(level - 1, above + there);
+            tile = level;
+            r -= above;  // the r-th of the sequences that reach it
+            unsigned mask = marks[0];
+#pragma unroll
+            for (int k = 1; k < ROWS; ++k)
+                if (r >= (unsigned)__popc(mask) && row == k - 1) {
+                    r -= __popc(mask);
+                    mask = marks[k];
+                    row = k;
+                }
+            mine = __ffs(__ballot_sync(kFullMask, (mask >> lane & 1) &&
+                                                      __popc(mask & ((1u << lane) - 1)) == (int)r)) - 1;
+        } else {
+            unsigned upto = marks[0], n = tiles[0];
+#pragma unroll
+            for (int k = 1; k < ROWS; ++k) {
+                const unsigned all = __shfl_sync(kFullMask, upto, 31) * heads;
+                if (r >= all && row == k - 1) {
+                    r -= all;
+                    upto = marks[k], n = tiles[k];
+                    row = k;
+                }
+            }
+            mine = __ffs(__ballot_sync(kFullMask, upto * heads > r)) - 1;
+            n = __shfl_sync(kFullMask, n, mine);
+            r -= (__shfl_sync(kFullMask, upto, mine) - n) * heads;
+            w.head = (int)(r / n);
+            tile = (int)(n - 1 - r % n);
+        }
+        w.first = tile * 2 * kPreRows;
+        return prefill_sequence(p, base + 32 * row + mine, w, false);
+    }
+};
 
 // Largest (MAX) or smallest of 128 values, NaN left aside.
 template <bool MAX>
@@ -270,22 +414,28 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 
     if (warp == 10) {
         // ---------------------------------------------------------- next work
-        if (lane == 0) {
+        // by lane 0 where a block is (256 queries, head, sequence), by the warp where the
+        // pieces of work are listed
+        auto fetch = [&](auto is_listed) {
+            constexpr bool LISTED = is_listed.value;
+            auto agreed = [](bool v) -> bool {
+                if constexpr (LISTED) v = __all_sync(kFullMask, v);
+                return v;
+            };
             int x = blockIdx.x / split, y = blockIdx.y, z = blockIdx.z, claims = 0;
             // a block that has not been launched yet becomes this CTA's; false: none is left
             auto claim = [&]() -> bool {
-                const uint32_t answer = smem_addr(smem + kPreOffClaim);
-                fence_async_smem();  // the last answer has been read
-                mbar_arrive_expect_tx(&bar[kPreClaim], 16);
-                asm volatile(
-                    "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
-                    "[%0], [%1];" ::"r"(answer), "r"(smem_addr(&bar[kPreClaim]))
-                    : "memory");
-                if (!mbar_wait(&bar[kPreClaim], claims & 1)) {
-                    ok = false;
-                    return false;
+                if (lane == 0) {
+                    fence_async_smem();  // the last answer has been read
+                    mbar_arrive_expect_tx(&bar[kPreClaim], 16);
+                    asm volatile(
+                        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+                        "[%0], [%1];" ::"r"(smem_addr(smem + kPreOffClaim)), "r"(smem_addr(&bar[kPreClaim]))
+                        : "memory");
                 }
-                ++claims;
+                if constexpr (LISTED) __syncwarp();
+                ok = agreed(mbar_wait(&bar[kPreClaim], claims++ & 1));
+                if (!ok) return false;
                 uint32_t got;
                 asm volatile(
                     "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t"
@@ -296,52 +446,79 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                     "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 "
                     "{%1, %2, %3, _}, a;\n\t}"
                     : "=&r"(got), "=&r"(x), "=&r"(y), "=&r"(z)
-                    : "r"(answer)
+                    : "r"(smem_addr(smem + kPreOffClaim))
                     : "memory");
+                if constexpr (LISTED) __syncwarp();  // before the next answer
                 return got != 0;
             };
-            bool have = true;  // (x, y, z) is a block to look at
+            PreList list(p, lane);
+            int64_t item = 0, end = 1;
+            if constexpr (LISTED) {
+                item = (int64_t)x * p.per;
+                end = item + p.per;
+                list.restart();
+            }
+            // Of listed pieces, the CTA that has the first block goes on behind the last one: it
+            // looks at every sequence's starts, and where some decrease, which makes a bad
+            // sequence, those behind may have more queries together than the host counts.
+            bool first = LISTED && x == 0, left = !SPLIT;
             for (int turn = 0;; ++turn) {
-                if (turn >= kPreQueue &&
-                    !mbar_wait_or(work_free(turn), (turn / kPreQueue - 1) & 1, abort_flag)) {
-                    ok = false;
-                    break;
+                if (turn >= kPreQueue) {
+                    ok = agreed(mbar_wait_or(work_free(turn), (turn / kPreQueue - 1) & 1, abort_flag));
+                    if (!ok) break;
                 }
                 PreWork w;
-                for (;;) {
-                    w = {0, -1, 0, 0, 0, 0, 0, 0x7fffffff};
-                    if (!have && (SPLIT || !claim())) break;
-                    have = false;
-                    // the longest tiles of causal sequences come first: of each head in turn,
-                    // or of all
-                    const int seq = p.by_length ? y : z;
-                    const int last = (p.by_length ? gridDim.z : gridDim.x / split) - 1;
-                    w.first = (last - (p.by_length ? z : x)) * 2 * kPreRows;
-                    w.head = p.by_length ? x : y;
-                    w.q0 = p.q_starts[seq];
-                    w.k0 = p.k_starts[seq];
-                    const int q1 = p.q_starts[seq + 1], k1 = p.k_starts[seq + 1];
-                    const bool good = w.q0 >= 0 && q1 >= w.q0 && q1 - w.q0 <= p.max_q && q1 <= p.total_q &&
-                                      w.k0 >= 0 && k1 >= w.k0 && k1 <= p.total_k;
-                    if (!good && w.head == 0 && w.first == 0) record_error(p.err, PA_ERR_BAD_INDEX);
-                    if (good && w.first < q1 - w.q0) {
-                        w.n_q = q1 - w.q0;
-                        w.n_k = k1 - w.k0;
-                        if constexpr (SPLIT) {  // this CTA's share of the keys
-                            const int all = max(prefill_tiles(w, 0, p.causal), prefill_tiles(w, 1, p.causal));
-                            const int per = (all + split - 1) / split;
-                            w.from = per * (int)cluster_ctarank();
-                            w.upto = w.from + per;
+                bool found = false;
+                while (!found) {
+                    if (item == end) {
+                        if (!left) break;
+                        left = claim();  // if not, no more claims
+                        if (left) {
+                            item = LISTED ? (int64_t)x * p.per : 0;
+                            end = LISTED ? item + p.per : 1;
+                            first |= LISTED && x == 0;
+                        } else if (first) {
+                            item = (int64_t)gridDim.x * p.per;
+                            end = 1ll << 62;
+                        } else {
+                            break;
                         }
-                        break;
                     }
+                    w.from = 0, w.upto = 0x7fffffff;
+                    if constexpr (LISTED) {
+                        found = list.find(item, w);
+                        item = found ? item + 1 : end;
+                    } else {
+                        // the longest tiles of causal sequences come first: of each head in turn,
+                        // or of all
+                        const int last = (int)(p.by_length ? gridDim.z : gridDim.x / split) - 1;
+                        w.first = (last - (p.by_length ? z : x)) * 2 * kPreRows;
+                        w.head = p.by_length ? x : y;
+                        found = prefill_sequence(p, p.by_length ? y : z, w, w.head == 0 && w.first == 0) &&
+                                w.first < w.n_q;
+                        item = end;
+                    }
+                    if (!found && !agreed(!*abort_flag)) break;
                 }
-                queue[2 * (turn % kPreQueue)] = make_int4(w.q0, w.n_q, w.k0, w.n_k);
-                queue[2 * (turn % kPreQueue) + 1] = make_int4(w.head, w.first, w.from, w.upto);
-                mbar_arrive(work_full(turn));
-                if (w.n_q < 0) break;
+                if (!found) w = {0, -1, 0, 0, 0, 0, 0, 0};  // no more work
+                if constexpr (SPLIT) {  // this CTA's share of the keys
+                    const int all = max(prefill_tiles(w, 0, p.causal), prefill_tiles(w, 1, p.causal));
+                    const int per = (all + split - 1) / split;
+                    w.from = per * (int)cluster_ctarank();
+                    w.upto = w.from + per;
+                }
+                if (lane == 0) {
+                    queue[2 * (turn % kPreQueue)] = make_int4(w.q0, w.n_q, w.k0, w.n_k);
+                    queue[2 * (turn % kPreQueue) + 1] = make_int4(w.head, w.first, w.from, w.upto);
+                    mbar_arrive(work_full(turn));
+                }
+                if (!found) break;
             }
-        }
+        };
+        if (!SPLIT && p.per > 0)
+            fetch(std::bool_constant<!SPLIT>());
+        else if (lane == 0)
+            fetch(std::false_type());
         __syncwarp();
     } else if (warp == 0) {
         // ---------------------------------------------------------- producer
@@ -738,6 +915,7 @@ extern "C" pa_status pa_prefill_latent(
     p.total_k = total_k;
     p.max_q = max_q_len;
     p.num_heads = num_heads;
+    p.num_seqs = num_seqs;
     p.causal = causal != 0;
     p.wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
     p.scale_log2 = latent_scale(scale);
@@ -758,22 +936,32 @@ extern "C" pa_status pa_prefill_latent(
                      map3(&map_v, q, kPreValue, total_q, q_token_stride, q_head_stride)) ||
         !boxed_tensor_map(&map_pe, keys ? k_pe : q, 2, pe_dims, pe_step, box, bf16))
         return PA_ERR_CUDA;
-    const unsigned tiles = (unsigned)(((int64_t)max_q_len + 2 * kPreRows - 1) / (2 * kPreRows));
+    const int64_t tiles = ((int64_t)max_q_len + 2 * kPreRows - 1) / (2 * kPreRows);
+    const int64_t works = tiles * num_heads * num_seqs;  // pieces of work at most
     // few pieces of work with many keys each: clusters that share the keys of one
-    const int64_t works = (int64_t)tiles * num_heads * num_seqs;
     const int64_t key_tiles = ((int64_t)total_k / num_seqs + kPreKeys - 1) / kPreKeys;
     p.split = 1;
     for (int c = kPreMaxSplit; c > 1 && p.split == 1; c /= 2)
         if (key_tiles >= c * kPreSplitTiles && works <= sm_count() / c && works <= prefill_clusters(bf16, c))
             p.split = c;
     if (p.split == 1 && 5 * works <= 6 * sm_count() && key_tiles >= kPreSplitLong) p.split = 2;
-    p.by_length = p.split == 1 && tiles <= 65535 && (int64_t)total_k * num_heads <= kPreByLength;
+    p.by_length = p.split == 1 && (int64_t)total_k * num_heads <= kPreByLength;
+    dim3 grid = p.by_length ? dim3((unsigned)num_heads, (unsigned)num_seqs, (unsigned)tiles)
+                            : dim3((unsigned)(tiles * p.split), (unsigned)num_heads, (unsigned)num_seqs);
+    // Sequences one behind the other have a piece of work of a head for each that has a
+    // query, and one for every 256 queries beside those.
+    const int64_t some = num_seqs < total_q ? num_seqs : total_q;
+    const int64_t count = (some + (total_q - some) / (2 * kPreRows)) * num_heads;
+    if (p.split == 1 && (works > kPreSparse * count || works > kPreBlocks || (p.by_length && tiles > 65535))) {
+        const int64_t most = works < count ? works : count;
+        p.per = (int)((most + kPreBlocks - 1) / kPreBlocks);
+        grid = dim3((unsigned)((most + p.per - 1) / p.per));
+    }
     auto kern = p.split > 1 ? (bf16 ? prefill_latent_kernel<true, true> : prefill_latent_kernel<false, true>)
                             : (bf16 ? prefill_latent_kernel<true, false> : prefill_latent_kernel<false, false>);
     if (!ensure_smem_attr(reinterpret_cast<const void *>(kern), kPreSmem)) return PA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = p.by_length ? dim3((unsigned)num_heads, (unsigned)num_seqs, tiles)
-                              : dim3(tiles * (unsigned)p.split, (unsigned)num_heads, (unsigned)num_seqs);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(kPreThreads);
     cfg.dynamicSmemBytes = kPreSmem;
     cfg.stream = as_stream(stream);

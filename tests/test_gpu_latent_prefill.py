@@ -1,10 +1,11 @@
 """Prompts' expanded attention where a CTA takes over many pieces of work: pieces
-without keys among them."""
+without keys among them, and batches of many sequences and of very different lengths."""
 import numpy as np
 import pytest
+import torch
 
-from _latent import Prefill
-from paged_kv_cache_64_gb300 import api
+from _latent import Prefill, check
+from paged_kv_cache_64_gb300 import _lib, api
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +42,76 @@ def test_runs_of_works_without_keys(length):
 def test_many_more_queries_than_keys(heads, n_q, n_k):
     """Causal: all queries but the last n_k meet no key, whole pieces of work of them."""
     run(Prefill(np.random.default_rng(heads), "bf16", [n_q], [n_k], heads, True))
+
+
+# ------------------------------------------------------------------ which work a block is
+@pytest.mark.parametrize("max_q_len", [100, 1 << 20, (1 << 31) - 1])
+def test_bound_on_queries_far_above_them(max_q_len):
+    rng = np.random.default_rng(20)
+    n_q = rng.integers(0, 20, 300)
+    run(Prefill(rng, "bf16", n_q, n_q + rng.integers(0, 9, 300), 2, True), max_q_len=max_q_len)
+
+
+@pytest.mark.parametrize("heads,context", [(3, 20), (12, 110)])
+@pytest.mark.parametrize("at", [0, 200, 290, 399])
+def test_one_long_prompt_among_many_short(heads, context, at):
+    """More sequences than the fetching warp holds at once, in either order of work."""
+    rng = np.random.default_rng(at)
+    n_q = rng.integers(0, 6, 400)
+    n_q[at] = 900
+    n_k = n_q + rng.integers(context // 2, context, 400)
+    case = Prefill(rng, "bf16", n_q, n_k, heads, True)
+    assert (len(case.kv) * heads > 400000) == (heads == 12)
+    run(case)
+
+
+@pytest.mark.parametrize("full", [[0], [599], [255, 256], [10, 511, 512]])
+def test_padded_batches(full):
+    """Most sequences are empty."""
+    rng = np.random.default_rng(full[0])
+    n_q = np.zeros(600, np.int64)
+    n_q[full] = rng.integers(200, 700, len(full))
+    run(Prefill(rng, "f16", n_q, n_q, 2, False))
+
+
+def test_more_pieces_of_work_than_blocks():
+    """65,535 sequences of a token with one key: each output is that key's value."""
+    S, heads = 65535, 32
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v = (torch.empty(S, heads, w, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+               for w in (192, 128, 128))
+    k_pe = torch.empty(S, 64, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    starts = torch.arange(S + 1, dtype=torch.int32, device="cuda")
+    out = torch.full_like(v, 7.0)
+    api.prefill_latent(out, q, k, v, k_pe, starts, starts, 1, 0.1)
+    api.check_error()
+    assert torch.equal(out, v)
+
+
+def test_starts_that_go_back():
+    """Sequences that repeat others' queries behind a bad one: more pieces of work than
+    as many tokens and sequences have in order."""
+    rng = np.random.default_rng(21)
+    case = Prefill(rng, "bf16", [600, 600], [600, 600], 1, True, gap=0)
+    ref, bound = case.reference()
+    starts = torch.tensor([0, 600] * 9 + [1200], dtype=torch.int32, device="cuda")
+    out = case.empty()
+    api.prefill_latent(out, **{**case.gpu(), "q_starts": starts, "k_starts": starts})
+    with pytest.raises(_lib.PagedAttentionError) as e:
+        api.check_error()
+    assert e.value.code == 6
+    check(out, ref, bound)
+
+
+def test_bad_starts_far_behind():
+    """A bad sequence behind the last piece of work is reported too."""
+    rng = np.random.default_rng(22)
+    n = np.zeros(700, np.int64)
+    n[3] = 40
+    case = Prefill(rng, "bf16", n, n, 2, True)
+    g, out = case.gpu(), case.empty()
+    g["k_starts"][700] += 1 << 20
+    api.prefill_latent(out, **g)
+    with pytest.raises(_lib.PagedAttentionError):
+        api.check_error()
+    case.check(out)

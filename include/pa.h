@@ -493,8 +493,8 @@ pa_status pa_cache_read_latent(void *rows_out, const int64_t *slot_mapping, int 
  * cuts merged by a second launch; the result does not depend on the order in
  * which they run.  The weights are rounded to dtype before they meet the
  * values; their sum is not.  Scores and sums are formed in fp32, the sums before
- * their division (scores in fp32's range and |c| L_i below 2^119 are safe).  A
- * live row that holds a NaN or an infinity may make the outputs of its sequence
+ * their division (dot products and scores in fp32's range and |c| L_i below 2^119
+ * are safe, whatever the scale).  A live row that holds a NaN or an infinity may make the outputs of its sequence
  * NaN.  out overlaps no other argument. */
 pa_status pa_decode_latent(void *out, const void *q, const void *pool, int num_blocks,
                            const int32_t *block_tables, int max_blocks_per_seq,
@@ -527,8 +527,8 @@ size_t pa_decode_latent_workspace_size(int num_seqs, int num_heads, int rank, in
  * they were).  num_heads in 1 .. 1024, num_seqs up to 65535, total_k at most
  * 2^24.  The weights are rounded to dtype before they meet the values; their
  * sum is not.  Scores and sums are formed in fp32, the sums before their division
- * (scores in fp32's range and |v| n_k below 2^119 are safe).  out overlaps no
- * other argument. */
+ * (dot products and scores in fp32's range and |v| n_k below 2^119 are safe,
+ * whatever the scale).  out overlaps no other argument. */
 pa_status pa_prefill_latent(void *out, const void *q, int64_t q_token_stride,
                             int64_t q_head_stride, const void *k, int64_t k_token_stride,
                             int64_t k_head_stride, const void *v, int64_t v_token_stride,

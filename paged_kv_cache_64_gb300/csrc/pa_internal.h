@@ -21,12 +21,11 @@ bool ensure_smem_attr(const void *kernel, int bytes);
 
 inline cudaStream_t as_stream(void *s) { return static_cast<cudaStream_t>(s); }
 
-// scale * log2(e) in fp32, kept from 0: a score times it then is -inf where a masked
-// position's is (infinite with the other sign), and scores of any size are equal
-// under a scale that small.
+// scale * log2(e) in fp32, kept from 0: a masked position's infinity times it stays
+// infinite.  The smallest fp32 number in its place makes less than 5e-7 of any score.
 inline float latent_scale(float scale) {
     const float x = (float)((double)scale * 1.4426950408889634);
-    return x >= 0.f && x < 1e-30f ? 1e-30f : x < 0.f && x > -1e-30f ? -1e-30f : x;
+    return x == 0.f ? 1.401298464324817e-45f : x;  // 2^-149
 }
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

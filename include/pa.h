@@ -435,8 +435,9 @@ pa_status pa_qk_norm_rope(void *q_out, int64_t q_out_stride, const void *q, int6
  *   interleaved, and cos, sin the position's table row:
  *       (a, b) becomes (a cos_i - b sin_i, b cos_i + a sin_i)
  *   for y = latent[t][rank .. rank + 64) and every head q[t][h][0 .. 64)
- * in fp32 throughout, rounded to dtype once.  The turned queries go to q_out,
- * the row (c, turned y) to the token's slot and to rows_out.
+ * in fp32 throughout (the sum of x^2 in its range), rounded to dtype once.  The
+ * turned queries go to q_out, the row (c, turned y) to the token's slot and to
+ * rows_out.
  * Device pointers, 16-byte aligned:
  *   q, q_out: 64 dense values a head; *_token_stride and *_head_stride
  *     elements from a token and a head to the next (multiples of 8, at least
@@ -494,8 +495,8 @@ pa_status pa_cache_read_latent(void *rows_out, const int64_t *slot_mapping, int 
  * which they run.  The weights are rounded to dtype before they meet the
  * values; their sum is not.  Scores and sums are formed in fp32, the sums before
  * their division (dot products and scores in fp32's range and |c| L_i below 2^119
- * are safe, whatever the scale).  A live row that holds a NaN or an infinity may make the outputs of its sequence
- * NaN.  out overlaps no other argument. */
+ * are safe, whatever the scale).  A live row that holds a NaN or an infinity may
+ * make the outputs of its sequence NaN.  out overlaps no other argument. */
 pa_status pa_decode_latent(void *out, const void *q, const void *pool, int num_blocks,
                            const int32_t *block_tables, int max_blocks_per_seq,
                            const int32_t *seq_lens, int max_seq_len, int num_seqs, int num_heads,

@@ -1,8 +1,11 @@
-"""Latent attention and its rows at unusual values: scales far below the scores' sizes."""
+"""Latent attention and its rows at unusual values: scales far below the scores' sizes;
+infinities and NaN in rows."""
 import numpy as np
 import pytest
+import torch
 
-from _latent import Decode, Prefill, check
+from _latent import LEAST, TORCH, UNIT, Decode, Prefill, bits16, check, dev, table
+from oracle import int4, latent
 from paged_kv_cache_64_gb300 import api
 
 pytestmark = pytest.mark.gpu
@@ -28,3 +31,50 @@ def test_small_scales_of_large_scores(size, scale):
     api.prefill_latent(out, **case.gpu())
     api.check_error()
     case.check(out)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rank", [256, 512])
+def test_rows_with_infinities(dtype, interleaved, rank):
+    """An infinity or a NaN of a rotary part stays in its pair, one of the latent part in
+    that part: 0 beside an infinity, NaN beside a NaN."""
+    rng = np.random.default_rng(32)
+    tokens, heads, nan = 6, 3, float("nan")
+    q = bits16(rng, tokens, heads, 64, dtype=dtype)
+    x = bits16(rng, tokens, rank + 64, dtype=dtype)
+    weight, cs = bits16(rng, rank, dtype=dtype), table(50)
+    pos = np.array([1, 7, 20, 33, 48, 5])
+
+    def put(a, value):
+        a[...] = int4.narrow(np.float64(value), dtype)
+
+    put(x[1, rank + 3:rank + 4], np.inf)
+    put(x[2, rank + 10:rank + 11], nan)
+    put(x[3, 5:6], -np.inf)
+    put(x[4, rank - 1:rank], nan)
+    put(q[1, 0, 40:41], -np.inf)
+    put(q[2, 2, 63:64], nan)
+    pool = torch.zeros(2, 16, rank + 64, dtype=TORCH[dtype], device="cuda")
+    rows = torch.zeros(tokens, rank + 64, dtype=TORCH[dtype], device="cuda")
+    q_out = torch.zeros(tokens, heads, 64, dtype=TORCH[dtype], device="cuda")
+    slots = torch.as_tensor(np.array([3, 31, 0, 17, -1, 9])).cuda()
+    api.latent_norm_rope(q_out, dev(q, dtype), dev(x, dtype), dev(weight, dtype), 1e-5,
+                         torch.as_tensor(cs).cuda(), torch.as_tensor(pos).cuda(), slots, pool,
+                         rows_out=rows, interleaved=interleaved)
+    api.check_error()
+    with np.errstate(invalid="ignore"):
+        ref = latent.norm_rope(q, x, weight, 1e-5, cs, pos, interleaved, dtype)
+    assert not np.isfinite(ref[0][1, 0]).all() and np.isfinite(ref[0]).sum() >= ref[0].size - 4
+    assert np.isfinite(ref[2][[0, 5]]).all() and (~np.isfinite(ref[2][[1, 2], rank:])).any(1).all()
+    assert (ref[2][3, :rank] == 0).sum() == rank - 1 and np.isnan(ref[2][4, :rank]).all()
+    assert np.isfinite(ref[2][[1, 2], :rank]).all() and np.isfinite(ref[2][[3, 4], rank:]).all()
+    for got, y, size in ((q_out, ref[0], ref[1]), (rows, ref[2], ref[3])):
+        g = got.double().cpu().numpy()
+        live = np.isfinite(y)
+        assert np.array_equal(g[~live], y[~live], equal_nan=True)
+        # half a step of the result, and fp32 sums of few terms: below 2^-18
+        bound = UNIT[dtype] * abs(y) + LEAST[dtype] + 2.0 ** -18 * size
+        assert (abs(g[live] - y[live]) <= bound[live]).all()
+    kept = slots >= 0
+    assert torch.equal(pool.view(-1, rank + 64)[slots[kept]].view(torch.int16), rows[kept].view(torch.int16))

@@ -39,10 +39,9 @@
 // 31-2,048 tokens, 16 heads: 122 us, 0.88 PFLOP/s: half-masked tiles (15% of the work),
 // the ends of pieces of work (a tile's last softmax, its output and the next one's first
 // in turn), and the launch's end.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
-#include <map>
-#include <mutex>
 #include <type_traits>
 
 #include "pa_decode.cuh"
@@ -852,16 +851,13 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 }
 
 // Clusters of c CTAs that the current device holds at once (0 if the query fails),
-// kept by type, size and device.
+// kept by device, size and type.
 static int prefill_clusters(bool bf16, int c) {
-    static std::mutex mu;
-    static std::map<int, int> known;
+    static std::atomic<int> known[128][kPreMaxSplit + 1][2];  // one more than the number, or 0
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    std::lock_guard<std::mutex> lock(mu);
-    const int key = (dev * 16 + c) * 2 + bf16;
-    const auto it = known.find(key);
-    if (it != known.end()) return it->second;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 0;
+    std::atomic<int> &slot = known[dev][c][bf16];
+    if (const int n = slot.load()) return n - 1;
     const void *kern = bf16 ? reinterpret_cast<const void *>(prefill_latent_kernel<true, true>)
                             : reinterpret_cast<const void *>(prefill_latent_kernel<false, true>);
     if (!ensure_smem_attr(kern, kPreSmem)) return 0;
@@ -877,7 +873,7 @@ static int prefill_clusters(bool bf16, int c) {
     cfg.numAttrs = 1;
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
-    known[key] = n;
+    slot.store(n + 1);
     return n;
 }
 

@@ -486,7 +486,8 @@ pa_status pa_cache_read_latent(void *rows_out, const int64_t *slot_mapping, int 
  * dense, 16-byte aligned; block_tables, seq_lens, max_seq_len as in pa_decode;
  * num_heads in 1 .. 1024, num_seqs up to 65535, num_blocks * block_size and
  * max_blocks_per_seq * block_size below 2^31, the smaller of max_seq_len and
- * the latter at most 2^24 (else PA_ERR_INVALID).
+ * the latter at most 2^24, and num_seqs times a 64th of it below 2^31 (else
+ * PA_ERR_INVALID).
  * workspace: device memory of pa_decode_latent_workspace_size bytes, 256-byte
  * aligned, no initialisation needed; calls that may overlap on the GPU need
  * workspaces of their own.  The batch's positions are shared out evenly over
@@ -525,11 +526,12 @@ size_t pa_decode_latent_workspace_size(int num_seqs, int num_heads, int rank, in
  * queries reaches must be finite.
  * q_starts, k_starts int32 [num_seqs + 1].  A sequence whose starts decrease or
  * leave [0, total], or with n_q > max_q_len, is a bad index (its rows left as
- * they were).  num_heads in 1 .. 1024, num_seqs up to 65535, total_k at most
- * 2^24.  The weights are rounded to dtype before they meet the values; their
- * sum is not.  Scores and sums are formed in fp32, the sums before their division
- * (dot products and scores in fp32's range and |v| n_k below 2^119 are safe,
- * whatever the scale).  out overlaps no other argument. */
+ * they were).  max_q_len may be any bound; of 0, nothing is done.  num_heads in
+ * 1 .. 1024, num_seqs up to 65535, total_k at most 2^24.  The weights are rounded
+ * to dtype before they meet the values; their sum is not.  Scores and sums are
+ * formed in fp32, the sums before their division (dot products and scores in
+ * fp32's range and |v| n_k below 2^119 are safe, whatever the scale).  out
+ * overlaps no other argument. */
 pa_status pa_prefill_latent(void *out, const void *q, int64_t q_token_stride,
                             int64_t q_head_stride, const void *k, int64_t k_token_stride,
                             int64_t k_head_stride, const void *v, int64_t v_token_stride,

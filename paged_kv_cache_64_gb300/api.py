@@ -717,7 +717,7 @@ def decode_latent(out, q, pool, block_tables, seq_lens, max_seq_len, scale, work
         _explain(dev, q=(q, None), out=(out, None), pool=(pool, None),
                  block_tables=(block_tables, torch.int32), seq_lens=(seq_lens, torch.int32))
     fn = _lib.load().pa_decode_latent
-    max_len = int(max_seq_len)
+    max_len = min(int(max_seq_len), tables[1] * bs)  # a table has no more
     args = (out.data_ptr(), q.data_ptr(), pool.data_ptr(), nb, block_tables.data_ptr(), tables[1],
             seq_lens.data_ptr(), max_len, S, heads, rank, bs, float(scale))
 
@@ -781,7 +781,8 @@ def prefill_latent(out, q, k, v, k_pe, q_starts, k_starts, max_q_len, scale, cau
     rc = _run(dev, stream, _lib.load().pa_prefill_latent,
               (out.data_ptr(), q.data_ptr(), *_steps(q, "q"), k.data_ptr(), *_steps(k, "k"),
                v.data_ptr(), *_steps(v, "v"), k_pe.data_ptr(), pe_step, q_starts.data_ptr(),
-               k_starts.data_ptr(), q_starts.shape[0] - 1, qs[0], ks[0], int(max_q_len), qs[1],
+               k_starts.data_ptr(), q_starts.shape[0] - 1, qs[0], ks[0],
+               min(int(max_q_len), qs[0]), qs[1],  # no sequence has more
                float(scale), 1 if causal else 0, code))
     if rc:
         _check("pa_prefill_latent", rc, out=out, q=q, k=k, v=v, k_pe=k_pe)

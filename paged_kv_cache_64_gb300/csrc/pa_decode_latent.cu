@@ -918,14 +918,15 @@ extern "C" pa_status pa_decode_latent(void *out, const void *q, const void *pool
         return PA_ERR_INVALID;
     if ((rank != 256 && rank != 512) || (block_size != 16 && block_size != 32 && block_size != 64))
         return PA_ERR_UNSUPPORTED;
-    if ((int64_t)num_blocks * block_size >= 1ll << 31 ||
-        (int64_t)max_blocks_per_seq * block_size >= 1ll << 31 ||
-        ((int64_t)max_seq_len / kLatTile + 1) * num_seqs >= 1ll << 31)
+    // positions that a sequence is taken to have at most
+    const int64_t cover = (int64_t)max_blocks_per_seq * block_size;
+    const int64_t longest = max_seq_len < cover ? max_seq_len : cover;
+    if ((int64_t)num_blocks * block_size >= 1ll << 31 || cover >= 1ll << 31 ||
+        (longest / kLatTile + 1) * num_seqs >= 1ll << 31)
         return PA_ERR_INVALID;
     // a CTA may have a whole sequence, and its next queries wait for the end of it: well
     // within the limit of a wait (64 positions take about 1.7 us)
-    if (max_seq_len > kLatMaxLen && (int64_t)max_blocks_per_seq * block_size > kLatMaxLen)
-        return PA_ERR_INVALID;
+    if (longest > kLatMaxLen) return PA_ERR_INVALID;
     if (num_seqs == 0) return PA_OK;
     const void *ptrs[] = {out, q, pool};
     for (const void *ptr : ptrs)

@@ -901,6 +901,7 @@ extern "C" pa_status pa_prefill_latent(
     if (!out || !q || !q_starts || !k_starts || !aligned16(out) || !aligned16(q)) return PA_ERR_INVALID;
     if (total_k > 0 && (!k || !v || !k_pe)) return PA_ERR_INVALID;
     if (!aligned16(k) || !aligned16(v) || !aligned16(k_pe)) return PA_ERR_INVALID;
+    if (max_q_len > total_q) max_q_len = total_q;  // no sequence has more
     PrefillLatentParams p = {};
     p.err = error_word();
     if (!p.err) return PA_ERR_CUDA;

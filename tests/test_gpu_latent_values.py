@@ -78,3 +78,20 @@ def test_rows_with_infinities(dtype, interleaved, rank):
         assert (abs(g[live] - y[live]) <= bound[live]).all()
     kept = slots >= 0
     assert torch.equal(pool.view(-1, rank + 64)[slots[kept]].view(torch.int16), rows[kept].view(torch.int16))
+
+
+@pytest.mark.parametrize("bound", [5000, (1 << 31) - 1, (1 << 32) + 3, 1 << 40])
+def test_bounds_on_lengths_past_every_length(bound):
+    """max_seq_len and max_q_len are bounds: however large, also past 32 bits."""
+    rng = np.random.default_rng(33)
+    case = Decode(rng, "bf16", rng.integers(0, 200, 70), 5, 256, 16)
+    out = case.empty()
+    api.decode_latent(out, **{**case.gpu(), "max_seq_len": bound})
+    api.check_error()
+    ref, far = case.reference()
+    check(out, ref, far)
+    case = Prefill(rng, "bf16", [30, 300, 1], [30, 310, 5], 2, True)
+    out = case.empty()
+    api.prefill_latent(out, **{**case.gpu(), "max_q_len": bound})
+    api.check_error()
+    case.check(out)

@@ -62,9 +62,12 @@ constexpr int kPreOffBar = kPreOffRing + kPreSlots * kPreSlab;
 constexpr int kPreSmem = kPreOffBar + 1024 + 1024;  // + slack to align the base to 1 KiB
 constexpr int kPreColS = 0, kPreColO = 256;        // TMEM columns: S_A S_B O_A O_B
 // Up to so many (key, head) pairs the longest tiles of all heads go first, past them
-// those of each head in turn, so that a head's tiles read its keys from L2 together:
-// 16 heads of 16,600 tokens 122 us the first way, 132 the other; 32 heads of 6,000
-// tokens behind 24,000 1,049 and 911.
+// those of each head in turn, so that a head's tiles read its keys from L2 together.
+// By length against by head, in us: one sequence of 8,192, 16 heads (131,000 pairs) 254 and 336; 16 ragged prompts, 16
+// heads (266,000) 143 and 167; 8 pieces behind a context, 8 heads (394,000) 353 and 368;
+// 4, 16 heads (674,000) 702 and 725; 64 ragged prompts, 4 heads (789,000) 810 and 810; 8
+// pieces, 16 heads (892,000) 983 and 950, 32 heads (1,792,000) 2,072 and 1,938.  One long
+// sequence gains for longer: 32,768, 32 heads (1,049,000) 6,745 and 7,403.
 constexpr int kPreByLength = 400000;
 // 256 queries meet 2^24 keys in about 0.3 s; the next work's queries and the fetching
 // warp wait for the end of one such piece, which a wait's limit has to cover.

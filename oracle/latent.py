@@ -37,8 +37,8 @@ def norm_rope(q, latent, weight, eps, cos_sin, positions, interleaved, dtype):
 
 
 def _attend(q, keys, values, scale):
-    """softmax(scale q keys^T) values for q [H, n, w], keys [H, m, w], values [H, m, d], with the
-    weights' sum of |values| and the largest sum of a score's absolute terms."""
+    """Scores scale q keys^T for q [H, n, w], keys [H, m, w], the sums of their absolute terms,
+    and the values [H, m, d] as they are: what _weigh takes."""
     with np.errstate(invalid="ignore"):
         s = np.einsum("hnw,hmw->hnm", q, keys) * scale
         terms = np.einsum("hnw,hmw->hnm", abs(q), abs(keys)) * abs(scale)
@@ -46,6 +46,8 @@ def _attend(q, keys, values, scale):
 
 
 def _weigh(s, terms, values):
+    """softmax(s) values, with the weights' sum of |values| and the largest of the terms of a
+    row's live scores; zeros where a row has none."""
     if s.shape[-1] == 0:
         shape = (*s.shape[:-1], values.shape[-1])
         return np.zeros(shape), np.zeros(shape), np.zeros(s.shape[:-1])

@@ -42,8 +42,10 @@
 // tensor pipe.  Beside 64 heads' queries two tiles fit: a stage's way (copy about 950
 // clocks from L2, q.K 1,300, softmax 1,000, P.V 900) is longer than two tiles' products,
 // which leaves the tensor pipe 71% busy in steady state.  Measured: 128 sequences of
-// 513-8192 positions, 128 heads, 178-190 us (0.83 PFLOP/s); 16 of 16-32k, 64 heads, 87 us
-// (5.2 TB/s); one of 200,003, 32 heads, 51 us (6.1 TB/s from the first tile to the last).
+// 513-8192 positions, 128 heads, 178-191 us (0.83 PFLOP/s); 16 of 16-32k, 64 heads, 84-91
+// us (5.0-5.4 TB/s); one of 200,003, 32 heads, 52 us (6.1 TB/s from the first tile to the
+// last).  Past 64 heads the groups are whole ones of 64: 65 heads take what 128 do (64
+// sequences of 513-8192: 64 heads 71 us, 65 101, 96 103, 128 104).
 // Issued from code that the compiler does not know to be a warp's, every instruction
 // takes 64 clocks (the first of these 316 us then, 286 with that mended alone).
 #include <cmath>

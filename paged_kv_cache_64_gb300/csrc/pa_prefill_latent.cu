@@ -34,9 +34,9 @@
 //
 // What bounds it.  128 keys of one tile are 12 instructions of 64 clocks and 16 of 32,
 // 1,280 clocks of the tensor pipe; their softmax, 128 exponentials a thread, runs under
-// the other tile's.  2 x 2-4k queries behind 6-12k keys, 32 heads: 880-1,040 us, 1.2-1.45
-// PFLOP/s, 72-85% of a library product's sustained rate at the power limit; 16 prompts of
-// 31-2,048 tokens, 16 heads: 122 us, 0.88 PFLOP/s: half-masked tiles (15% of the work),
+// the other tile's.  2 x 2-4k queries behind 6-12k keys, 32 heads: 810-1,050 us, 1.2-1.55
+// PFLOP/s, 70-92% of a library product's sustained rate at the power limit; 16 prompts of
+// 31-2,048 tokens, 16 heads: 120-126 us, 0.87 PFLOP/s: half-masked tiles (15% of the work),
 // the ends of pieces of work (a tile's last softmax, its output and the next one's first
 // in turn), and the launch's end.
 #include <atomic>

@@ -95,3 +95,24 @@ def test_bounds_on_lengths_past_every_length(bound):
     api.prefill_latent(out, **{**case.gpu(), "max_q_len": bound})
     api.check_error()
     case.check(out)
+
+
+def test_prompt_keys_of_nan_behind_the_causal_limit():
+    """A key of NaN, or of infinities, reaches only the queries that meet it."""
+    rng = np.random.default_rng(34)
+    case = Prefill(rng, "bf16", [200, 140], [330, 140], 2, True)
+    keys = [int(case.k_starts[1]) - 1, int(case.k_starts[2]) - 20]
+    case.kv[keys[0], :, :128] = 0x7FC0
+    case.kv[keys[1], 0, :128] = 0x7F80
+    case.rows[keys[1], 256:] = 0xFF80
+    out = case.empty()
+    api.prefill_latent(out, **case.gpu())
+    api.check_error()
+    live = np.ones(len(case.q), bool)
+    live[:case.q_starts[0]] = live[case.q_starts[2]:] = False
+    live[case.q_starts[1] - 1] = False
+    live[case.q_starts[2] - 20:] = False
+    with np.errstate(invalid="ignore"):
+        ref, bound = case.reference()
+    check(out[torch.as_tensor(live).cuda()], ref[live], bound[live])
+    assert torch.isnan(out[int(case.q_starts[1]) - 1]).all()

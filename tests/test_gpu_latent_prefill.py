@@ -115,3 +115,33 @@ def test_bad_starts_far_behind():
     with pytest.raises(_lib.PagedAttentionError):
         api.check_error()
     case.check(out)
+
+
+@pytest.mark.parametrize("max_q_len", [300, 3000])
+def test_lengths_change_between_replays(max_q_len):
+    """A graph's launch is of the tokens and bounds it was captured with; which work its
+    blocks are follows the starts at each replay."""
+    rng = np.random.default_rng(23)
+    n = np.full(250, 12)
+    case = Prefill(rng, "bf16", n, n, 3, True, gap=0)
+    g, out = case.gpu(), case.empty()
+    g["max_q_len"] = max_q_len
+    api.prefill_latent(out, **g)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.prefill_latent(out, **g)
+    for kind in range(4):
+        n = rng.multinomial(3000, rng.dirichlet(np.full(250, 0.05 if kind % 2 else 5.0)))
+        n = np.minimum(n, max_q_len)
+        case.n_q = n
+        case.n_k = np.where(rng.random(250) < 0.3, 0, n) if kind > 1 else n
+        case.q_starts, case.k_starts = (np.concatenate([[0], np.cumsum(x)]).astype(np.int32)
+                                        for x in (case.n_q, case.n_k))
+        g["q_starts"].copy_(torch.as_tensor(case.q_starts))
+        g["k_starts"].copy_(torch.as_tensor(case.k_starts))
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        api.check_error()
+        case.check(out)

@@ -116,3 +116,20 @@ def test_prompt_keys_of_nan_behind_the_causal_limit():
         ref, bound = case.reference()
     check(out[torch.as_tensor(live).cuda()], ref[live], bound[live])
     assert torch.isnan(out[int(case.q_starts[1]) - 1]).all()
+
+
+def test_tables_with_entries_of_no_block_behind_the_lengths():
+    """Entries past a sequence's blocks may hold anything: they are not looked at."""
+    rng = np.random.default_rng(35)
+    case = Decode(rng, "f16", [1, 16, 17, 513, 0, 2000], 20, 512, 16)
+    wide = np.full((6, 500), -1, np.int32)
+    wide[:, 1::3] = 1 << 30
+    for i, n in enumerate(case.lens):
+        count = -(-n // 16)
+        wide[i, :count] = case.tables[i, :count]
+    case.tables = wide
+    out = case.empty()
+    api.decode_latent(out, **{**case.gpu(), "max_seq_len": 8000})
+    api.check_error()
+    ref, bound = case.reference()
+    check(out, ref, bound)

@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                             item = LISTED ? (int64_t)x * p.per : 0;
                             end = LISTED ? item + p.per : 1;
                             first |= LISTED && x == 0;
-                        } else if (first) {
+                        } else if (first && ok) {
                             item = (int64_t)gridDim.x * p.per;
                             end = 1ll << 62;
                         } else {
